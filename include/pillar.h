@@ -69,6 +69,8 @@ extern "C" {
 #define PILLAR_FLAG_COUNT 8         /* sparse_cnt outside [0, max_sparse] (clamped) */
 #define PILLAR_FLAG_TIMEOUT 16      /* a bounded device wait gave up; outputs are incomplete */
 #define PILLAR_FLAG_TOPK 32         /* a Top-K budget exceeded max_topk (clamped) */
+#define PILLAR_FLAG_BLOCK 64        /* pillar_block_map: too few free blocks, or a bad free-ring state */
+#define PILLAR_FLAG_VALUE 128       /* pillar_kv8_append: a NaN, infinity or bad scale */
 
 typedef struct pillar_shape {
     int32_t B;             /* requests in the batch (>= 0) */
@@ -538,6 +540,120 @@ PILLAR_API int pillar_offload_evict(pillar_offload_fifo_t *f, int32_t req, int32
  */
 PILLAR_API int pillar_offload_reload(pillar_offload_fifo_t *f, pillar_offload_chunk_t *out, int32_t max_out,
                                      int32_t *nout);
+
+/*
+ * Cache blocks.  The operators below keep a request's context in blocks of
+ * PILLAR_KV_BLOCK tokens: block_table[b, i] (int32, [B, max_blocks]) is the
+ * block that holds positions [16 i, 16 i + 16) of request b, and position t
+ * lives in slot block_table[b, t / 16] * 16 + t % 16 of a pool of
+ * num_slots / 16 blocks (num_slots a multiple of 16).  Such slots are ordinary
+ * page-size-1 slots: the slot table that pillar_block_map writes serves
+ * pillar_attn_unified and its new slots serve pillar_kv_append.
+ */
+#define PILLAR_KV_BLOCK 16
+
+/* pillar_block_map_workspace_bytes -- workspace of pillar_block_map for a
+ * batch of shape->B requests. */
+PILLAR_API int pillar_block_map_workspace_bytes(const pillar_shape_t *shape, size_t *bytes);
+
+/*
+ * pillar_block_map -- the block tables of a batch whose lengths change, and
+ * the maps the other calls take, made on the device (no copy to the host
+ * between a model step and the next one's tables).
+ *
+ * Request b goes from prev_len[b] to req_len[b] positions.  With
+ * n = ceil(req_len / 16) and m = ceil(prev_len / 16) it takes n - m blocks
+ * from the free ring when n > m, and gives its blocks n .. m-1 back when
+ * n < m (a rollback of rejected tokens; req_len 0: the request is finished).
+ * Blocks are taken in batch order from the ring's head and given back, in
+ * batch order, at its tail, so the result does not depend on timing.  When
+ * the ring runs short, the first request whose blocks do not fit and every
+ * later one that needs blocks keep prev_len (PILLAR_FLAG_BLOCK); the others
+ * are served.
+ *
+ *   req_len,
+ *   prev_len     [B] int32, in [0, max_len].  A bad req_len leaves the request
+ *                at prev_len, a bad prev_len counts as an empty request of
+ *                length 0 (PILLAR_FLAG_REQUEST).
+ *   block_table  [B, max_blocks] int32: entries [0, m) are read, entries
+ *                [m, n) written, all others left as they were.
+ *   free_ring    [num_slots / 16] int32: the free blocks, from index head on,
+ *                count of them, modulo the ring's size.
+ *   free_state   [2] int32: {head, count}, read and updated.
+ *   granted_len  [B] int32: the length each request has after the call.
+ *   kv_off       [B+1] int64: exclusive prefix sums of granted_len.
+ *   slot_table   int32: slot_table[kv_off[b] + t] is the slot of position t of
+ *                request b (the slot table of pillar_attn_unified with
+ *                req_len = granted_len).  Entries at or past kv_off[B] are left
+ *                as they were, and so are entries at or past slot_capacity
+ *                (PILLAR_FLAG_COUNT).
+ *   new_off      [B+1] int32: exclusive prefix sums of the new tokens,
+ *                max(granted_len - prev_len, 0).
+ *   new_slots    int32: new_slots[new_off[b] + i] is the slot of position
+ *                prev_len[b] + i (the slots of pillar_kv_append);
+ *                new_capacity entries, as slot_capacity.
+ *   workspace    pillar_block_map_workspace_bytes bytes, 256-byte aligned; its
+ *                error word is cleared by the call and read with
+ *                pillar_get_error.  A block outside [0, num_slots / 16) gives
+ *                slot -1 (PILLAR_FLAG_SLOT).
+ * Only shape->B, max_len and num_slots are used (the whole shape is checked).
+ * All arrays are device memory, 4-byte aligned (kv_off 8, slot_table 16) and
+ * must not overlap.  Asynchronous on `stream`; allocates nothing.  Returns
+ * PILLAR_OK, PILLAR_ERR_ARG, PILLAR_ERR_WORKSPACE or PILLAR_ERR_CUDA.
+ */
+PILLAR_API int pillar_block_map(const pillar_shape_t *shape, const int32_t *req_len, const int32_t *prev_len,
+                                int32_t *block_table, int32_t max_blocks, int32_t *free_ring, int32_t *free_state,
+                                int32_t *granted_len, int64_t *kv_off, int32_t *slot_table, int64_t slot_capacity,
+                                int32_t *new_off, int32_t *new_slots, int64_t new_capacity, void *workspace,
+                                size_t ws_bytes, void *stream);
+
+/*
+ * The 8-bit cache.  K and V are held as e4m3 codes (4 exponent bits of bias
+ * 7, 3 fraction bits, largest value 448) with one fp32 scale per block of 16
+ * tokens and KV head: value = code * scale.
+ *   k8_pool, v8_pool  [num_slots / 16, Hkv, 16, D] codes, one byte each: the 16
+ *                     rows of a (block, KV head) lie together
+ *   k_scale, v_scale  [num_slots / 16, Hkv] fp32
+ * Blocks and block tables are those of pillar_block_map.
+ */
+
+/*
+ * pillar_kv8_append -- rounds the new tokens' K and V rows into the cache
+ * (the 8-bit form of pillar_kv_append).  Request b's new tokens are its last
+ * ones: with n_b = new_off[b+1] - new_off[b], packed row new_off[b] + i is
+ * position req_len[b] - n_b + i.  For the new rows x of one (block, KV head),
+ * a = max |x| and e the smallest integer >= -126 with a <= 448 * 2^e:
+ *   scale' = 2^e when row 0 of the block is among them, else max(scale, 2^e)
+ *   codes  = x / scale' rounded to the nearest e4m3 (ties to even); the block's
+ *            earlier rows become code * scale / scale' rounded the same way
+ * Rows of the block behind the last new one are left as they were, and a
+ * block without new rows is not touched.  A call with the same new rows again
+ * leaves what the first one did.  A block that gets new rows must belong to one
+ * request only.
+ *
+ *   k_new, v_new  bf16, row i at i * k_stride (v_stride) elements: [Hkv, D] each,
+ *                 16-byte aligned rows (a stride is a multiple of 8, at least
+ *                 Hkv * D; 0 means Hkv * D)
+ *   n             rows of k_new and v_new; rows at or past new_off[B] are not read
+ *   req_len       [B] int32, the lengths that include the new tokens
+ *   new_off       [B+1] int32, ascending from 0 (as pillar_block_map writes it)
+ *   block_table   [B, max_blocks] int32
+ *   device_flags  device int32 or null, or-ed: PILLAR_FLAG_REQUEST for offsets or
+ *                 lengths that do not fit together, n, max_len or max_blocks (the
+ *                 rows concerned are skipped), PILLAR_FLAG_SLOT for a block
+ *                 outside the pool (skipped), PILLAR_FLAG_VALUE for a NaN (stored
+ *                 as 0), an infinity (stored as the largest value of its sign;
+ *                 the scale goes by the finite values), or a scale of earlier
+ *                 rows that is negative or not finite (taken as 0)
+ * Only shape->B, Hkv, D, max_len and num_slots are used.  Pools are 16-byte
+ * aligned, the other arrays 4.  Asynchronous on `stream`; allocates nothing.
+ * Returns PILLAR_OK, PILLAR_ERR_ARG or PILLAR_ERR_CUDA.
+ */
+PILLAR_API int pillar_kv8_append(const pillar_shape_t *shape, const uint16_t *k_new, int64_t k_stride,
+                                 const uint16_t *v_new, int64_t v_stride, int32_t n, const int32_t *req_len,
+                                 const int32_t *new_off, const int32_t *block_table, int32_t max_blocks,
+                                 uint8_t *k8_pool, uint8_t *v8_pool, float *k_scale, float *v_scale,
+                                 int32_t *device_flags, void *stream);
 
 #ifdef __cplusplus
 }

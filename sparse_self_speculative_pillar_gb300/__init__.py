@@ -31,6 +31,11 @@ Entry points (same names as the C ABI):
   pillar_offload_init(capacity, chunk), pillar_offload_reserve(f, n, new_request),
   pillar_offload_release(f, n), pillar_offload_evict(f, req, len),
   pillar_offload_reload(f, max_out)         (host-side FIFO of offloaded KV chunks)
+  pillar_block_map_workspace_bytes(shape)
+  pillar_block_map(shape, req_len, prev_len, block_table, free_ring, free_state, granted_len, kv_off, slot_table,
+                   new_off, new_slots, workspace, stream=None)   (block tables and slot maps from lengths)
+  pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_pool, v8_pool, k_scale, v_scale,
+                    device_flags=None, stream=None)              (new rows into the 8-bit cache)
 """
 from __future__ import annotations
 
@@ -49,9 +54,13 @@ __all__ = [
     "pillar_kv_append", "PillarBuckets", "pillar_buckets_init", "pillar_buckets_admit", "pillar_buckets_retire", "pillar_buckets_step",
     "pillar_kv_offload", "pillar_kv_reload", "PillarOffloadFifo", "pillar_offload_init", "pillar_offload_reserve",
     "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
+    "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
+    "FLAG_BLOCK", "FLAG_VALUE", "KV_BLOCK",
 ]
 
 FLAG_INDEX, FLAG_SLOT, FLAG_REQUEST, FLAG_COUNT, FLAG_TIMEOUT, FLAG_TOPK = 1, 2, 4, 8, 16, 32
+FLAG_BLOCK, FLAG_VALUE = 64, 128
+KV_BLOCK = 16  # PILLAR_KV_BLOCK: tokens of a cache block
 # values of PillarShape.schedule (PILLAR_SCHEDULE_* in the header)
 SCHEDULE_UNIFIED, SCHEDULE_DRAFT_ONLY, SCHEDULE_VERIFY_ONLY, SCHEDULE_UNIFORM_ROWS, SCHEDULE_NAIVE_JOINT = 0, 1, 2, 3, 4
 EXPORTED = ("pillar_attn_workspace_bytes", "pillar_attn_unified", "pillar_attn_unified_slotted",
@@ -60,7 +69,8 @@ EXPORTED = ("pillar_attn_workspace_bytes", "pillar_attn_unified", "pillar_attn_u
             "pillar_kv_append", "pillar_buckets_init", "pillar_buckets_admit", "pillar_buckets_retire",
             "pillar_buckets_step", "pillar_kv_offload", "pillar_kv_reload", "pillar_offload_init",
             "pillar_attn_plan", "pillar_attn_run",
-            "pillar_offload_reserve", "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload")
+            "pillar_offload_reserve", "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
+            "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append")
 MAX_BUCKETS = 64  # PILLAR_MAX_BUCKETS
 OFFLOAD_QUEUE = 1024  # PILLAR_OFFLOAD_QUEUE
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024 + 256
@@ -163,6 +173,10 @@ def load():
     lib.pillar_offload_release.argtypes = [FP, ctypes.c_int64]
     lib.pillar_offload_evict.argtypes = [FP, ctypes.c_int32, ctypes.c_int32, I32P]
     lib.pillar_offload_reload.argtypes = [FP, ctypes.POINTER(PillarOffloadChunk), ctypes.c_int32, I32P]
+    I32, I64, SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.pillar_block_map_workspace_bytes.argtypes = [SP, ctypes.POINTER(SZ)]
+    lib.pillar_block_map.argtypes = [SP, P, P, P, I32, P, P, P, P, P, I64, P, P, I64, P, SZ, P]
+    lib.pillar_kv8_append.argtypes = [SP, P, I64, P, I64, I32, P, P, P, I32, P, P, P, P, P, P]
     lib.pillar_status_string.restype = ctypes.c_char_p
     for n in EXPORTED:
         if n == "pillar_status_string":
@@ -346,6 +360,111 @@ def pillar_kv_reload(shape, host_k, host_v, slots, k_pool, v_pool, device_flags=
                                  _ptr(k_pool), _ptr(v_pool), _ptr(device_flags), _stream(stream))
     if st:
         raise PillarError("pillar_kv_reload", st)
+
+
+# --------------------------------------------------------------- cache blocks
+
+class _Types:
+    """Element types the calls below take, by name (torch is imported on the first call)."""
+
+    def __getattr__(self, name):
+        import torch
+        self.i32, self.i64, self.f32 = (torch.int32,), (torch.int64,), (torch.float32,)
+        self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 bits travel in 16-bit integers too
+        self.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+        return self.__dict__[name]
+
+
+_T = _Types()
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _layout(name, x, dtypes, shape, dev):
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name}: {x.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if len(x.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, x.shape)):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
+    if not x.is_cuda or x.device.index != dev:
+        raise ValueError(f"{name}: on {x.device}, expected the current CUDA device")
+
+
+def _arg(name, x, dtypes, shape, dev):
+    """Pointer of a CUDA tensor whose element type, shape (None: any extent), layout and device are as given: these calls
+    index their arrays by the sizes of other ones, so a tensor that does not fit is refused here."""
+    _layout(name, x, dtypes, shape, dev)
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return x.data_ptr()
+
+
+def _rows(name, x, heads, D, dev, rows=None):
+    """Pointer and token stride of [rows, heads, D] bf16 whose tokens may lie apart (a slice of a fused projection)."""
+    _layout(name, x, _T.bf16, (rows, heads, D), dev)
+    st = x.stride()
+    if x.numel() == 0:
+        return x.data_ptr(), 0
+    if st[2] != 1 or (heads > 1 and st[1] != D) or (x.shape[0] > 1 and st[0] < heads * D):
+        raise ValueError(f"{name}: strides {st}, expected each token's {heads} x {D} values to be contiguous")
+    return x.data_ptr(), st[0] if x.shape[0] > 1 else 0
+
+
+def _workspace(x, dev):
+    if not x.is_cuda or x.device.index != dev or not x.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the current CUDA device")
+    return x.data_ptr(), x.numel() * x.element_size()
+
+
+def pillar_block_map_workspace_bytes(shape: PillarShape) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().pillar_block_map_workspace_bytes(ctypes.byref(shape), ctypes.byref(out))
+    if st:
+        raise PillarError("pillar_block_map_workspace_bytes", st)
+    return int(out.value)
+
+
+def pillar_block_map(shape, req_len, prev_len, block_table, free_ring, free_state, granted_len, kv_off, slot_table,
+                     new_off, new_slots, workspace, stream=None):
+    """Blocks for a batch whose lengths go from prev_len to req_len: takes them from and gives them back to the free
+    ring, and writes the block table's new entries, the slot table and the new tokens' slots."""
+    dev, B = _current_device(), shape.B
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = load().pillar_block_map(
+        ctypes.byref(shape), _arg("req_len", req_len, _T.i32, (B,), dev), _arg("prev_len", prev_len, _T.i32, (B,), dev),
+        _arg("block_table", block_table, _T.i32, (B, None), dev), block_table.shape[1],
+        _arg("free_ring", free_ring, _T.i32, (shape.num_slots // KV_BLOCK,), dev),
+        _arg("free_state", free_state, _T.i32, (2,), dev), _arg("granted_len", granted_len, _T.i32, (B,), dev),
+        _arg("kv_off", kv_off, _T.i64, (B + 1,), dev), _arg("slot_table", slot_table, _T.i32, (None,), dev),
+        slot_table.numel(), _arg("new_off", new_off, _T.i32, (B + 1,), dev),
+        _arg("new_slots", new_slots, _T.i32, (None,), dev), new_slots.numel(), ws, ws_bytes, _stream(stream))
+    if st:
+        raise PillarError("pillar_block_map", st)
+
+
+def _pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev):
+    blocks = (shape.num_slots // KV_BLOCK, shape.Hkv)
+    return (_arg("k8_pool", k8_pool, _T.codes, blocks + (KV_BLOCK, shape.D), dev),
+            _arg("v8_pool", v8_pool, _T.codes, blocks + (KV_BLOCK, shape.D), dev),
+            _arg("k_scale", k_scale, _T.f32, blocks, dev), _arg("v_scale", v_scale, _T.f32, blocks, dev))
+
+
+def pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_pool, v8_pool, k_scale, v_scale,
+                      device_flags=None, stream=None):
+    """The new tokens' K/V rows ([n, Hkv, D] bf16, tokens may lie apart) as e4m3 codes under the scales of their blocks;
+    request b's rows new_off[b] .. new_off[b+1]-1 are its last positions."""
+    dev, B = _current_device(), shape.B
+    kp, ks = _rows("k_new", k_new, shape.Hkv, shape.D, dev)
+    vp, vs = _rows("v_new", v_new, shape.Hkv, shape.D, dev, k_new.shape[0])
+    st = load().pillar_kv8_append(
+        ctypes.byref(shape), kp, ks, vp, vs, k_new.shape[0], _arg("req_len", req_len, _T.i32, (B,), dev),
+        _arg("new_off", new_off, _T.i32, (B + 1,), dev), _arg("block_table", block_table, _T.i32, (B, None), dev),
+        block_table.shape[1], *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
+        None if device_flags is None else _arg("device_flags", device_flags, _T.i32, (1,), dev), _stream(stream))
+    if st:
+        raise PillarError("pillar_kv8_append", st)
 
 
 # --------------------------------------------------------------- offload FIFO (host side)

@@ -10,7 +10,9 @@
 
 #include "pillar_internal.h"
 #include "pillar_kv.h"
+#include "pillar_kv8.h"
 #include "pillar_lists.h"
+#include "pillar_map.h"
 
 namespace pillar {
 
@@ -394,6 +396,113 @@ int pillar_draft_lists(const pillar_shape_t *shape, int32_t V, const int32_t *ne
     a.max_topk = shape->max_topk;
     a.max_sparse = shape->max_sparse;
     return launch_draft_lists(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+// Blocks of the pool of a shape, or -1 when its slots do not make whole blocks.
+static int pool_blocks(const pillar_shape_t &s) {
+    return s.num_slots % PILLAR_KV_BLOCK == 0 ? (int)(s.num_slots / PILLAR_KV_BLOCK) : -1;
+}
+
+int pillar_block_map_workspace_bytes(const pillar_shape_t *shape, size_t *bytes) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    if (!bytes) return PILLAR_ERR_ARG;
+    *bytes = map_ws_bytes(shape->B);
+    return PILLAR_OK;
+}
+
+int pillar_block_map(const pillar_shape_t *shape, const int32_t *req_len, const int32_t *prev_len,
+                     int32_t *block_table, int32_t max_blocks, int32_t *free_ring, int32_t *free_state,
+                     int32_t *granted_len, int64_t *kv_off, int32_t *slot_table, int64_t slot_capacity,
+                     int32_t *new_off, int32_t *new_slots, int64_t new_capacity, void *workspace, size_t ws_bytes,
+                     void *stream) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    const int blocks = pool_blocks(*shape);
+    if (blocks < 1 || max_blocks < 1 || slot_capacity < 0 || new_capacity < 0) return PILLAR_ERR_ARG;
+    if (!kv_off || !new_off || !aligned(kv_off, 8) || !aligned(new_off, 4)) return PILLAR_ERR_ARG;
+    if (shape->B > 0 && (!req_len || !prev_len || !block_table || !free_ring || !free_state || !granted_len ||
+                         (!slot_table && slot_capacity > 0) || (!new_slots && new_capacity > 0)))
+        return PILLAR_ERR_ARG;
+    if (!aligned(req_len, 4) || !aligned(prev_len, 4) || !aligned(block_table, 4) || !aligned(free_ring, 4) ||
+        !aligned(free_state, 4) || !aligned(granted_len, 4) || !aligned(slot_table, 16) || !aligned(new_slots, 4))
+        return PILLAR_ERR_ARG;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < map_ws_bytes(shape->B)) return PILLAR_ERR_WORKSPACE;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (shape->B == 0) {  // an empty batch: its offsets are one zero each
+        if (cudaMemsetAsync(workspace, 0, sizeof(int), cs) != cudaSuccess ||
+            cudaMemsetAsync(kv_off, 0, sizeof(int64_t), cs) != cudaSuccess ||
+            cudaMemsetAsync(new_off, 0, sizeof(int32_t), cs) != cudaSuccess)
+            return PILLAR_ERR_CUDA;
+        return PILLAR_OK;
+    }
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    MapArgs a;
+    a.req_len = req_len;
+    a.prev_len = prev_len;
+    a.table = block_table;
+    a.ring = free_ring;
+    a.state = free_state;
+    a.granted = granted_len;
+    a.kv_off = reinterpret_cast<long long *>(kv_off);
+    a.slots = slot_table;
+    a.slot_capacity = slot_capacity;
+    a.new_off = new_off;
+    a.new_slots = new_slots;
+    a.new_capacity = new_capacity;
+    a.ws = static_cast<char *>(workspace);
+    a.B = shape->B;
+    a.max_blocks = max_blocks;
+    a.max_len = shape->max_len;
+    a.num_blocks = blocks;
+    return launch_block_map(a, nsm, cs) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+// A token stride of rows of `heads` heads of D bf16 values: 0 is the packed one; the rows stay 16-byte aligned.
+static bool row_stride(int64_t given, int heads, int D, long long *stride) {
+    *stride = given ? (long long)given : (long long)heads * D;
+    return *stride >= (long long)heads * D && *stride % 8 == 0 && *stride <= (1ll << 40);
+}
+
+int pillar_kv8_append(const pillar_shape_t *shape, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
+                      int64_t v_stride, int32_t n, const int32_t *req_len, const int32_t *new_off,
+                      const int32_t *block_table, int32_t max_blocks, uint8_t *k8_pool, uint8_t *v8_pool,
+                      float *k_scale, float *v_scale, int32_t *device_flags, void *stream) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    Kv8AppendArgs a;
+    a.num_blocks = pool_blocks(*shape);
+    if (n < 0 || a.num_blocks < 1 || max_blocks < 1) return PILLAR_ERR_ARG;
+    if (!row_stride(k_stride, shape->Hkv, shape->D, &a.k_stride) ||
+        !row_stride(v_stride, shape->Hkv, shape->D, &a.v_stride))
+        return PILLAR_ERR_ARG;
+    if (n == 0 || shape->B == 0) return PILLAR_OK;
+    if (!k_new || !v_new || !req_len || !new_off || !block_table || !k8_pool || !v8_pool || !k_scale || !v_scale)
+        return PILLAR_ERR_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k8_pool, 16) || !aligned(v8_pool, 16) ||
+        !aligned(req_len, 4) || !aligned(new_off, 4) || !aligned(block_table, 4) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(device_flags, 4))
+        return PILLAR_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.req_len = req_len;
+    a.new_off = new_off;
+    a.table = block_table;
+    a.k8 = k8_pool;
+    a.v8 = v8_pool;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.flags = device_flags;
+    a.n = n;
+    a.B = shape->B;
+    a.Hkv = shape->Hkv;
+    a.D = shape->D;
+    a.max_blocks = max_blocks;
+    a.max_len = shape->max_len;
+    return launch_kv8_append(a, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
 }
 
 int pillar_get_error(void *workspace, void *stream, int32_t *flags) {
