@@ -655,6 +655,40 @@ PILLAR_API int pillar_kv8_append(const pillar_shape_t *shape, const uint16_t *k_
                                  uint8_t *k8_pool, uint8_t *v8_pool, float *k_scale, float *v_scale,
                                  int32_t *device_flags, void *stream);
 
+/*
+ * pillar_attn_kv8 -- the unified draft/verify step over the 8-bit cache:
+ * pillar_attn_unified with k8_pool, v8_pool, k_scale, v_scale and block_table
+ * in the place of the bf16 pools and the slot table.  Position t of request b
+ * is row t % 16 of block block_table[b, t / 16].  With k = 0 and every request
+ * in verify mode it is plain decoding: one query row over its whole context.
+ *   verify_logits  as pillar_attn_unified writes them (so that
+ *                  pillar_topk_select follows unchanged), or NULL: no dump
+ *   workspace      pillar_attn_workspace_bytes
+ * Alignment: q, out and the pools 16 bytes, verify_logits 8, the other arrays
+ * 4.  The schedule is UNIFIED, DRAFT_ONLY or VERIFY_ONLY (PILLAR_ERR_ARG
+ * otherwise); wait_timeout_us has no meaning here (nothing waits on the
+ * device).  A block outside [0, num_slots / 16) or a position past
+ * max_blocks is skipped and flagged PILLAR_FLAG_SLOT.  A NaN code or scale of
+ * a key makes the rows of its request and KV head NaN that share a tile of 64
+ * keys with it, whether they see it or not; pillar_kv8_append writes none.
+ *
+ * pillar_attn_run_kv8 -- the same on the plan that pillar_attn_plan left in the
+ * workspace (as pillar_attn_run): one plan for the layers of a model step.
+ *
+ * Returns PILLAR_OK, PILLAR_ERR_ARG, PILLAR_ERR_WORKSPACE or PILLAR_ERR_CUDA.
+ */
+PILLAR_API int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool,
+                               const uint8_t *v8_pool, const float *k_scale, const float *v_scale,
+                               const int32_t *block_table, int32_t max_blocks, const int32_t *req_mode,
+                               const int32_t *req_len, const int32_t *sparse_idx, const int32_t *sparse_cnt,
+                               uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
+                               size_t ws_bytes, void *stream);
+PILLAR_API int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool,
+                                   const uint8_t *v8_pool, const float *k_scale, const float *v_scale,
+                                   const int32_t *block_table, int32_t max_blocks, const int32_t *sparse_idx,
+                                   uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
+                                   size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

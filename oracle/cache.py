@@ -133,3 +133,60 @@ def kv8_append(codes, scale, new, req_len, new_off, table):
                 codes[blk, h, r:r + hi - lo] = e4m3_encode(x / s)
                 scale[blk, h] = s
     return codes, scale
+
+
+# ---------------------------------------------------------------- attention
+
+def _attend(q, k, v, scale):
+    """One query row over the keys it sees: output, log-sum-exp, scaled scores (all fp64)."""
+    s = scale * (k @ q)
+    if len(s) == 0:
+        return np.zeros(v.shape[1]), -math.inf, s
+    m = s.max()
+    e = np.exp(s - m)
+    return e @ v / e.sum(), m + math.log(e.sum()), s
+
+
+def attn_kv8(q, k8, v8, k_scale, v_scale, table, req_mode, req_len, sparse_idx, sparse_cnt, k, scale):
+    """q [T, Hq, D] fp64; the cache as codes [num_blocks, Hkv, 16, D] and scales.  Listed positions outside [0, L) and
+    blocks outside the pool are left out.  Returns out [T, Hq, D], the packed logits and the LSEs [V, Hq, k+1]."""
+    T, Hq, D = q.shape
+    nblk, Hkv = k8.shape[:2]
+    G, row = Hq // Hkv, 0
+    out, logits, lse = np.zeros_like(q), [], []
+    for b in range(len(req_len)):
+        L, verify = int(req_len[b]), int(req_mode[b]) == 1
+        nq = k + 1 if verify else 1
+        dump, z = np.full((Hq, nq, L), -math.inf), np.full((Hq, nq), -math.inf)
+        for g in range(Hkv):
+            listed = range(L) if verify else [int(t) for t in sparse_idx[b, g, :int(sparse_cnt[b, g])]]
+            t = np.array([x for x in listed if 0 <= x < L and 0 <= int(table[b, x // BLOCK]) < nblk], np.int64)
+            blk = table[b, t // BLOCK].astype(np.int64) if len(t) else np.zeros(0, np.int64)
+            kk = e4m3_decode(k8[blk, g, t % BLOCK]) * k_scale[blk, g].astype(np.float64)[:, None]
+            vv = e4m3_decode(v8[blk, g, t % BLOCK]) * v_scale[blk, g].astype(np.float64)[:, None]
+            for j in range(nq):
+                n = int(np.searchsorted(t, L - nq + j, side="right")) if verify else len(t)
+                for h in range(g * G, (g + 1) * G):
+                    o, zz, s = _attend(q[row + j, h], kk[:n], vv[:n], scale)
+                    out[row + j, h] = o
+                    if verify:
+                        dump[h, j, t[:n]] = s
+                        z[h, j] = zz
+        if verify:
+            logits.append(dump.reshape(-1))
+            lse.append(z)
+        row += nq
+    return (out, np.concatenate(logits) if logits else np.zeros(0),
+            np.stack(lse) if lse else np.zeros((0, Hq, k + 1)))
+
+
+def prompt_attn(q, k, v, seq_off, scale):
+    """Causal attention of packed prompts, fp64 [T, heads, D]; rows outside the sequences are left at zero (LSE 0)."""
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    out, lse = np.zeros((T, Hq, D)), np.zeros((T, Hq))
+    for a, e in zip(seq_off[:-1], seq_off[1:]):
+        for h in range(Hq):
+            for i in range(int(a), int(e)):
+                out[i, h], lse[i, h], _ = _attend(q[i, h], k[int(a):i + 1, h // G], v[int(a):i + 1, h // G], scale)
+    return out, lse

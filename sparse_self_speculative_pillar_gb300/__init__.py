@@ -36,6 +36,10 @@ Entry points (same names as the C ABI):
                    new_off, new_slots, workspace, stream=None)   (block tables and slot maps from lengths)
   pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_pool, v8_pool, k_scale, v_scale,
                     device_flags=None, stream=None)              (new rows into the 8-bit cache)
+  pillar_attn_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, req_mode, req_len, sparse_idx, sparse_cnt,
+                  out, verify_logits, verify_lse, workspace, stream=None)   (the unified step over the 8-bit cache)
+  pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
+                      verify_lse, workspace, stream=None)        (the same on a plan of pillar_attn_plan)
 """
 from __future__ import annotations
 
@@ -55,6 +59,7 @@ __all__ = [
     "pillar_kv_offload", "pillar_kv_reload", "PillarOffloadFifo", "pillar_offload_init", "pillar_offload_reserve",
     "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
     "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
+    "pillar_attn_kv8", "pillar_attn_run_kv8",
     "FLAG_BLOCK", "FLAG_VALUE", "KV_BLOCK",
 ]
 
@@ -70,7 +75,8 @@ EXPORTED = ("pillar_attn_workspace_bytes", "pillar_attn_unified", "pillar_attn_u
             "pillar_buckets_step", "pillar_kv_offload", "pillar_kv_reload", "pillar_offload_init",
             "pillar_attn_plan", "pillar_attn_run",
             "pillar_offload_reserve", "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
-            "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append")
+            "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
+            "pillar_attn_kv8", "pillar_attn_run_kv8")
 MAX_BUCKETS = 64  # PILLAR_MAX_BUCKETS
 OFFLOAD_QUEUE = 1024  # PILLAR_OFFLOAD_QUEUE
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024 + 256
@@ -177,6 +183,8 @@ def load():
     lib.pillar_block_map_workspace_bytes.argtypes = [SP, ctypes.POINTER(SZ)]
     lib.pillar_block_map.argtypes = [SP, P, P, P, I32, P, P, P, P, P, I64, P, P, I64, P, SZ, P]
     lib.pillar_kv8_append.argtypes = [SP, P, I64, P, I64, I32, P, P, P, I32, P, P, P, P, P, P]
+    lib.pillar_attn_kv8.argtypes = [SP] + [P] * 6 + [I32] + [P] * 8 + [SZ, P]
+    lib.pillar_attn_run_kv8.argtypes = [SP] + [P] * 6 + [I32] + [P] * 5 + [SZ, P]
     lib.pillar_status_string.restype = ctypes.c_char_p
     for n in EXPORTED:
         if n == "pillar_status_string":
@@ -465,6 +473,45 @@ def pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_poo
         None if device_flags is None else _arg("device_flags", device_flags, _T.i32, (1,), dev), _stream(stream))
     if st:
         raise PillarError("pillar_kv8_append", st)
+
+
+def _kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev):
+    return (_arg("q", q, _T.bf16, (None, shape.Hq, shape.D), dev),
+            *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
+            _arg("block_table", block_table, _T.i32, (shape.B, None), dev), block_table.shape[1])
+
+
+def _kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev):
+    return (_arg("out", out, _T.bf16, tuple(q.shape), dev),
+            None if verify_logits is None else _arg("verify_logits", verify_logits, _T.f32, (None,), dev),
+            _arg("verify_lse", verify_lse, _T.f32, (None, shape.Hq, shape.k + 1), dev), *_workspace(workspace, dev))
+
+
+def pillar_attn_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, req_mode, req_len, sparse_idx, sparse_cnt,
+                    out, verify_logits, verify_lse, workspace, stream=None):
+    """The unified draft/verify step over the 8-bit cache; verify_logits None: no dump.  (The sizes of q, out, the logits
+    and the LSEs follow from modes and lengths that only the device knows, as in pillar_attn_unified.)"""
+    dev, B = _current_device(), shape.B
+    st = load().pillar_attn_kv8(
+        ctypes.byref(shape), *_kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev),
+        _arg("req_mode", req_mode, _T.i32, (B,), dev), _arg("req_len", req_len, _T.i32, (B,), dev),
+        _arg("sparse_idx", sparse_idx, _T.i32, (B, shape.Hkv, shape.max_sparse), dev),
+        _arg("sparse_cnt", sparse_cnt, _T.i32, (B, shape.Hkv), dev),
+        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _stream(stream))
+    if st:
+        raise PillarError("pillar_attn_kv8", st)
+
+
+def pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
+                        verify_lse, workspace, stream=None):
+    """pillar_attn_kv8 on the plan that pillar_attn_plan left in the workspace."""
+    dev = _current_device()
+    st = load().pillar_attn_run_kv8(
+        ctypes.byref(shape), *_kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev),
+        _arg("sparse_idx", sparse_idx, _T.i32, (shape.B, shape.Hkv, shape.max_sparse), dev),
+        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _stream(stream))
+    if st:
+        raise PillarError("pillar_attn_run_kv8", st)
 
 
 # --------------------------------------------------------------- offload FIFO (host side)

@@ -505,6 +505,72 @@ int pillar_kv8_append(const pillar_shape_t *shape, const uint16_t *k_new, int64_
     return launch_kv8_append(a, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
 }
 
+// The host checks of an attention run over the 8-bit cache.
+static int attn_kv8_checks(const pillar_shape_t *shape, const uint16_t *q, const Kv8Cache &c, const int32_t *sparse_idx,
+                           const uint16_t *out, const float *verify_logits, const float *verify_lse,
+                           const void *workspace, size_t ws_bytes) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    const pillar_shape_t &s = *shape;
+    if (s.schedule > PILLAR_SCHEDULE_VERIFY_ONLY) return PILLAR_ERR_ARG;
+    if (s.B == 0) return PILLAR_OK;
+    if (pool_blocks(s) < 1 || c.max_blocks < 1) return PILLAR_ERR_ARG;
+    if (!q || !c.k8 || !c.v8 || !c.k_scale || !c.v_scale || !c.table || !out || !verify_lse) return PILLAR_ERR_ARG;
+    if (s.max_sparse > 0 && !sparse_idx) return PILLAR_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(c.k8, 16) || !aligned(c.v8, 16) || !aligned(out, 16) || !aligned(c.k_scale, 4) ||
+        !aligned(c.v_scale, 4) || !aligned(c.table, 4) || !aligned(sparse_idx, 4) || !aligned(verify_logits, 8) ||
+        !aligned(verify_lse, 4))
+        return PILLAR_ERR_ARG;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < attn_layout(s).total) return PILLAR_ERR_WORKSPACE;
+    return PILLAR_OK;
+}
+
+int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool, const uint8_t *v8_pool,
+                        const float *k_scale, const float *v_scale, const int32_t *block_table, int32_t max_blocks,
+                        const int32_t *sparse_idx, uint16_t *out, float *verify_logits, float *verify_lse,
+                        void *workspace, size_t ws_bytes, void *stream) {
+    Kv8Cache c{k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, 0};
+    const int st = attn_kv8_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
+    if (st != PILLAR_OK) return st;
+    const pillar_shape_t &s = *shape;
+    if (s.B == 0) return PILLAR_OK;
+    c.num_blocks = pool_blocks(s);
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    AttnArgs aa = {};
+    aa.q = q;
+    aa.sparse_idx = sparse_idx;
+    aa.out = out;
+    aa.logits = verify_logits;
+    aa.lse = verify_lse;
+    aa.ws = static_cast<char *>(workspace);
+    aa.lay = attn_layout(s);
+    aa.num_slots = s.num_slots;
+    aa.Hq = s.Hq;
+    aa.Hkv = s.Hkv;
+    aa.D = s.D;
+    aa.k = s.k;
+    aa.max_sparse = s.max_sparse;
+    aa.schedule = s.schedule;
+    aa.scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / std::sqrt((float)s.D);
+    return launch_attn_kv8(aa, c, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool, const uint8_t *v8_pool,
+                    const float *k_scale, const float *v_scale, const int32_t *block_table, int32_t max_blocks,
+                    const int32_t *req_mode, const int32_t *req_len, const int32_t *sparse_idx,
+                    const int32_t *sparse_cnt, uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
+                    size_t ws_bytes, void *stream) {
+    // the run's checks first, so that a bad call enqueues nothing
+    const Kv8Cache c{k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, 0};
+    const int st = attn_kv8_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
+    if (st != PILLAR_OK) return st;
+    const int sp = pillar_attn_plan(shape, req_mode, req_len, sparse_cnt, workspace, ws_bytes, stream);
+    if (sp != PILLAR_OK) return sp;
+    return pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, sparse_idx, out,
+                               verify_logits, verify_lse, workspace, ws_bytes, stream);
+}
+
 int pillar_get_error(void *workspace, void *stream, int32_t *flags) {
     if (!workspace || !flags) return PILLAR_ERR_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);

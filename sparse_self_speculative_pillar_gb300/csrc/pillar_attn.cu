@@ -1264,12 +1264,8 @@ static cudaError_t pool_tensor_map(CUtensorMap *m, const void *pool, long long n
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_attn(const AttnArgs &a, int nsm, cudaStream_t st) {
-    AttnParams p;
-    cudaError_t e = pool_tensor_map(&p.tmap_k, a.k_pool, a.num_slots, a.Hkv, a.D);
-    if (e != cudaSuccess) return e;
-    e = pool_tensor_map(&p.tmap_v, a.v_pool, a.num_slots, a.Hkv, a.D);
-    if (e != cudaSuccess) return e;
+// The kernel parameters of a call, but for the tensor maps.
+static void fill_params(const AttnArgs &a, AttnParams &p) {
     p.q = a.q;
     p.k_pool = a.k_pool;
     p.v_pool = a.v_pool;
@@ -1303,7 +1299,33 @@ cudaError_t launch_attn(const AttnArgs &a, int nsm, cudaStream_t st) {
     p.max_sparse = a.max_sparse;
     p.scale = a.scale;
     p.wait_ns = a.wait_ns;
+}
+
+cudaError_t launch_attn(const AttnArgs &a, int nsm, cudaStream_t st) {
+    AttnParams p;
+    cudaError_t e = pool_tensor_map(&p.tmap_k, a.k_pool, a.num_slots, a.Hkv, a.D);
+    if (e != cudaSuccess) return e;
+    e = pool_tensor_map(&p.tmap_v, a.v_pool, a.num_slots, a.Hkv, a.D);
+    if (e != cudaSuccess) return e;
+    fill_params(a, p);
     return a.D == 128 ? launch_unified_t<128>(p, nsm, st) : launch_unified_t<64>(p, nsm, st);
+}
+
+// The merge of split units alone, after another kernel that left partial records of the same layout
+// (it reads no pool, so it needs no tensor map).
+cudaError_t launch_merge(const AttnArgs &a, int nsm, cudaStream_t st) {
+    AttnParams p = {};
+    fill_params(a, p);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nsm * kMergeCtasPerSm);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return a.D == 128 ? cudaLaunchKernelEx(&cfg, merge_kernel<128>, p) : cudaLaunchKernelEx(&cfg, merge_kernel<64>, p);
 }
 
 }  // namespace pillar

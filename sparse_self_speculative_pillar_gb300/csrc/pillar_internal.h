@@ -164,6 +164,16 @@ struct AttnArgs {
     unsigned long long wait_ns;  // bound of every pipeline wait
 };
 cudaError_t launch_attn(const AttnArgs &a, int grid, cudaStream_t st);
+cudaError_t launch_merge(const AttnArgs &a, int nsm, cudaStream_t st);
+
+// The 8-bit cache of an attention run (the rest of its arguments are AttnArgs).
+struct Kv8Cache {
+    const uint8_t *k8, *v8;
+    const float *k_scale, *v_scale;
+    const int *table;
+    int max_blocks, num_blocks;
+};
+cudaError_t launch_attn_kv8(const AttnArgs &a, const Kv8Cache &c, int nsm, cudaStream_t st);
 
 struct TopkArgs {
     const float *logits, *lse;

@@ -59,3 +59,39 @@ def test_block_map_grows_rolls_back_and_runs_short():
     short = C.block_map([16, 33, 20, 4], [16, 0, 16, 3], np.arange(16).reshape(4, 4) % 6, ring, [0, 2], 64, 6)
     assert short["bad"] == {"block"} and short["granted"].tolist() == [16, 0, 16, 4]  # 33 does not fit, nor what follows
     assert short["state"].tolist() == [0, 2]
+
+
+def test_attention_over_the_cache_agrees_with_the_bf16_oracle():
+    """Codes under powers of two are bf16 values, so the step's own oracle, written apart, has to agree."""
+    import oracle
+    rng = np.random.default_rng(8)
+    Hq, Hkv, D, k, lens, mode = 4, 2, 64, 2, [37, 20, 5], [1, 0, 1]
+    k8, v8 = (rng.integers(0, 120, (9, Hkv, 16, D)).astype(np.uint8) for _ in "kv")
+    ks, vs = (2.0 ** rng.integers(-9, -5, (9, Hkv)).astype(np.float64) for _ in "kv")
+    table = np.array([[3, 0, 7], [5, 1, 0], [8, 0, 0]])
+    idx, cnt = rng.integers(0, 20, (3, Hkv, 6)), np.array([[0, 0], [6, 0], [0, 0]])
+    from workloads import bf16_bits_to_f32, f32_to_bf16_bits
+    qb = f32_to_bf16_bits(rng.standard_normal((7, Hq, D)).astype(np.float32) * 0.3)
+    out, logits, lse = C.attn_kv8(bf16_bits_to_f32(qb).astype(np.float64), k8, v8, ks, vs, table, mode, lens, idx, cnt, k,
+                                  D ** -0.5)
+    bits = [f32_to_bf16_bits((C.e4m3_decode(c) * s[..., None, None]).transpose(0, 2, 1, 3).reshape(-1, Hkv, D)
+                             .astype(np.float32)) for c, s in ((k8, ks), (v8, vs))]
+    slots = np.concatenate([[table[b, t // 16] * 16 + t % 16 for t in range(n)] for b, n in enumerate(lens)])
+    r = oracle.attn_unified(Hq=Hq, Hkv=Hkv, D=D, k=k, scale=D ** -0.5, q=qb, k_pool=bits[0], v_pool=bits[1],
+                            slot_table=slots.astype(np.int32), req_mode=np.array(mode, np.int32),
+                            req_len=np.array(lens, np.int32), sparse_idx=idx.astype(np.int32),
+                            sparse_cnt=cnt.astype(np.int32))
+    np.testing.assert_allclose(out, r.out, rtol=1e-12, atol=1e-13)
+    np.testing.assert_allclose(logits, r.logits, rtol=1e-12, atol=1e-13)
+    np.testing.assert_allclose(lse, oracle.verify_lse_of(r, np.array(mode), k, Hq), rtol=1e-12)
+
+
+def test_prompt_attention_closed_forms():
+    rng = np.random.default_rng(9)
+    q, k, v = rng.standard_normal((6, 4, 8)), rng.standard_normal((6, 2, 8)), rng.standard_normal((6, 2, 8))
+    out, lse = C.prompt_attn(q, k, v, [0, 1, 1, 5], 0.3)
+    np.testing.assert_allclose(out[0], v[0].repeat(2, 0))                 # a row alone is its value
+    np.testing.assert_allclose(lse[1], 0.3 * (q[1] * k[1].repeat(2, 0)).sum(-1))
+    assert np.all(out[5] == 0)                                            # behind the last sequence
+    same, _ = C.prompt_attn(q, np.ones_like(k), v, [0, 6], 0.3)
+    np.testing.assert_allclose(same[3, 0], v[:4, 0].mean(0))              # equal keys: the mean of what is seen
