@@ -553,6 +553,7 @@ int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const ui
     aa.max_sparse = s.max_sparse;
     aa.schedule = s.schedule;
     aa.scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / std::sqrt((float)s.D);
+    aa.wait_ns = s.wait_timeout_us > 0 ? (unsigned long long)s.wait_timeout_us * 1000ull : kWaitTimeoutNs;
     return launch_attn_kv8(aa, c, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
 }
 

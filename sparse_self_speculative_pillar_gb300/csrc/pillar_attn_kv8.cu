@@ -8,49 +8,60 @@
 // units are those of the bf16 step; only the kernel between them differs.
 //
 // What bounds it: the bytes of the cache (2 D per key and head) and, for
-// verify rows, the fp32 logits.  The arithmetic is small next to them -- at
-// most 64 rows per key -- but an 8-bit code has to become a tensor-core
-// operand first, so the kernel is built around converting each byte in the
-// registers it is consumed from:
-//   * mma.m16n8k16 with f16 operands and fp32 accumulators.  Every e4m3 value
-//     is an f16 value; a bf16 query row divided by a power of two (its largest
-//     magnitude brought to [2^14, 2^15)) is one too, except for elements 2^-28
-//     below the row's largest, whose rounding (2^-39 of it) fp32 would not see
-//     either.  So q . k8 is a sum of exact products, as with bf16 keys.
-//     tcgen05 would want the converted tile written back to shared memory,
-//     twice the bytes that the loads bring in, to fill an M of 64 or 128 that
-//     at most 64 rows use.
+// verify rows, the fp32 logits; and next to them the work of turning 8-bit codes
+// into tensor-core operands, which decided the shape of the kernel:
+//   * Every e4m3 value is an f16 value, and a bf16 query row divided by a power of
+//     two (its largest magnitude brought to [2^14, 2^15)) is one too, but for
+//     elements 2^-28 below that, whose rounding (2^-39 of it) fp32 would not see.
+//     So q . k8 is a sum of exact products with f16 operands, as with bf16 keys.
+//     (mma with e4m3 operands would take the codes as they are, but this GPU
+//     converts them to f16 inside the instruction, for every use: measured 590 to
+//     700 pairs a cycle and SM with operands that change, 960 with f16 ones; a
+//     kernel on it took 448 us where this one takes the time stated below.
+//     tcgen05 has native e4m3, but 64 or 128 rows at a time, with scores and
+//     probabilities passing through tensor memory; a draft request has at most
+//     eight rows, and a tile's bytes arrive every 0.36 us.)
+//   * The keys are the m of m16n8k16, the query rows its n: S^T = K Q^T and
+//     O^T = V^T P^T.  A tile of eight rows wastes little, its O^T is 32 registers a
+//     lane, and above all an operand made of K or V serves every row tile of its
+//     warp.
 //   * The order of the reduction index is free as long as both operands use the
 //     same one.  Within a row, lane c of four takes bytes [16c, 16c + 16) (and
-//     the same 64 further on), so a lane's 16-byte loads hold whole operand
-//     registers of consecutive steps; within 16 keys, columns n of the two
-//     8-key tiles are keys 4 (n / 2) + n % 2 and two further on, so a lane owns
-//     four consecutive keys: one 16-byte load of their scales, one 16-byte store
-//     of their logits, and its probabilities are in place for the second
-//     product.  V's rows are read whole by eight lanes, and one byte permute
-//     pairs two keys' values of a dimension.
+//     the same 64 further on), so that a 16-byte load holds the lane's part of
+//     four steps; V's rows are read whole by eight lanes, a byte permute pairs two
+//     keys' values of a dimension, and one conversion makes an operand register.
+//     P is transposed between the products by movmatrix.
 //   * K and V rows land in shared memory by 16-byte asynchronous copies, their
 //     16-byte chunks XOR-ed with the row so that these loads meet no bank twice.
 //   * P is rounded to f16 with the scale of its key's values in it, relative to
-//     the largest value scale met so far (the accumulator is rescaled when that
-//     grows, as it is when the row maximum does): weights stay in [0, 2^15], and
-//     those down to 2^-29 of it keep all eleven bits.
-// A CTA of four warps works through items of the planner's queue, 64 keys a
-// tile.  Rows are padded to tiles of 16: with one such tile each warp takes 16
-// of the 64 keys, with two 32, with more all of them, and the warps of a tile
-// join at the item's end.
+//     the largest value scale its warp has met: weights are at most 2^15, and at
+//     least 2^7 for the row's largest probability at the largest scale.  A row's
+//     reference maximum moves only when a score passes it by more than 2^8, which
+//     a vote of the warp finds out: no reductions on most steps.
+// Two CTAs of eight warps per SM work through items of the planner's queue, 128
+// keys at a time out of a ring of 64-key stages that all threads fill.  The warps
+// share an item's row tiles, up to two each, and its keys, 16 at a time, and join
+// through shared memory at the item's end; meanwhile the other CTA's loads keep
+// coming.  (The time of a step is the latency of its chain of conversions, products
+// and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row tiles
+// hide it better than eight warps of three or four, which one CTA with a loader warp
+// of its own had; 448 against 470 us, and one loader warp was the limit next.)
 #include "pillar_device.cuh"
 
 namespace pillar {
 
 namespace {
 
-constexpr int kThreads8 = 128;
-constexpr int kStages8 = 4;
+constexpr int kThreads8 = 256;
+constexpr int kWarps8 = kThreads8 / 32;
+constexpr int kStages8 = 5;         // 64-key stages: two being read, three in flight
+constexpr int kStep = 128;          // keys between two barriers
+constexpr int kPairs = 4;           // steps whose rows are resolved ahead
+constexpr int kMaxTiles = kMaxRows / 8;  // row tiles of an item
+constexpr int kWarpTiles = 2;       // row tiles of a warp, at most
 constexpr int kBlk = PILLAR_KV_BLOCK;
-constexpr float kGrowLog2 = 8.f;    // O is rescaled once a row maximum grew by more than 2^8
-constexpr float kWeight = 128.f;    // weight of a probability of 1 at the largest value scale: 2^7 * 2^8 <= 2^15
-constexpr int kNever = 0x7fffffff;  // position of a key that no row sees
+constexpr float kGrowLog2 = 8.f;    // a row's reference maximum moves once a score passes it by more than 2^8
+constexpr float kWeight = 128.f;    // weight of a probability of 1 at the largest value scale: times 2^8 it is 2^15
 
 struct Kv8Params {
     const uint16_t *q;
@@ -68,30 +79,70 @@ struct Kv8Params {
     float scale;
 };
 
-template <int D>
-struct Stage8 {
-    alignas(16) uint8_t k[kTileKeys * D];
-    uint8_t v[kTileKeys * D];
-    float ks[kTileKeys], vs[kTileKeys];
-    int pos[kTileKeys];  // position (verify), 0 (draft), or kNever
+// A work item (in shared memory: the registers are needed elsewhere).
+struct Work {
+    int b, g, begin, n, L, q_off, vidx, nsplit, rec, verify;
+    long long logit_off;
 };
 
-// Byte offset of 16-byte chunk c of row r.
+// The records of the item after this one, copied while this one runs.
+struct alignas(16) Ahead {
+    Item item;
+    ReqInfo req;
+    UnitInfo unit;
+    long long logit_off;
+};
+
+template <int D>
+struct Stage8 {
+    alignas(128) uint8_t k[kTileKeys * D];
+    uint8_t v[kTileKeys * D];
+    float ks[kTileKeys], vs[kTileKeys];
+};
+
+template <int D>
+struct Smem8 {
+    Stage8<D> stage[kStages8];
+    uint2 q[kMaxTiles][D / 16][32];    // query operands: row tile, step, lane
+    float fac[kMaxRows];               // per row: logit = sum * fac * ks
+    int row[kPairs][kStep];            // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
+    unsigned mask[kPairs][kStep / 32]; // which of 32 keys there are
+    Ahead ahead;
+    Work w;
+    int item;                          // index of the item after this one
+};
+
+// How an item's row tiles and keys are shared out: groups of `share` warps, `tiles` row tiles each.
+struct Split {
+    int tiles, share;
+};
+__device__ __forceinline__ Split split_of(int rows) {
+    const int nrt = (rows + 7) / 8;
+    if (nrt <= 2) return {nrt, kWarps8};
+    return nrt <= 4 ? Split{2, kWarps8 / 2} : Split{2, kWarps8 / 4};
+}
+
+// Byte offset of 16-byte chunk c of row r.  K: the two rows that eight lanes read together differ in bit 0
+// of r; V: the four rows differ in bits 1 and 2.  (At D = 64 two rows make one 128-byte line.)  The XORs do
+// not depend on multiples of 8 of the row, so an offset is a lane's base plus a constant.
 template <int D>
 __device__ __forceinline__ int k_chunk(int r, int c) {
     return D == 128 ? r * 128 + (c ^ ((r & 1) << 2)) * 16 : r * 64 + c * 16;
 }
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
-    if (D == 128) return r * 128 + (c ^ (((r >> 2) & 3) << 1)) * 16;
-    return (r >> 1) * 128 + ((((r & 1) << 2) | c) ^ (((r >> 2) & 3) << 1)) * 16;
+    if (D == 128) return r * 128 + (c ^ (((r >> 1) & 3) << 1)) * 16;
+    return (r >> 1) * 128 + ((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) * 16;
 }
 
-__device__ __forceinline__ void cp16(void *dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp4(void *dst, const void *src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 4 : 0) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -110,243 +161,216 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
     return h;
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+// The transpose of an 8 x 8 tile of 16-bit values (lane t: row t / 4, columns 2 (t % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A work item as every thread of the CTA holds it.
-struct Work {
-    int b, g, begin, n, L, q_off, vidx, nsplit, rec;
-    long long logit_off;
-    bool verify;
-};
-
-// One of the two query rows of a thread.
-struct Row8 {
-    int lim;         // last position it sees (-1: no row of the item)
-    int j, gi;       // query token, head of the group
-    float fac;       // logit = accumulator * fac * ks
-    float m, l;      // reference maximum, this thread's part of the sum
-    long long lb;    // its logits (-1: none to write)
-};
-
+// Rows 2c and 2c + 1 of each row tile, as the eight lanes with this c hold them.
 template <int D>
 struct Acc {
-    float o[D / 8][4];
-    Row8 r[2];
-    uint32_t q[D / 16][4];
-    float wsc;       // weight of a probability = p * vs * wsc
-    float vmax;      // largest |vs| so far
+    float o[kWarpTiles][D / 16][4];  // O^T: dimension of lane g and the next one, rows 2c and 2c + 1
+    float m[kWarpTiles][2], l[kWarpTiles][2], fac[kWarpTiles][2];  // reference maximum, this lane's part of the sum
+    float wsc, vmax;                 // weight of a probability = p * vs * wsc; largest |vs| so far
 };
 
-// Query row `row` of the item as f16 operand registers: q[step][h], q[step][h + 2].
-template <int D, int H>
-__device__ __forceinline__ void load_row(const Kv8Params &p, const Work &w, int row, int rows, int c, Acc<D> &a) {
-    Row8 &r = a.r[H];
-    r.lim = -1;
-    r.j = r.gi = 0;
-    r.fac = 0.f;
-    r.m = neg_inf();
-    r.l = 0.f;
-    r.lb = -1;
-    uint4 x[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) x[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-        r.j = w.verify ? row / p.G : 0;
-        r.gi = row - r.j * p.G;
-        r.lim = w.verify ? w.L - (p.k + 1) + r.j : kNever - 1;
-        const uint16_t *src = p.q + ((size_t)(w.q_off + r.j) * p.Hq + (size_t)w.g * p.G + r.gi) * D + c * 16;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            x[2 * i] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * i));
-            x[2 * i + 1] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * i + 8));
-        }
-        if (w.verify && p.logits) r.lb = w.logit_off + ((long long)(w.g * p.G + r.gi) * (p.k + 1) + r.j) * w.L;
-    }
-    // the row's largest magnitude, over the four lanes that share it
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, x[i].x & 0x7fff7fffu), __vmaxu2(x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu)),
-                      x[i].w & 0x7fff7fffu);
-    mx = max(mx & 0xffffu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const int e = max((int)(mx >> 7), 15);               // biased exponent; 2^(141 - e) stays finite
-    const float up = __int_as_float((141 - e + 127) << 23);  // brings it to 2^14
-    const float down = __int_as_float((e - 141 + 127) << 23);
-    r.fac = down * p.scale;
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const uint32_t wd[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
-                                x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {  // elements 4s .. 4s+3 of the lane's 16
-            a.q[4 * i + s][H] = pack_f16x2(bf16lo(wd[2 * s]) * up, bf16hi(wd[2 * s]) * up);
-            a.q[4 * i + s][H + 2] = pack_f16x2(bf16lo(wd[2 * s + 1]) * up, bf16hi(wd[2 * s + 1]) * up);
-        }
-    }
+// What a warp knows about its item beyond the record.
+struct Part {
+    int rows, row0;  // rows of the item, first row of this warp's tiles
+    int share, kg;   // warps that share the keys, this one's number among them
+    int sure;        // every row sees up to here
+};
+
+// Last position that row r sees.
+__device__ __forceinline__ int row_limit(const Kv8Params &p, const Work &w, int r) {
+    return w.verify ? w.L - (p.k + 1) + r / p.G : 0x7fffffff;
 }
 
-// NG groups of 16 keys of a staged tile, starting with key k0 of the tile.
-template <int D, int NG>
-__device__ __forceinline__ void tile_keys(const Kv8Params &p, const Work &w, const Stage8<D> &st, int k0, int tile0, int nk,
-                                          Acc<D> &a) {
+// 16 NK keys of a stage, from its row r0 on, for the first NT row tiles of a warp.  vis: which of 32 keys from
+// r0 on there are; all: the rows see every one; pos0: position of the first (verify); left: keys of the item from
+// the first one on.
+template <int D, int NT, int NK>
+__device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const Part &pt, const Stage8<D> &st, int r0,
+                                      unsigned vis, bool all, int pos0, int left, const uint2 (*q)[D / 16][32], Acc<D> &a) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    float s[NG][2][4];
+    float s[NK][NT][4];  // keys 16 h + g and 16 h + 8 + g, rows 2c and 2c + 1
 #pragma unroll
-    for (int q = 0; q < NG; ++q)
+    for (int h = 0; h < NK; ++h)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int row = k0 + q * 16 + 4 * (g >> 1) + (g & 1) + 2 * t;
-            uint32_t kw[D / 16];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(st.k + k_chunk<D>(row, 4 * i + c));
-                kw[4 * i] = x.x, kw[4 * i + 1] = x.y, kw[4 * i + 2] = x.z, kw[4 * i + 3] = x.w;
-            }
+            for (int e = 0; e < 4; ++e) s[h][t][e] = 0.f;
+    const uint8_t *kb = st.k + r0 * D + k_chunk<D>(g, c);
+    const int flip = (g & 1) ? -64 : 64;  // the chunk four further on, under the XOR
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[q][t][e] = 0.f;
+    for (int i = 0; i < D / 64; ++i) {
+        uint4 x[NK][2];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) mma16816(s[q][t], a.q[i], f16x2_of(kw[i]), f16x2_of(kw[i] >> 16));
-        }
-    // scale, mask, dump; the rows' maxima
-    float mt[2] = {neg_inf(), neg_inf()};
+        for (int h = 0; h < NK; ++h)
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-        const int kb = k0 + q * 16 + 4 * c;  // this lane's four keys: kb .. kb+3
-        const float4 ks = *reinterpret_cast<const float4 *>(st.ks + kb);
-        const int4 ps = *reinterpret_cast<const int4 *>(st.pos + kb);
+            for (int e = 0; e < 2; ++e)
+                x[h][e] = *reinterpret_cast<const uint4 *>(kb + (i ? flip : 0) + (16 * h + 8 * e) * D);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const Row8 &r = a.r[h];
-            float v0 = s[q][0][2 * h] * r.fac * ks.x, v1 = s[q][0][2 * h + 1] * r.fac * ks.y;
-            float v2 = s[q][1][2 * h] * r.fac * ks.z, v3 = s[q][1][2 * h + 1] * r.fac * ks.w;
-            if (ps.x > r.lim) v0 = neg_inf();
-            if (ps.y > r.lim) v1 = neg_inf();
-            if (ps.z > r.lim) v2 = neg_inf();
-            if (ps.w > r.lim) v3 = neg_inf();
-            s[q][0][2 * h] = v0, s[q][0][2 * h + 1] = v1, s[q][1][2 * h] = v2, s[q][1][2 * h + 1] = v3;
-            mt[h] = fmaxf(mt[h], fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)));
-            if (r.lb >= 0) {
-                float *dst = p.logits + r.lb + w.begin + tile0 + kb;
-                const int odd = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
-                if (kb + 4 <= nk && (odd & 7) == 0) {
-                    if (odd == 0) {
-                        *reinterpret_cast<float4 *>(dst) = make_float4(v0, v1, v2, v3);
-                    } else {
-                        *reinterpret_cast<float2 *>(dst) = make_float2(v0, v1);
-                        *reinterpret_cast<float2 *>(dst + 2) = make_float2(v2, v3);
-                    }
-                } else {
-                    if (kb < nk) dst[0] = v0;
-                    if (kb + 1 < nk) dst[1] = v1;
-                    if (kb + 2 < nk) dst[2] = v2;
-                    if (kb + 3 < nk) dst[3] = v3;
-                }
+        for (int j = 0; j < 4; ++j) {
+            uint2 b[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) b[t] = q[t][4 * i + j][lane];
+#pragma unroll
+            for (int h = 0; h < NK; ++h) {
+                const uint32_t w0 = j == 0 ? x[h][0].x : j == 1 ? x[h][0].y : j == 2 ? x[h][0].z : x[h][0].w;
+                const uint32_t w1 = j == 0 ? x[h][1].x : j == 1 ? x[h][1].y : j == 2 ? x[h][1].z : x[h][1].w;
+                const uint32_t a0 = f16x2_of(w0), a1 = f16x2_of(w1), a2 = f16x2_of(w0 >> 16), a3 = f16x2_of(w1 >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(s[h][t], a0, a1, a2, a3, b[t].x, b[t].y);
             }
         }
     }
-    float f[2] = {1.f, 1.f};
+    // scale, mask, dump; does a score pass its row's reference?
     bool grow = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        Row8 &r = a.r[h];
-        mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
-        mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
-        const float mn = fmaxf(r.m, mt[h]);
-        if (r.m == neg_inf()) {
-            r.m = mn;
-        } else if ((mn - r.m) * kLog2e > kGrowLog2) {
-            f[h] = ex2_approx((r.m - mn) * kLog2e);
-            r.l *= f[h];
-            r.m = mn;
-            grow = true;
+    for (int h = 0; h < NK; ++h) {
+        const float k0 = st.ks[r0 + 16 * h + g], k1 = st.ks[r0 + 16 * h + 8 + g];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h][t][e] *= a.fac[t][e & 1] * (e < 2 ? k0 : k1);
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = 16 * h + (e < 2 ? 0 : 8) + g;
+                    if (!((vis >> key) & 1) || pos0 + key > row_limit(p, w, pt.row0 + 8 * t + 2 * c + (e & 1)))
+                        s[h][t][e] = neg_inf();
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                grow |= (fmaxf(s[h][t][e], s[h][t][e + 2]) - a.m[t][e]) * kLog2e > kGrowLog2;
         }
     }
-    // the value scales of the tile
-    {
-        const float2 vs = *reinterpret_cast<const float2 *>(st.vs + 2 * lane);
-        const float tm = __uint_as_float(__reduce_max_sync(
-            0xffffffffu, max(__float_as_uint(vs.x) & 0x7fffffffu, __float_as_uint(vs.y) & 0x7fffffffu)));
-        if (tm > a.vmax) {  // (the same in every warp of the CTA)
-            const float wn = fminf(kWeight / tm, 0x1p126f);
-            if (a.vmax > 0.f) {
-                const float ratio = wn / a.wsc;
-                f[0] *= ratio;
-                f[1] *= ratio;
-                grow = true;
+    if (w.verify && p.logits) {
+        const long long base = w.logit_off + pos0 + g;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = pt.row0 + 8 * t + 2 * c + e;
+                if (r < pt.rows) {
+                    const int j = r / p.G;
+                    float *dst = p.logits + base + (long long)((w.g * p.G + r - j * p.G) * (p.k + 1) + j) * w.L;
+#pragma unroll
+                    for (int h = 0; h < NK; ++h) {  // eight lanes write 32 bytes of a row
+                        if (16 * h + g < left) dst[16 * h] = s[h][t][e];
+                        if (16 * h + 8 + g < left) dst[16 * h + 8] = s[h][t][e + 2];
+                    }
+                }
             }
+    }
+    // the value scales of the keys
+    float vw[NK][2];
+    float tm = 0.f;
+#pragma unroll
+    for (int h = 0; h < NK; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            vw[h][e] = st.vs[r0 + 16 * h + 8 * e + g];
+            tm = fmaxf(tm, fabsf(vw[h][e]));
+        }
+    grow |= tm > a.vmax;
+    if (__any_sync(0xffffffffu, grow)) {  // rare: new reference maxima, a larger value scale
+        tm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tm)));
+        float vf = 1.f;
+        if (tm > a.vmax) {
+            const float wn = fminf(kWeight / tm, 0x1p126f);
+            if (a.vmax > 0.f) vf = wn / a.wsc;
             a.vmax = tm;
             a.wsc = wn;
         }
-    }
-    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            a.o[i][0] *= f[0], a.o[i][1] *= f[0];
-            a.o[i][2] *= f[1], a.o[i][3] *= f[1];
+        for (int t = 0; t < NT; ++t) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = a.m[t][e];
+#pragma unroll
+                for (int h = 0; h < NK; ++h) mx = fmaxf(mx, fmaxf(s[h][t][e], s[h][t][e + 2]));
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float was = a.m[t][e], fl = was == neg_inf() ? 1.f : ex2_approx((was - mx) * kLog2e);
+                a.l[t][e] *= fl;
+                f[e] = fl * vf;
+                a.m[t][e] = mx;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                a.o[t][i][0] *= f[0], a.o[t][i][1] *= f[1];
+                a.o[t][i][2] *= f[0], a.o[t][i][3] *= f[1];
+            }
         }
     }
+    uint32_t pb[NK][NT][2];  // P^T operands
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-        const int kb = k0 + q * 16 + 4 * c;
-        float4 ws = *reinterpret_cast<const float4 *>(st.vs + kb);
-        ws.x *= a.wsc, ws.y *= a.wsc, ws.z *= a.wsc, ws.w *= a.wsc;
-        uint32_t pa[4];
+    for (int h = 0; h < NK; ++h) {
+        const float w0 = vw[h][0] * a.wsc, w1 = vw[h][1] * a.wsc;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Row8 &r = a.r[h];
-            const float nb = -(r.m == neg_inf() ? 0.f : r.m) * kLog2e;
-            const float p0 = ex2_approx(fmaf(s[q][0][2 * h], kLog2e, nb)), p1 = ex2_approx(fmaf(s[q][0][2 * h + 1], kLog2e, nb));
-            const float p2 = ex2_approx(fmaf(s[q][1][2 * h], kLog2e, nb)), p3 = ex2_approx(fmaf(s[q][1][2 * h + 1], kLog2e, nb));
-            r.l += (p0 + p1) + (p2 + p3);
-            pa[h] = pack_f16x2(p0 * ws.x, p1 * ws.y);
-            pa[h + 2] = pack_f16x2(p2 * ws.z, p3 * ws.w);
+        for (int t = 0; t < NT; ++t) {
+            float e4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float ref = a.m[t][e & 1];
+                e4[e] = ex2_approx(fmaf(s[h][t][e], kLog2e, -(ref == neg_inf() ? 0.f : ref) * kLog2e));
+            }
+            a.l[t][0] += e4[0] + e4[2];
+            a.l[t][1] += e4[1] + e4[3];
+            pb[h][t][0] = transpose8x8(pack_f16x2(e4[0] * w0, e4[1] * w0));
+            pb[h][t][1] = transpose8x8(pack_f16x2(e4[2] * w1, e4[3] * w1));
         }
-        // V: this lane's dimensions of its four keys (a whole 16-byte chunk at D = 128, half of one at D = 64)
-        constexpr int W = D / 32;  // words per key
-        uint32_t vw[4][W];
+    }
+    // V: this lane's dimensions (16 at D = 128, 8 at D = 64) of keys 2c, 2c + 1, 2c + 8, 2c + 9
+    constexpr int W = D / 32;  // words per key
+    const uint8_t *vb = st.v + r0 * D + (D == 128 ? v_chunk<D>(2 * c, g) : v_chunk<D>(2 * c, g >> 1) + (g & 1) * 8);
+    const int next = D == 128 ? 128 : ((c & 2) ? -64 : 64);  // (D = 64: the other half of the line, under the XOR)
+#pragma unroll
+    for (int h = 0; h < NK; ++h) {
+        uint32_t x[4][W];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            const uint8_t *src = vb + (16 * h + 8 * (u >> 1)) * D + ((u & 1) ? next : 0);
             if (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(st.v + v_chunk<D>(kb + u, g));
-                vw[u][0] = x.x, vw[u][1] = x.y, vw[u][W - 2] = x.z, vw[u][W - 1] = x.w;
+                const uint4 y = *reinterpret_cast<const uint4 *>(src);
+                x[u][0] = y.x, x[u][1] = y.y, x[u][W - 2] = y.z, x[u][W - 1] = y.w;
             } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(st.v + v_chunk<D>(kb + u, g >> 1) + (g & 1) * 8);
-                vw[u][0] = x.x, vw[u][1] = x.y;
+                const uint2 y = *reinterpret_cast<const uint2 *>(src);
+                x[u][0] = y.x, x[u][1] = y.y;
             }
         }
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {  // two dimensions at a time: bytes (2 hf, 2 hf + 1) of the word
-                const uint32_t ab = __byte_perm(vw[0][i], vw[1][i], hf ? 0x7362 : 0x5140);
-                const uint32_t cd = __byte_perm(vw[2][i], vw[3][i], hf ? 0x7362 : 0x5140);
-                mma16816(a.o[4 * i + 2 * hf], pa, f16x2_of(ab), f16x2_of(cd));
-                mma16816(a.o[4 * i + 2 * hf + 1], pa, f16x2_of(ab >> 16), f16x2_of(cd >> 16));
+            for (int hf = 0; hf < 2; ++hf) {  // dimensions 4 i + 2 hf and the next
+                const uint32_t ab = __byte_perm(x[0][i], x[1][i], hf ? 0x7362 : 0x5140);
+                const uint32_t cd = __byte_perm(x[2][i], x[3][i], hf ? 0x7362 : 0x5140);
+                const uint32_t a0 = f16x2_of(ab), a1 = f16x2_of(ab >> 16), a2 = f16x2_of(cd), a3 = f16x2_of(cd >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(a.o[t][2 * i + hf], a0, a1, a2, a3, pb[h][t][0], pb[h][t][1]);
             }
     }
 }
 
-// Where the rows of an item go: row r, dimensions [d, d + N) of the normalised output.
-template <int D>
-__device__ __forceinline__ void store_row(const Kv8Params &p, const Work &w, int row, int j, int gi, int d, const float *v,
-                                          int n) {
-    if (w.nsplit == 1) {
-        uint16_t *dst = p.out + ((size_t)(w.q_off + j) * p.Hq + (size_t)w.g * p.G + gi) * D + d;
-        for (int i = 0; i < n; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) =
-                make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]), pack_bf16x2(v[i + 4], v[i + 5]),
-                           pack_bf16x2(v[i + 6], v[i + 7]));
-    } else {
-        float *dst = p.part_o + ((size_t)w.rec + row) * D + d;
-        for (int i = 0; i < n; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    }
+// Dimensions [d, d + 4) of the normalised output of row `row` (query token j, head gi of the group).
+__device__ __forceinline__ void store4(const Kv8Params &p, const Work &w, int D, int row, int j, int gi, int d, float4 v) {
+    if (w.nsplit == 1)
+        *reinterpret_cast<uint2 *>(p.out + ((size_t)(w.q_off + j) * p.Hq + (size_t)w.g * p.G + gi) * D + d) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    else
+        *reinterpret_cast<float4 *>(p.part_o + ((size_t)w.rec + row) * D + d) = v;
 }
 
 __device__ __forceinline__ void store_lse(const Kv8Params &p, const Work &w, int row, int j, int gi, float m, float l) {
@@ -355,197 +379,292 @@ __device__ __forceinline__ void store_lse(const Kv8Params &p, const Work &w, int
     else if (w.verify) p.lse[((size_t)w.vidx * p.Hq + (size_t)w.g * p.G + gi) * (p.k + 1) + j] = z;
 }
 
+// The f16 query operands of row tile t, by one warp: step j, lane (g, c): four elements of row 8 t + g, taken as the K
+// loads take bytes (64 (j / 4) + 16 c + 4 (j % 4) on).
 template <int D>
-__global__ void __launch_bounds__(kThreads8, 3) attn_kv8_kernel(const __grid_constant__ Kv8Params p) {
-    extern __shared__ __align__(16) char smem[];
-    Stage8<D> *stage = reinterpret_cast<Stage8<D> *>(smem);
-    __shared__ int s_item;
+__device__ __forceinline__ void stage_queries(const Kv8Params &p, const Work &w, Smem8<D> &sm, int t, int rows) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, row = t * 8 + g;
+    uint4 x[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) x[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+        const int j = w.verify ? row / p.G : 0;
+        const uint16_t *src = p.q + ((size_t)(w.q_off + j) * p.Hq + (size_t)w.g * p.G + row - j * p.G) * D + c * 16;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            x[2 * i] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * i));
+            x[2 * i + 1] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * i + 8));
+        }
+    }
+    uint32_t mx = 0;  // the row's largest magnitude, over the four lanes that share it
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, x[i].x & 0x7fff7fffu), __vmaxu2(x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu)),
+                      x[i].w & 0x7fff7fffu);
+    mx = max(mx & 0xffffu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int e = max((int)(mx >> 7), 15);                // biased exponent, such that 2^(141 - e) is finite
+    const float up = __int_as_float((268 - e) << 23);     // 2^(141 - e): the largest comes to [2^14, 2^15)
+    const float down = __int_as_float((e - 14) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const uint32_t wd[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
+                                x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sm.q[t][4 * i + j][lane] = make_uint2(pack_f16x2(bf16lo(wd[2 * j]) * up, bf16hi(wd[2 * j]) * up),
+                                                  pack_f16x2(bf16lo(wd[2 * j + 1]) * up, bf16hi(wd[2 * j + 1]) * up));
+    }
+    if (c == 0) sm.fac[row] = down * p.scale;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_constant__ Kv8Params p) {
+    extern __shared__ __align__(128) char smem[];
+    Smem8<D> &sm = *reinterpret_cast<Smem8<D> *>(smem);
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int num_items = *reinterpret_cast<volatile int *>(&p.hdr->num_items);
     int bad = 0;
-    if (tid == 0) s_item = atomicAdd(&p.hdr->item_counter, 1);
-    __syncthreads();
-    int it = s_item;
-    while (it < num_items) {
-        __syncthreads();  // everyone has read s_item, and the last item's shared memory
-        if (tid == 0) s_item = atomicAdd(&p.hdr->item_counter, 1);  // the item after this one
-        Work w;
-        {
-            const Item itm = p.items[it];
-            w.b = itm.unit / p.Hkv;
-            w.g = itm.unit - w.b * p.Hkv;
-            const ReqInfo ri = p.req[w.b];
-            const UnitInfo ui = p.unit[itm.unit];
-            w.begin = itm.begin;
-            w.n = itm.end - itm.begin;
-            w.L = ri.len;
-            w.q_off = ri.q_off;
-            w.vidx = ri.vidx;
-            w.nsplit = ui.nsplit;
-            w.rec = ui.rec_base + itm.split * ui.rec_rows;
-            w.verify = ri.mode == 1;
-            w.logit_off = w.verify ? p.logit_off[w.b] : 0;
+    // (thread 0 alone copies the records ahead and reads them)
+    auto copy_item = [&](int it) { cp16(smem_u32(&sm.ahead.item), p.items + it, 16); };
+    auto copy_unit = [&]() {
+        const int unit = sm.ahead.item.unit, b = unit / p.Hkv;
+        cp16(smem_u32(&sm.ahead.req), p.req + b, 16);
+        cp16(smem_u32(&sm.ahead.unit), p.unit + unit, 16);
+        cp8(smem_u32(&sm.ahead.logit_off), p.logit_off + b);
+    };
+    int done = 0;  // how far thread 0 is with the next item: 0 nothing, 1 its item record, 2 all of them
+    if (tid == 0) {
+        const int it = atomicAdd(&p.hdr->item_counter, 1);
+        sm.item = it;
+        if (it < num_items) {
+            copy_item(it);
+            cp_wait<0>();  // (thread 0 has committed nothing: the next line does)
+            cp_commit();
+            cp_wait<0>();
+            copy_unit();
+            cp_commit();
+            cp_wait<0>();
+            done = 2;
         }
-        const int ntiles = (w.n + kTileKeys - 1) / kTileKeys;
-        // --- the loads: thread tid fetches half of row tid / 2 of every tile.  The chain of a key -- its
-        // position, its block, its rows -- is spread over the tiles ahead.
-        const int lr = tid >> 1, lh = tid & 1;
-        const int *list = p.sparse_idx + ((size_t)w.b * p.Hkv + w.g) * p.max_sparse + w.begin;
-        const int *tab = p.c.table + (size_t)w.b * p.c.max_blocks;
-        auto position = [&](int t) {  // -1: no such key
-            const int i = t * kTileKeys + lr;
+    }
+    __syncthreads();
+    while (sm.item < num_items) {
+        __syncthreads();  // everyone has read the item's index
+        if (tid == 0) {
+            const Ahead &n = sm.ahead;
+            Work w;
+            w.b = n.item.unit / p.Hkv;
+            w.g = n.item.unit - w.b * p.Hkv;
+            w.begin = n.item.begin;
+            w.n = n.item.end - n.item.begin;
+            w.L = n.req.len;
+            w.q_off = n.req.q_off;
+            w.vidx = n.req.vidx;
+            w.nsplit = n.unit.nsplit;
+            w.rec = n.unit.rec_base + n.item.split * n.unit.rec_rows;
+            w.verify = n.req.mode == 1;
+            w.logit_off = w.verify ? n.logit_off : 0;
+            sm.w = w;
+            sm.item = atomicAdd(&p.hdr->item_counter, 1);  // the item after this one
+            done = 0;
+        }
+        __syncthreads();
+        const Work &w = sm.w;
+        const int steps = (w.n + kStep - 1) / kStep;
+        // --- the loads.  Thread tid < 128 finds key tid of each step: its position, its block, its row of the
+        // pools, one link of that chain a step, so that each has a step's time to arrive.  The rows go
+        // through shared memory to the copies, in which the 16-byte pieces of a row belong to adjacent lanes.
+        auto position = [&](int t) {  // of key tid of step t; -1: no such key
+            const int i = t * kStep + tid;
             if (i >= w.n) return -1;
             if (w.verify) return w.begin + i;
-            const int pos = __ldg(list + i);
+            const int pos = __ldg(p.sparse_idx + ((size_t)w.b * p.Hkv + w.g) * p.max_sparse + w.begin + i);
             if (pos < 0 || pos >= w.L) {
                 bad |= PILLAR_FLAG_INDEX;
                 return -1;
             }
             return pos;
         };
-        auto block = [&](int pos) { return pos >= 0 && pos / kBlk < p.c.max_blocks ? __ldg(tab + pos / kBlk) : -1; };
-        auto fetch = [&](int t, int pos, int blk) {
-            Stage8<D> &st = stage[t % kStages8];
-            const bool ok = blk >= 0 && blk < p.c.num_blocks;
+        auto block = [&](int pos) {
+            return pos >= 0 && pos / kBlk < p.c.max_blocks ? __ldg(p.c.table + (size_t)w.b * p.c.max_blocks + pos / kBlk) : -1;
+        };
+        auto resolve = [&](int t, int pos, int blk) {  // (the first four warps, whole)
+            const bool ok = pos >= 0 && blk >= 0 && blk < p.c.num_blocks;
             if (pos >= 0 && !ok) bad |= PILLAR_FLAG_SLOT;
-            const size_t unit = ok ? (size_t)blk * p.Hkv + w.g : 0;
-            const size_t row = (unit * kBlk + (ok ? pos % kBlk : 0)) * D;
+            sm.row[t % kPairs][tid] = ok ? (blk * p.Hkv + w.g) * kBlk + pos % kBlk : -1;
+            const unsigned m = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) sm.mask[t % kPairs][warp] = m;
+        };
+        auto fetch = [&](int s) {  // 64-key stage s of the item
+            constexpr int RL = D / 16, RP = kThreads8 / RL;  // lanes of a row, rows of a pass
+            Stage8<D> &st = sm.stage[s % kStages8];
+            const int *rows = sm.row[(s >> 1) % kPairs] + (s & 1) * kTileKeys;
+            const int ch = tid % RL;
+            const uint32_t kd = smem_u32(st.k), vd = smem_u32(st.v);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int ch = lh * (D / 32) + i;
-                cp16(st.k + k_chunk<D>(lr, ch), p.c.k8 + row + ch * 16, ok);
-                cp16(st.v + v_chunk<D>(lr, ch), p.c.v8 + row + ch * 16, ok);
+            for (int i = 0; i < kTileKeys / RP; ++i) {
+                const int r = i * RP + tid / RL, at = rows[r];
+                const size_t src = (size_t)max(at, 0) * D + ch * 16;
+                const int bytes = at >= 0 ? 16 : 0;  // (no key: zeros)
+                cp16(kd + k_chunk<D>(r, ch), p.c.k8 + src, bytes);
+                cp16(vd + v_chunk<D>(r, ch), p.c.v8 + src, bytes);
             }
-            if (lh == 0) {
-                cp4(&st.ks[lr], p.c.k_scale + unit, ok);
-                st.pos[lr] = !ok ? kNever : (w.verify ? pos : 0);
-            } else {
-                cp4(&st.vs[lr], p.c.v_scale + unit, ok);
+            if (tid < 2 * kTileKeys) {
+                const int r = tid & (kTileKeys - 1), at = rows[r], unit = max(at, 0) / kBlk, bytes = at >= 0 ? 4 : 0;
+                if (tid < kTileKeys) cp4(smem_u32(&st.ks[r]), p.c.k_scale + unit, bytes);
+                else cp4(smem_u32(&st.vs[r]), p.c.v_scale + unit, bytes);
             }
         };
-        int posv[kStages8 + 1], blkv[kStages8];
+        int pos_r = -1, blk_r = -1, pos_b = -1;
+        if (tid < kStep) {
+            int pos[5], blk[4];
 #pragma unroll
-        for (int t = 0; t < kStages8 + 1; ++t) posv[t] = position(t);
+            for (int t = 0; t < 5; ++t) pos[t] = position(t);
 #pragma unroll
-        for (int t = 0; t < kStages8; ++t) blkv[t] = block(posv[t]);
-        Acc<D> a;
-        const int rows = w.verify ? p.M : p.G;
-        const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;  // row tiles (as warps share them out)
-        const int mtile = warp & (mt - 1), kg = warp / mt;   // this warp's row tile, its share of the keys
-        const bool active = mtile * 16 < rows;
+            for (int t = 0; t < 4; ++t) blk[t] = block(pos[t]);
 #pragma unroll
-        for (int t = 0; t < kStages8 - 1; ++t) {
-            if (t < ntiles) fetch(t, posv[t], blkv[t]);
+            for (int t = 0; t < 3; ++t) resolve(t, pos[t], blk[t]);
+            pos_r = pos[3], blk_r = blk[3], pos_b = pos[4];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            if (s < 2 * steps) fetch(s);
             cp_commit();
         }
-        int blk_next = blkv[kStages8 - 1], pos_next = posv[kStages8 - 1], pos_after = posv[kStages8];
-        load_row<D, 0>(p, w, mtile * 16 + g, rows, c, a);
-        load_row<D, 1>(p, w, mtile * 16 + g + 8, rows, c, a);
+        Part pt;
+        pt.rows = w.verify ? p.M : p.G;
+        const Split sp = split_of(pt.rows);
+        pt.share = sp.share;
+        pt.kg = warp & (sp.share - 1);
+        pt.row0 = warp / sp.share * sp.tiles * 8;
+        pt.sure = w.verify ? w.L - (p.k + 1) : 0x7fffffff;
+        if (warp < kWarps8 / sp.share * sp.tiles) stage_queries<D>(p, w, sm, warp, pt.rows);
+        __syncthreads();
+        Acc<D> a;
         a.wsc = 0x1p126f;
         a.vmax = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int t = 0; t < kWarpTiles; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a.o[i][e] = 0.f;
-        for (int t = 0; t < ntiles; ++t) {
-            cp_wait<kStages8 - 2>();
-            __syncthreads();  // tile t is in shared memory, and tile t-1's stage is free
-            if (t + kStages8 - 1 < ntiles) fetch(t + kStages8 - 1, pos_next, blk_next);
-            cp_commit();
-            pos_next = pos_after;
-            blk_next = block(pos_next);
-            pos_after = position(t + kStages8 + 1);
-            if (active) {
-                const Stage8<D> &st = stage[t % kStages8];
-                const int t0 = t * kTileKeys, nk = min(kTileKeys, w.n - t0);
-                if (mt == 1) tile_keys<D, 1>(p, w, st, kg * 16, t0, nk, a);
-                else if (mt == 2) tile_keys<D, 2>(p, w, st, kg * 32, t0, nk, a);
-                else tile_keys<D, 2>(p, w, st, 0, t0, nk, a), tile_keys<D, 2>(p, w, st, 32, t0, nk, a);
+            for (int e = 0; e < 2; ++e) {
+                a.m[t][e] = neg_inf();
+                a.l[t][e] = 0.f;
+                a.fac[t][e] = t < sp.tiles ? sm.fac[pt.row0 + 8 * t + 2 * c + e] : 0.f;
             }
-        }
-        // --- the item's rows
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            a.r[h].l += __shfl_xor_sync(0xffffffffu, a.r[h].l, 1);
-            a.r[h].l += __shfl_xor_sync(0xffffffffu, a.r[h].l, 2);
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.o[t][i][e] = 0.f;
         }
-        const float unw = 1.f / a.wsc;
-        if (mt == 4) {
+        const bool active = pt.row0 < pt.rows;
+        const uint2(*q)[D / 16][32] = &sm.q[pt.row0 / 8];
+        for (int t = 0; t < steps; ++t) {
+            cp_wait<1>();
+            __syncthreads();  // stages 2t and 2t+1 are in shared memory, and those of step t-1 are free
+            if (tid == 0 && done < 2 && sm.item < num_items) {  // the next item's records, one link a step
+                if (done == 0) copy_item(sm.item);
+                else copy_unit();
+                ++done;
+            }
+#pragma unroll
+            for (int s = 2 * t + 3; s < 2 * t + 5; ++s) {
+                if (s < 2 * steps) fetch(s);
+                cp_commit();
+            }
+            if (tid < kStep) {
+                resolve(t + 3, pos_r, blk_r);
+                pos_r = pos_b;
+                blk_r = block(pos_b);
+                pos_b = position(t + 5);
+            }
             if (active) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const Row8 &r = a.r[h];
-                    const int row = mtile * 16 + g + 8 * h;
-                    if (row >= rows) continue;
-                    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-                    float v[D / 4];
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        v[i] = a.o[i][2 * h] * inv * unw;
-                        v[D / 8 + i] = a.o[i][2 * h + 1] * inv * unw;
-                    }
-                    store_row<D>(p, w, row, r.j, r.gi, c * (D / 4), v, D / 4);
-                    if (c == 0) store_lse(p, w, row, r.j, r.gi, r.m, r.l);
+#pragma unroll 1
+                for (int q16 = pt.kg; q16 < kStep / 16; q16 += pt.share) {
+                    const int k0 = t * kStep + 16 * q16;
+                    if (k0 >= w.n) break;
+                    const unsigned vis = (sm.mask[t % kPairs][q16 >> 1] >> (16 * (q16 & 1))) & 0xffffu;
+                    const int pos0 = w.verify ? w.begin + k0 : 0;
+                    const bool all = vis == 0xffffu && (!w.verify || pos0 + 15 <= pt.sure);
+                    const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages8];
+                    if (sp.tiles == 1) keys8<D, 1, 1>(p, w, pt, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, a);
+                    else keys8<D, 2, 1>(p, w, pt, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, a);
                 }
             }
-        } else {  // the warps that shared a row tile's keys: m, l and O through shared memory
-            constexpr int LD = D + 4;
-            float *so = reinterpret_cast<float *>(smem);           // [4 warps][16][LD]
-            float *sm = so + 4 * 16 * LD, *sl = sm + 4 * 16;       // [4 warps][16]
+        }
+        if (tid == 0 && sm.item < num_items) {  // (a short item: the rest of the next one's records)
             cp_wait<0>();
+            if (done == 0) {
+                copy_item(sm.item);
+                cp_commit();
+                cp_wait<0>();
+            }
+            if (done < 2) copy_unit();
+            done = 2;
+            cp_commit();
+        }
+        // --- the item's rows: the warps that shared the keys of a row tile join, one tile of each group at a time
+        const float unw = 1.f / a.wsc;
+        float(*so)[8][D + 4] = reinterpret_cast<float(*)[8][D + 4]>(sm.stage);  // [warps][8][D + 4]
+        float(*smx)[8] = reinterpret_cast<float(*)[8]>(so + kWarps8), (*sl)[8] = smx + kWarps8;
+        static_assert(sizeof(float) * kWarps8 * 8 * (D + 6) <= sizeof(sm.stage), "the join fits into the stages");
+        cp_wait<0>();
+#pragma unroll
+        for (int t = 0; t < kWarpTiles; ++t) {
+            if (t >= sp.tiles) break;
             __syncthreads();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int lrow = g + 8 * h;
-                float *dst = so + (warp * 16 + lrow) * LD + c * (D / 4);
+            for (int e = 0; e < 2; ++e) {
+                float *dst = &so[warp][2 * c + e][g * (D / 8)];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    dst[i] = a.o[i][2 * h];
-                    dst[D / 8 + i] = a.o[i][2 * h + 1];
-                }
-                if (c == 0) sm[warp * 16 + lrow] = a.r[h].m, sl[warp * 16 + lrow] = a.r[h].l;
+                for (int i = 0; i < D / 16; i += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * i) =
+                        make_float4(a.o[t][i][e] * unw, a.o[t][i][e + 2] * unw, a.o[t][i + 1][e] * unw,
+                                    a.o[t][i + 1][e + 2] * unw);
+                float l = a.l[t][e];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                if (g == 0) smx[warp][2 * c + e] = a.m[t][e], sl[warp][2 * c + e] = l;
             }
             __syncthreads();
-            const int share = 4 / mt;
-            constexpr int C8 = D / 8;
-            for (int x = tid; x < rows * C8; x += kThreads8) {
-                const int row = x / C8, d = (x - row * C8) * 8;
-                const int tile = row >> 4, lrow = row & 15;
-                float m = neg_inf(), l = 0.f;
-                for (int s = 0; s < share; ++s) m = fmaxf(m, sm[(s * mt + tile) * 16 + lrow]);
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (m > neg_inf()) {
-                    for (int s = 0; s < share; ++s) {
-                        const int at = (s * mt + tile) * 16 + lrow;
-                        const float f = ex2_approx((sm[at] - m) * kLog2e);
-                        l += f * sl[at];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] += f * so[at * LD + d + i];
+            constexpr int C4 = D / 4;  // four dimensions a thread
+            const int groups = kWarps8 / pt.share;
+            for (int x = tid; x < groups * 8 * C4; x += kThreads8) {
+                const int gr = x / (8 * C4), y = x - gr * 8 * C4, lr = y / C4, d = (y - lr * C4) * 4;
+                const int row = (gr * sp.tiles + t) * 8 + lr, w0 = gr * pt.share;
+                if (row >= pt.rows) continue;
+                float mx = neg_inf(), l = 0.f;
+                for (int s = 0; s < pt.share; ++s) mx = fmaxf(mx, smx[w0 + s][lr]);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (mx > neg_inf()) {
+                    for (int s = 0; s < pt.share; ++s) {
+                        const float f = ex2_approx((smx[w0 + s][lr] - mx) * kLog2e);
+                        const float4 o = *reinterpret_cast<const float4 *>(&so[w0 + s][lr][d]);
+                        l += f * sl[w0 + s][lr];
+                        v.x += f * o.x, v.y += f * o.y, v.z += f * o.z, v.w += f * o.w;
                     }
                 } else {
-                    for (int s = 0; s < share; ++s) l += sl[(s * mt + tile) * 16 + lrow];  // 0, or a NaN
+                    for (int s = 0; s < pt.share; ++s) l += sl[w0 + s][lr];  // 0, or a NaN
                 }
-                const float inv = l == 0.f ? 0.f : unw / l;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= inv;
-                const int j = w.verify ? row / p.G : 0;
-                store_row<D>(p, w, row, j, row - j * p.G, d, v, 8);
-                if (d == 0) store_lse(p, w, row, j, row - j * p.G, m, l);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+                const int j = w.verify ? row / p.G : 0, gi = row - j * p.G;
+                store4(p, w, D, row, j, gi, d, v);
+                if (d == 0) store_lse(p, w, row, j, gi, mx, l);
             }
         }
-        __syncthreads();  // (an item without keys has had no barrier since s_item was written)
-        it = s_item;
     }
     if (bad) atomicOr(&p.hdr->err, bad);
 }
 
 template <int D>
 cudaError_t launch_t(const Kv8Params &p, int nsm, cudaStream_t st) {
-    constexpr int kSmem = kStages8 * (int)sizeof(Stage8<D>);
-    static_assert(4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 4 <= kSmem, "the join fits into the stages");
-    static int occupancy[kMaxDevices];
+    constexpr int kSmem = (int)sizeof(Smem8<D>);
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
     static unsigned long long configured[kMaxDevices] = {};
     int dev = 0;
     unsigned long long ctx = 0;
@@ -555,20 +674,15 @@ cudaError_t launch_t(const Kv8Params &p, int nsm, cudaStream_t st) {
     if (ctx == 0 || __atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE) != ctx) {
         e = cudaFuncSetAttribute(attn_kv8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kv8_kernel<D>, kThreads8, kSmem);
-        if (e != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
         e = current_device_context(&dev, &ctx);  // (the calls above made a context current)
         if (e != cudaSuccess) return e;
-        __atomic_store_n(&occupancy[dev], n, __ATOMIC_RELAXED);
         __atomic_store_n(&configured[dev], ctx, __ATOMIC_RELEASE);
     }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(nsm * __atomic_load_n(&occupancy[dev], __ATOMIC_RELAXED));
+    cfg.gridDim = dim3(2 * nsm);
     cfg.blockDim = dim3(kThreads8);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
