@@ -30,6 +30,8 @@
 //     the same 64 further on), so that a 16-byte load holds the lane's part of
 //     four steps; V's rows are read whole by eight lanes, a byte permute pairs two
 //     keys' values of a dimension, and one conversion makes an operand register.
+//     Among 16 keys, m = g and g + 8 are keys 2g and 2g + 1, so that a lane holds
+//     neighbours: their scales are one load, their logits one store.
 //     P is transposed between the products by movmatrix.
 //   * K and V rows land in shared memory by 16-byte asynchronous copies, their
 //     16-byte chunks XOR-ed with the row so that these loads meet no bank twice.
@@ -85,6 +87,12 @@ struct Work {
     long long logit_off;
 };
 
+struct RowInfo {
+    long long logits;  // offset of the row's logit at position 0 (-1: none to write)
+    int lim;           // last position it sees
+    int pad;
+};
+
 // The records of the item after this one, copied while this one runs.
 struct alignas(16) Ahead {
     Item item;
@@ -105,6 +113,7 @@ struct Smem8 {
     Stage8<D> stage[kStages8];
     uint2 q[kMaxTiles][D / 16][32];    // query operands: row tile, step, lane
     float fac[kMaxRows];               // per row: logit = sum * fac * ks
+    RowInfo rows[kMaxRows];
     int row[kPairs][kStep];            // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
     unsigned mask[kPairs][kStep / 32]; // which of 32 keys there are
     Ahead ahead;
@@ -122,17 +131,18 @@ __device__ __forceinline__ Split split_of(int rows) {
     return nrt <= 4 ? Split{2, kWarps8 / 2} : Split{2, kWarps8 / 4};
 }
 
-// Byte offset of 16-byte chunk c of row r.  K: the two rows that eight lanes read together differ in bit 0
-// of r; V: the four rows differ in bits 1 and 2.  (At D = 64 two rows make one 128-byte line.)  The XORs do
-// not depend on multiples of 8 of the row, so an offset is a lane's base plus a constant.
+// Byte offset of 16-byte chunk c of row r.  K: the two rows that eight lanes read together differ in bit 1
+// of r; V: the four rows differ in bits 2 and 3.  (At D = 64 two rows make one 128-byte line.)  The XORs do
+// not depend on multiples of 16 of the row, so an offset is a lane's base plus a constant.
 template <int D>
 __device__ __forceinline__ int k_chunk(int r, int c) {
-    return D == 128 ? r * 128 + (c ^ ((r & 1) << 2)) * 16 : r * 64 + c * 16;
+    if (D == 128) return r * 128 + (c ^ ((r & 2) << 1)) * 16;
+    return (r >> 1) * 128 + ((((r & 1) << 2) | c) ^ ((r & 2) << 1)) * 16;
 }
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
-    if (D == 128) return r * 128 + (c ^ (((r >> 1) & 3) << 1)) * 16;
-    return (r >> 1) * 128 + ((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) * 16;
+    if (D == 128) return r * 128 + (c ^ (((r >> 2) & 3) << 1)) * 16;
+    return (r >> 1) * 128 + ((((r & 1) << 2) | c) ^ (((r >> 2) & 3) << 1)) * 16;
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
@@ -189,27 +199,24 @@ struct Part {
     int sure;        // every row sees up to here
 };
 
-// Last position that row r sees.
-__device__ __forceinline__ int row_limit(const Kv8Params &p, const Work &w, int r) {
-    return w.verify ? w.L - (p.k + 1) + r / p.G : 0x7fffffff;
-}
-
 // 16 NK keys of a stage, from its row r0 on, for the first NT row tiles of a warp.  vis: which of 32 keys from
 // r0 on there are; all: the rows see every one; pos0: position of the first (verify); left: keys of the item from
 // the first one on.
 template <int D, int NT, int NK>
-__device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const Part &pt, const Stage8<D> &st, int r0,
-                                      unsigned vis, bool all, int pos0, int left, const uint2 (*q)[D / 16][32], Acc<D> &a) {
+__device__ __forceinline__ void keys8(const Kv8Params &p, const Stage8<D> &st, int r0,
+                                      unsigned vis, bool all, int pos0, int left, const uint2 (*q)[D / 16][32],
+                                      const RowInfo *rows, bool dump, Acc<D> &a) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    float s[NK][NT][4];  // keys 16 h + g and 16 h + 8 + g, rows 2c and 2c + 1
+    float s[NK][NT][4];  // keys 16 h + 2 g and the next, rows 2c and 2c + 1
 #pragma unroll
     for (int h = 0; h < NK; ++h)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[h][t][e] = 0.f;
-    const uint8_t *kb = st.k + r0 * D + k_chunk<D>(g, c);
-    const int flip = (g & 1) ? -64 : 64;  // the chunk four further on, under the XOR
+    const uint8_t *kb = st.k + r0 * D + k_chunk<D>(2 * g, c);
+    const int flip = (g & 1) ? -64 : 64;                // the chunk four further on, under the XOR,
+    const int odd = D == 128 ? D : flip;                // and the next key
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
         uint4 x[NK][2];
@@ -217,7 +224,7 @@ __device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const P
         for (int h = 0; h < NK; ++h)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                x[h][e] = *reinterpret_cast<const uint4 *>(kb + (i ? flip : 0) + (16 * h + 8 * e) * D);
+                x[h][e] = *reinterpret_cast<const uint4 *>(kb + (i ? flip : 0) + 16 * h * D + (e ? odd : 0));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint2 b[NT];
@@ -237,17 +244,16 @@ __device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const P
     bool grow = false;
 #pragma unroll
     for (int h = 0; h < NK; ++h) {
-        const float k0 = st.ks[r0 + 16 * h + g], k1 = st.ks[r0 + 16 * h + 8 + g];
+        const float2 ks = *reinterpret_cast<const float2 *>(st.ks + r0 + 16 * h + 2 * g);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[h][t][e] *= a.fac[t][e & 1] * (e < 2 ? k0 : k1);
+            for (int e = 0; e < 4; ++e) s[h][t][e] *= a.fac[t][e & 1] * (e < 2 ? ks.x : ks.y);
             if (!all) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int key = 16 * h + (e < 2 ? 0 : 8) + g;
-                    if (!((vis >> key) & 1) || pos0 + key > row_limit(p, w, pt.row0 + 8 * t + 2 * c + (e & 1)))
-                        s[h][t][e] = neg_inf();
+                    const int key = 16 * h + 2 * g + (e >> 1);
+                    if (!((vis >> key) & 1) || pos0 + key > rows[8 * t + 2 * c + (e & 1)].lim) s[h][t][e] = neg_inf();
                 }
             }
 #pragma unroll
@@ -255,20 +261,22 @@ __device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const P
                 grow |= (fmaxf(s[h][t][e], s[h][t][e + 2]) - a.m[t][e]) * kLog2e > kGrowLog2;
         }
     }
-    if (w.verify && p.logits) {
-        const long long base = w.logit_off + pos0 + g;
+    if (dump) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = pt.row0 + 8 * t + 2 * c + e;
-                if (r < pt.rows) {
-                    const int j = r / p.G;
-                    float *dst = p.logits + base + (long long)((w.g * p.G + r - j * p.G) * (p.k + 1) + j) * w.L;
+                const long long lb = rows[8 * t + 2 * c + e].logits;
+                if (lb < 0) continue;
+                float *dst = p.logits + lb + pos0 + 2 * g;  // eight lanes write 64 bytes of a row
 #pragma unroll
-                    for (int h = 0; h < NK; ++h) {  // eight lanes write 32 bytes of a row
-                        if (16 * h + g < left) dst[16 * h] = s[h][t][e];
-                        if (16 * h + 8 + g < left) dst[16 * h + 8] = s[h][t][e + 2];
+                for (int h = 0; h < NK; ++h) {
+                    const int key = 16 * h + 2 * g;
+                    if (key + 2 <= left && !(reinterpret_cast<uintptr_t>(dst) & 7)) {
+                        *reinterpret_cast<float2 *>(dst + 16 * h) = make_float2(s[h][t][e], s[h][t][e + 2]);
+                    } else {
+                        if (key < left) dst[16 * h] = s[h][t][e];
+                        if (key + 1 < left) dst[16 * h + 1] = s[h][t][e + 2];
                     }
                 }
             }
@@ -278,11 +286,11 @@ __device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const P
     float tm = 0.f;
 #pragma unroll
     for (int h = 0; h < NK; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            vw[h][e] = st.vs[r0 + 16 * h + 8 * e + g];
-            tm = fmaxf(tm, fabsf(vw[h][e]));
-        }
+    {
+        const float2 x = *reinterpret_cast<const float2 *>(st.vs + r0 + 16 * h + 2 * g);
+        vw[h][0] = x.x, vw[h][1] = x.y;
+        tm = fmaxf(tm, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
     grow |= tm > a.vmax;
     if (__any_sync(0xffffffffu, grow)) {  // rare: new reference maxima, a larger value scale
         tm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tm)));
@@ -333,16 +341,16 @@ __device__ __forceinline__ void keys8(const Kv8Params &p, const Work &w, const P
             pb[h][t][1] = transpose8x8(pack_f16x2(e4[2] * w1, e4[3] * w1));
         }
     }
-    // V: this lane's dimensions (16 at D = 128, 8 at D = 64) of keys 2c, 2c + 1, 2c + 8, 2c + 9
+    // V: this lane's dimensions (16 at D = 128, 8 at D = 64) of keys 4c .. 4c + 3 (k = 2c, 2c + 8, 2c + 1, 2c + 9)
     constexpr int W = D / 32;  // words per key
-    const uint8_t *vb = st.v + r0 * D + (D == 128 ? v_chunk<D>(2 * c, g) : v_chunk<D>(2 * c, g >> 1) + (g & 1) * 8);
+    const uint8_t *vb = st.v + r0 * D + (D == 128 ? v_chunk<D>(4 * c, g) : v_chunk<D>(4 * c, g >> 1) + (g & 1) * 8);
     const int next = D == 128 ? 128 : ((c & 2) ? -64 : 64);  // (D = 64: the other half of the line, under the XOR)
 #pragma unroll
     for (int h = 0; h < NK; ++h) {
         uint32_t x[4][W];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const uint8_t *src = vb + (16 * h + 8 * (u >> 1)) * D + ((u & 1) ? next : 0);
+            const uint8_t *src = vb + (16 * h + 2 * (u & 1)) * D + ((u >> 1) ? next : 0);  // key 4c + 2 (u % 2) + u / 2
             if (D == 128) {
                 const uint4 y = *reinterpret_cast<const uint4 *>(src);
                 x[u][0] = y.x, x[u][1] = y.y, x[u][W - 2] = y.z, x[u][W - 1] = y.w;
@@ -416,7 +424,16 @@ __device__ __forceinline__ void stage_queries(const Kv8Params &p, const Work &w,
             sm.q[t][4 * i + j][lane] = make_uint2(pack_f16x2(bf16lo(wd[2 * j]) * up, bf16hi(wd[2 * j]) * up),
                                                   pack_f16x2(bf16lo(wd[2 * j + 1]) * up, bf16hi(wd[2 * j + 1]) * up));
     }
-    if (c == 0) sm.fac[row] = down * p.scale;
+    if (c == 0) {
+        sm.fac[row] = down * p.scale;
+        RowInfo ri;
+        const int j = w.verify ? row / p.G : 0, gi = row - j * p.G;
+        ri.logits = row < rows && w.verify && p.logits
+                        ? w.logit_off + ((long long)(w.g * p.G + gi) * (p.k + 1) + j) * w.L : -1;
+        ri.lim = w.verify ? w.L - (p.k + 1) + j : 0x7fffffff;
+        ri.pad = 0;
+        sm.rows[row] = ri;
+    }
 }
 
 template <int D>
@@ -563,6 +580,8 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         }
         const bool active = pt.row0 < pt.rows;
         const uint2(*q)[D / 16][32] = &sm.q[pt.row0 / 8];
+        const RowInfo *rinfo = sm.rows + pt.row0;
+        const bool dump = w.verify && p.logits;
         for (int t = 0; t < steps; ++t) {
             cp_wait<1>();
             __syncthreads();  // stages 2t and 2t+1 are in shared memory, and those of step t-1 are free
@@ -591,8 +610,8 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                     const int pos0 = w.verify ? w.begin + k0 : 0;
                     const bool all = vis == 0xffffu && (!w.verify || pos0 + 15 <= pt.sure);
                     const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages8];
-                    if (sp.tiles == 1) keys8<D, 1, 1>(p, w, pt, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, a);
-                    else keys8<D, 2, 1>(p, w, pt, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, a);
+                    if (sp.tiles == 1) keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
+                    else keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
                 }
             }
         }
