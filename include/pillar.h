@@ -689,6 +689,47 @@ PILLAR_API int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *
                                    uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
                                    size_t ws_bytes, void *stream);
 
+/* pillar_prompt_attn_workspace_bytes -- workspace of pillar_prompt_attn for
+ * shape->B sequences of n tokens in all. */
+PILLAR_API int pillar_prompt_attn_workspace_bytes(const pillar_shape_t *shape, int32_t n, size_t *bytes);
+
+/*
+ * pillar_prompt_attn -- causal attention over whole prompts, packed one after
+ * another: what fills a context before its first draft step.  With rows
+ * [seq_off[b], seq_off[b+1]) the tokens of sequence b, row i of it and query
+ * head h attend rows 0 .. i of the sequence under KV head h / G:
+ *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j, h / G]) v[j, h / G]
+ *   lse[i, h] = log sum_j exp(scale * q[i, h] . k[j, h / G])   (natural log)
+ *
+ *   q             bf16, token i's [Hq, D] at i * q_stride elements
+ *   k, v          bf16, token i's [Hkv, D] at i * k_stride (v_stride)
+ *                 (a stride of 0 means packed rows; others are multiples of 8
+ *                 and at least the row, e.g. slices of one projection's output)
+ *   n             tokens in q, k, v, out and lse
+ *   seq_off       [B+1] int32, ascending, within [0, n].  A sequence whose
+ *                 offsets descend, leave [0, n] or are more than max_len apart
+ *                 is skipped (PILLAR_FLAG_REQUEST); so is what exceeds the
+ *                 workspace when sequences overlap.  Empty ones are allowed.
+ *                 Rows of no sequence are left as they were.
+ *   out           [n, Hq, D] bf16
+ *   lse           [n, Hq] fp32, or NULL
+ *   workspace     pillar_prompt_attn_workspace_bytes bytes, 256-byte aligned; its
+ *                 error word is cleared by the call and read with
+ *                 pillar_get_error
+ * Only shape->B, Hq, Hkv, D, max_len, sm_scale and wait_timeout_us are used (the
+ * whole shape is checked; k = 0 fits).  q, k, v and out are 16-byte aligned,
+ * seq_off and lse 4.  A NaN or infinity in a token's v may reach rows of its own
+ * sequence that precede it by less than 128 positions; it never reaches another
+ * sequence.  Every wait on the device is bounded as in pillar_attn_unified.
+ * Asynchronous on `stream`; allocates nothing.  Returns PILLAR_OK,
+ * PILLAR_ERR_ARG, PILLAR_ERR_WORKSPACE or PILLAR_ERR_CUDA; with n == 0 or
+ * B == 0 nothing is launched.
+ */
+PILLAR_API int pillar_prompt_attn(const pillar_shape_t *shape, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                                  int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t n,
+                                  const int32_t *seq_off, uint16_t *out, float *lse, void *workspace, size_t ws_bytes,
+                                  void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,6 +40,8 @@ Entry points (same names as the C ABI):
                   out, verify_logits, verify_lse, workspace, stream=None)   (the unified step over the 8-bit cache)
   pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
                       verify_lse, workspace, stream=None)        (the same on a plan of pillar_attn_plan)
+  pillar_prompt_attn_workspace_bytes(shape, n)
+  pillar_prompt_attn(shape, q, k, v, seq_off, out, lse, workspace, stream=None)   (causal attention over packed prompts)
 """
 from __future__ import annotations
 
@@ -59,7 +61,7 @@ __all__ = [
     "pillar_kv_offload", "pillar_kv_reload", "PillarOffloadFifo", "pillar_offload_init", "pillar_offload_reserve",
     "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
     "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
-    "pillar_attn_kv8", "pillar_attn_run_kv8",
+    "pillar_attn_kv8", "pillar_attn_run_kv8", "pillar_prompt_attn_workspace_bytes", "pillar_prompt_attn",
     "FLAG_BLOCK", "FLAG_VALUE", "KV_BLOCK",
 ]
 
@@ -76,7 +78,8 @@ EXPORTED = ("pillar_attn_workspace_bytes", "pillar_attn_unified", "pillar_attn_u
             "pillar_attn_plan", "pillar_attn_run",
             "pillar_offload_reserve", "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
             "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
-            "pillar_attn_kv8", "pillar_attn_run_kv8")
+            "pillar_attn_kv8", "pillar_attn_run_kv8",
+            "pillar_prompt_attn_workspace_bytes", "pillar_prompt_attn")
 MAX_BUCKETS = 64  # PILLAR_MAX_BUCKETS
 OFFLOAD_QUEUE = 1024  # PILLAR_OFFLOAD_QUEUE
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024 + 256
@@ -185,6 +188,8 @@ def load():
     lib.pillar_kv8_append.argtypes = [SP, P, I64, P, I64, I32, P, P, P, I32, P, P, P, P, P, P]
     lib.pillar_attn_kv8.argtypes = [SP] + [P] * 6 + [I32] + [P] * 8 + [SZ, P]
     lib.pillar_attn_run_kv8.argtypes = [SP] + [P] * 6 + [I32] + [P] * 5 + [SZ, P]
+    lib.pillar_prompt_attn_workspace_bytes.argtypes = [SP, I32, ctypes.POINTER(SZ)]
+    lib.pillar_prompt_attn.argtypes = [SP, P, I64, P, I64, P, I64, I32, P, P, P, P, SZ, P]
     lib.pillar_status_string.restype = ctypes.c_char_p
     for n in EXPORTED:
         if n == "pillar_status_string":
@@ -512,6 +517,32 @@ def pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_tabl
         *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _stream(stream))
     if st:
         raise PillarError("pillar_attn_run_kv8", st)
+
+
+# --------------------------------------------------------------- prompts
+
+def pillar_prompt_attn_workspace_bytes(shape: PillarShape, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().pillar_prompt_attn_workspace_bytes(ctypes.byref(shape), int(n), ctypes.byref(out))
+    if st:
+        raise PillarError("pillar_prompt_attn_workspace_bytes", st)
+    return int(out.value)
+
+
+def pillar_prompt_attn(shape, q, k, v, seq_off, out, lse, workspace, stream=None):
+    """Causal attention over prompts packed one after another ([n, heads, D] bf16; tokens may lie apart); lse [n, Hq] fp32
+    or None."""
+    dev, n = _current_device(), q.shape[0]
+    qp, qs = _rows("q", q, shape.Hq, shape.D, dev)
+    kp, ks = _rows("k", k, shape.Hkv, shape.D, dev, n)
+    vp, vs = _rows("v", v, shape.Hkv, shape.D, dev, n)
+    st = load().pillar_prompt_attn(
+        ctypes.byref(shape), qp, qs, kp, ks, vp, vs, n, _arg("seq_off", seq_off, _T.i32, (shape.B + 1,), dev),
+        _arg("out", out, _T.bf16, (n, shape.Hq, shape.D), dev),
+        None if lse is None else _arg("lse", lse, _T.f32, (n, shape.Hq), dev), *_workspace(workspace, dev),
+        _stream(stream))
+    if st:
+        raise PillarError("pillar_prompt_attn", st)
 
 
 # --------------------------------------------------------------- offload FIFO (host side)

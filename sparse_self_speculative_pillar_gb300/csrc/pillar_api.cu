@@ -13,6 +13,7 @@
 #include "pillar_kv8.h"
 #include "pillar_lists.h"
 #include "pillar_map.h"
+#include "pillar_prompt.h"
 
 namespace pillar {
 
@@ -570,6 +571,55 @@ int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_
     if (sp != PILLAR_OK) return sp;
     return pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, sparse_idx, out,
                                verify_logits, verify_lse, workspace, ws_bytes, stream);
+}
+
+int pillar_prompt_attn_workspace_bytes(const pillar_shape_t *shape, int32_t n, size_t *bytes) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    if (n < 0 || !bytes || prompt_max_tiles(shape->B, n) > 0x7fffffffll) return PILLAR_ERR_ARG;
+    *bytes = prompt_ws_bytes(shape->B, n);
+    return PILLAR_OK;
+}
+
+int pillar_prompt_attn(const pillar_shape_t *shape, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                       int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t n, const int32_t *seq_off,
+                       uint16_t *out, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    const pillar_shape_t &s = *shape;
+    PromptArgs a;
+    if (n < 0 || prompt_max_tiles(s.B, n) > 0x7fffffffll || !row_stride(q_stride, s.Hq, s.D, &a.q_stride) || !row_stride(k_stride, s.Hkv, s.D, &a.k_stride) ||
+        !row_stride(v_stride, s.Hkv, s.D, &a.v_stride))
+        return PILLAR_ERR_ARG;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (n == 0 || s.B == 0) {  // nothing to do; a workspace passed in still reads back as clean
+        if (workspace && ws_bytes >= sizeof(int) && cudaMemsetAsync(workspace, 0, sizeof(int), cs) != cudaSuccess)
+            return PILLAR_ERR_CUDA;
+        return PILLAR_OK;
+    }
+    if (!q || !k || !v || !seq_off || !out) return PILLAR_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(seq_off, 4) ||
+        !aligned(lse, 4))
+        return PILLAR_ERR_ARG;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < prompt_ws_bytes(s.B, n)) return PILLAR_ERR_WORKSPACE;
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.seq_off = seq_off;
+    a.out = out;
+    a.lse = lse;
+    a.ws = static_cast<char *>(workspace);
+    a.B = s.B;
+    a.n = n;
+    a.Hq = s.Hq;
+    a.Hkv = s.Hkv;
+    a.D = s.D;
+    a.max_len = s.max_len;
+    a.scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / std::sqrt((float)s.D);
+    a.wait_ns = s.wait_timeout_us > 0 ? (unsigned long long)s.wait_timeout_us * 1000ull : kWaitTimeoutNs;
+    return launch_prompt(a, nsm, cs) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
 }
 
 int pillar_get_error(void *workspace, void *stream, int32_t *flags) {
