@@ -21,6 +21,8 @@ namespace {
 using CtxGetCurrentFn = CUresult (*)(CUcontext *);
 using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
 
+}  // namespace
+
 void *driver_entry(const char *name, int version) {
     void *f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -29,7 +31,6 @@ void *driver_entry(const char *name, int version) {
         return nullptr;
     return f;
 }
-}  // namespace
 
 cudaError_t current_device_context(int *dev, unsigned long long *ctx_id) {
     static const CtxGetCurrentFn get_current = reinterpret_cast<CtxGetCurrentFn>(driver_entry("cuCtxGetCurrent", 4000));
@@ -576,7 +577,7 @@ int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_
 int pillar_prompt_attn_workspace_bytes(const pillar_shape_t *shape, int32_t n, size_t *bytes) {
     const int st = check_shape(shape);
     if (st != PILLAR_OK) return st;
-    if (n < 0 || !bytes || prompt_max_tiles(shape->B, n) > 0x7fffffffll) return PILLAR_ERR_ARG;
+    if (n < 0 || !bytes || prompt_max_tiles(shape->B, n) * shape->Hq > 0x7fffffffll) return PILLAR_ERR_ARG;
     *bytes = prompt_ws_bytes(shape->B, n);
     return PILLAR_OK;
 }
@@ -588,7 +589,7 @@ int pillar_prompt_attn(const pillar_shape_t *shape, const uint16_t *q, int64_t q
     if (st != PILLAR_OK) return st;
     const pillar_shape_t &s = *shape;
     PromptArgs a;
-    if (n < 0 || prompt_max_tiles(s.B, n) > 0x7fffffffll || !row_stride(q_stride, s.Hq, s.D, &a.q_stride) || !row_stride(k_stride, s.Hkv, s.D, &a.k_stride) ||
+    if (n < 0 || prompt_max_tiles(s.B, n) * s.Hq > 0x7fffffffll || !row_stride(q_stride, s.Hq, s.D, &a.q_stride) || !row_stride(k_stride, s.Hkv, s.D, &a.k_stride) ||
         !row_stride(v_stride, s.Hkv, s.D, &a.v_stride))
         return PILLAR_ERR_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);

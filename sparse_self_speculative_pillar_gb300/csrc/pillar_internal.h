@@ -88,6 +88,8 @@ constexpr int kMaxDevices = 64;
 // The current device and the unique id of the context current on it (0
 // when no context is current yet: the caller then sets up and asks again).
 cudaError_t current_device_context(int *dev, unsigned long long *ctx_id);
+// A driver function, resolved through the runtime (null when there is none): no link-time dependency.
+void *driver_entry(const char *name, int version);
 
 // 0: the default, chosen per request by its context length (see kLongContext)
 inline int verify_chunk_of(const pillar_shape_t &s) { return s.verify_chunk > 0 ? s.verify_chunk : 0; }

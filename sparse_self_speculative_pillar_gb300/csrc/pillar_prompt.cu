@@ -4,8 +4,27 @@
 //   out[i, h] = sum_{j <= i} softmax_j(scale q_ih . k_j,h/G) v_j,h/G   (j in i's sequence)
 //   lse[i, h] = log sum_{j <= i} e^(scale q_ih . k_j,h/G)
 //
-// A planner lists the sequences' 256-row tiles, longest first.  The attention
-// kernel: one warp per (row, head), a running maximum and sum over the keys.
+// A planner lists the sequences' 256-row tiles, those with the most keys first.
+// The attention kernel is persistent, one CTA per SM; CTA c takes units (tile,
+// head) c, 2 G - 1 - c, 2 G + c, ... of the G CTAs' rounds, so that the rounds'
+// slopes cancel.  A unit is two tiles of 128 query rows against the 128-key tiles
+// up to the diagonal:
+//   * a load thread brings Q, K and V tiles by TMA (128-byte swizzle; K and V through
+//     one ring, in the order in which they are used);
+//   * an MMA warp issues S_b = Q_b K^T (128 x 128, tcgen05, both operands in shared
+//     memory, fp32 in tensor memory) and O_b += P_b V (P from tensor memory, over
+//     its scores) for the two row tiles b in turn: while the softmax of one is at
+//     work, the tensor cores have the other's products;
+//   * two warpgroups, one per row tile, a row per thread: the whole row of scores
+//     in registers, its maximum, exponentials and sum without a shuffle, and
+//     bf16 probabilities back to tensor memory.  O is rescaled only when a row's
+//     maximum grew by more than 2^8.  At a unit's end they normalise and write O.
+// What bounds it: the tensor cores (4 D flops a visible pair; half of the diagonal
+// tile is computed and masked).  Keys behind a sequence's end lie in the next one:
+// their scores are behind the diagonal for every row that counts, and their values
+// are zeroed in shared memory, since 0 * NaN would carry over.
+#include <cuda.h>  // CUtensorMap
+
 #include "pillar_device.cuh"
 #include "pillar_prompt.h"
 
@@ -79,55 +98,491 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
     }
 }
 
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreadsP = (kSoftmaxWarps + 4) * 32;  // and the MMA warp, the load warp, two idle ones
+constexpr uint32_t kSoftmaxRegs = 208, kOtherRegsP = 80;
+static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegsP <= kThreadsP * 168, "registers of the launch");
+constexpr int kTileP = 128;  // query rows of a row tile, keys of a key tile
+constexpr uint32_t kTmemColsP = 512;
+constexpr float kRescaleLog2P = 8.f;
+
+struct PromptParams {
+    CUtensorMap q, k, v;  // [n, heads, D] bf16, box 128 tokens x 1 head x 64 columns, 128-byte swizzle
+    uint16_t *out;
+    float *lse;
+    PromptHeader *hdr;
+    const PromptTile *tiles;
+    int Hq, G;
+    float scale;
+    unsigned long long wait_ns;
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) prompt_kernel(const PromptArgs a, const PromptHeader *hdr, const PromptTile *tiles) {
-    pdl_wait_prerequisites();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
-    const long long warps = (long long)gridDim.x * 8;
-    const long long total = (long long)hdr->num_tiles * kPromptRows * a.Hq;
-    for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += warps) {
-        const int h = (int)(w % a.Hq);
-        const long long x = w / a.Hq;
-        const PromptTile t = tiles[x / kPromptRows];
-        const int i = t.tile * kPromptRows + (int)(x % kPromptRows);
-        if (i >= t.len) continue;
-        auto at = [&](const uint16_t *p, long long stride, long long row, int head, int e) {
-            return __uint_as_float((uint32_t)__ldg(p + row * stride + (long long)head * D + lane * E + e) << 16);
-        };
-        float q[E], o[E] = {};
+struct SmemP {
+    static constexpr int kTileBytes = kTileP * D * 2;
+    static constexpr int kSlots = D == 128 ? 5 : 8;  // K and V tiles in shared memory
+    alignas(1024) uint8_t q[2][kTileBytes];
+    uint8_t kv[kSlots][kTileBytes];
+    uint64_t qfull[2], qempty[2], kvfull[kSlots], kvempty[kSlots];
+    uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], cexit, drain;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(SmemP<128>) <= 227 * 1024, "shared memory of a CTA");
+static_assert(sizeof(SmemP<64>) > 114 * 1024, "never two CTAs on an SM: each takes all of its tensor memory");
+
+struct BoundsP {
+    volatile int *abort;
+    int *err;
+    unsigned long long ns;
+};
+__device__ __forceinline__ bool waitp(uint64_t *bar, uint32_t parity, const BoundsP &b) {
+    return mbar_wait(bar, parity, b.abort, b.err, b.ns);
+}
+// Bounded wait for copies or products already in flight, whatever the pipeline's bound and the abort flag say.
+__device__ __forceinline__ void drainp(uint64_t *bar, uint32_t parity) {
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
+}
+
+// Columns [x, x + 64) of head y of tokens z .. z + 127.
+__device__ __forceinline__ void tma_load3(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A unit of a CTA.
+struct Unit {
+    int row0, len, q0, h;  // the sequence's first row and length, the unit's first row in it, the query head
+    int na, nb;            // key tiles of the row tiles (nb 0: there is no second one)
+    __device__ __forceinline__ int nk() const { return nb ? nb : na; }
+    __device__ __forceinline__ int of(int b) const { return b ? nb : na; }
+};
+__device__ __forceinline__ bool get_unit(const PromptParams &p, int round, int total, Unit *u) {
+    const int c = blockIdx.x, G = gridDim.x;
+    const long long r = (long long)round * G + ((round & 1) ? G - 1 - c : c);
+    if (r >= total) return false;
+    const int t = (int)(r / p.Hq);
+    const PromptTile x = p.tiles[t];
+    u->row0 = x.row0;
+    u->len = x.len;
+    u->q0 = x.tile * kPromptRows;
+    u->h = (int)(r - (long long)t * p.Hq);
+    u->na = 2 * x.tile + 1;
+    u->nb = u->q0 + kTileP < x.len ? u->na + 1 : 0;
+    return true;
+}
+// (only the last round can be incomplete)
+__device__ __forceinline__ int rounds_of(int total) { return (total + gridDim.x - 1) / gridDim.x; }
+
+// ------------------------------------------------------------------ load thread
+
+template <int D>
+__device__ void load_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd, int total) {
+    using S = SmemP<D>;
+    int slot = 0;
+    uint32_t phase = 0, qph[2] = {0, 0}, issued = 0, parity = 0, qissued = 0, qparity = 0;
+    bool ok = true;
+    auto tile = [&](uint8_t *dst, const CUtensorMap *m, int head, int row, uint64_t *bar) {
+        mbar_arrive_expect_tx(bar, S::kTileBytes);
 #pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = at(a.q, a.q_stride, (long long)t.row0 + i, h, e);
-        float m = neg_inf(), l = 0.f;
-        for (int j = 0; j <= i; ++j) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s = fmaf(q[e], at(a.k, a.k_stride, (long long)t.row0 + j, h / G, e), s);
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            s *= a.scale;
-            const float mn = fmaxf(m, s), f = m == neg_inf() ? 0.f : expf(m - mn), p = expf(s - (mn == neg_inf() ? 0.f : mn));
-            l = l * f + p;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * at(a.v, a.v_stride, (long long)t.row0 + j, h / G, e);
-            m = mn;
+        for (int x = 0; x < D; x += 64) tma_load3(dst + x * (kTileP * 2), m, x, head, row, bar);
+    };
+    auto kv = [&](const CUtensorMap *m, int head, int row) {
+        ok = waitp(&sm.kvempty[slot], phase ^ 1, bd);
+        if (!ok) return;
+        tile(sm.kv[slot], m, head, row, &sm.kvfull[slot]);
+        issued |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | (phase << slot);
+        if (++slot == S::kSlots) slot = 0, phase ^= 1;
+    };
+    auto query = [&](const Unit &u, int b) {
+        ok = waitp(&sm.qempty[b], qph[b] ^ 1, bd);
+        if (!ok) return;
+        tile(sm.q[b], &p.q, u.h, u.row0 + u.q0 + b * kTileP, &sm.qfull[b]);
+        qissued |= 1u << b;
+        qparity = (qparity & ~(1u << b)) | (qph[b] << b);
+        qph[b] ^= 1;
+    };
+    const int rounds = rounds_of(total);
+    for (int r = 0; r < rounds && ok; ++r) {
+        Unit u;
+        if (!get_unit(p, r, total, &u)) break;
+        query(u, 0);
+        for (int j = 0; j < u.nk() && ok; ++j) {
+            kv(&p.k, u.h / p.G, u.row0 + j * kTileP);
+            if (ok && j == 0 && u.nb) query(u, 1);
+            if (ok) kv(&p.v, u.h / p.G, u.row0 + j * kTileP);
         }
-        const long long row = ((long long)t.row0 + i) * a.Hq + h;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(o[e] * inv);
-            a.out[row * D + lane * E + e] = *reinterpret_cast<const uint16_t *>(&b);
-        }
-        if (a.lse && lane == 0) a.lse[row] = l > 0.f ? m + logf(l) : (l == 0.f ? neg_inf() : l);
     }
+    if (!ok) {  // every copy lands before the CTA can exit
+        for (int s = 0; s < S::kSlots; ++s)
+            if ((issued >> s) & 1) drainp(&sm.kvfull[s], (parity >> s) & 1);
+        for (int b = 0; b < 2; ++b)
+            if ((qissued >> b) & 1) drainp(&sm.qfull[b], (qparity >> b) & 1);
+    }
+}
+
+// ------------------------------------------------------------------ MMA warp
+
+template <int D>
+__device__ void mma_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd, int total, uint32_t tm, int lane) {
+    using S = SmemP<D>;
+    constexpr uint32_t idS = umma_idesc_bf16(kTileP, kTileP, 0, 0), idO = umma_idesc_bf16(kTileP, D, 0, 1);
+    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, oph[2] = {0, 0};
+    int slot0 = 0;        // slot of the next unit's first K tile
+    uint32_t phase0 = 0;  // and its phase
+    bool issued = false;
+    auto slot_of = [&](int i, uint32_t *ph) {  // i-th K or V tile of the unit (K_j: 2 j, V_j: 2 j + 1)
+        const int x = slot0 + i;
+        *ph = (phase0 + x / S::kSlots) & 1;
+        return x % S::kSlots;
+    };
+    auto scores = [&](int b, int slot) {
+        const uint64_t dq = umma_sdesc_sw128(smem_u32(sm.q[b]), 16, 1024), dk = umma_sdesc_sw128(smem_u32(sm.kv[slot]), 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t step = (uint64_t)((ks >> 2) * (kTileP * 128 / 16) + (ks & 3) * 2);
+            umma_bf16(tm + b * kTileP, dq + step, dk + step, idS, ks > 0 ? 1u : 0u);
+        }
+    };
+    auto output = [&](int b, int slot, bool first) {
+        const uint64_t dv = umma_sdesc_sw128(smem_u32(sm.kv[slot]), kTileP * 128, 1024);
+#pragma unroll
+        for (int ks = 0; ks < kTileP / 16; ++ks)  // 16 keys: two 8-key atoms of 1024 bytes
+            umma_bf16_ts(tm + 2 * kTileP + b * D, tm + b * kTileP + ks * 8, dv + (uint64_t)(ks * 128), idO,
+                         first && ks == 0 ? 0u : 1u);
+    };
+    const int rounds = rounds_of(total);
+    for (int r = 0; r < rounds; ++r) {
+        Unit u;
+        if (!get_unit(p, r, total, &u)) break;
+        const int nk = u.nk();
+        uint32_t ph;
+        int s = slot_of(0, &ph);
+        bool ok = waitp(&sm.kvfull[s], ph, bd);
+        for (int b = 0; b < 2 && ok; ++b) {
+            if (!u.of(b)) continue;
+            ok = waitp(&sm.qfull[b], qph[b], bd);
+            if (!ok) break;
+            qph[b] ^= 1;
+            tc_fence_after();
+            if (lane == 0) {
+                scores(b, s);
+                umma_commit(&sm.sfull[b]);
+                if (u.of(b) == 1) umma_commit(&sm.qempty[b]);
+            }
+            issued = true;
+        }
+        if (ok && lane == 0) umma_commit(&sm.kvempty[s]);
+        for (int j = 0; j < nk && ok; ++j) {
+            const int vs = slot_of(2 * j + 1, &ph);
+            ok = waitp(&sm.kvfull[vs], ph, bd);
+            if (!ok) break;
+            const int tail = u.len - j * kTileP;  // keys of the sequence in this tile
+            if (tail < kTileP) {
+#pragma unroll
+                for (int x = 0; x < D; x += 64)
+                    for (int i = tail * 128 + lane * 16; i < kTileP * 128; i += 32 * 16)
+                        *reinterpret_cast<uint4 *>(sm.kv[vs] + x * (kTileP * 2) + i) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const int ks = slot_of(2 * j + 2, &ph);
+            bool have_k = false;
+            for (int b = 0; b < 2 && ok; ++b) {
+                if (j >= u.of(b)) continue;
+                if (j == 0) {  // O of this row tile has been read out
+                    ok = waitp(&sm.ofree[b], oph[b] ^ 1, bd);
+                    if (!ok) break;
+                    oph[b] ^= 1;
+                }
+                ok = waitp(&sm.pfull[b], pph[b], bd);
+                if (!ok) break;
+                pph[b] ^= 1;
+                tc_fence_after();
+                if (lane == 0) {
+                    output(b, vs, j == 0);
+                    umma_commit(&sm.pvdone[b]);
+                }
+                if (j + 1 < u.of(b)) {
+                    if (!have_k) {
+                        ok = waitp(&sm.kvfull[ks], ph, bd);
+                        if (!ok) break;
+                        have_k = true;
+                        tc_fence_after();
+                    }
+                    if (lane == 0) {  // over P: the tensor cores take the products in the order of their issue
+                        scores(b, ks);
+                        umma_commit(&sm.sfull[b]);
+                        if (j + 2 == u.of(b)) umma_commit(&sm.qempty[b]);
+                    }
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                umma_commit(&sm.kvempty[vs]);
+                if (have_k) umma_commit(&sm.kvempty[ks]);
+            }
+        }
+        if (!ok) break;
+        slot0 += 2 * nk;
+        phase0 = (phase0 + slot0 / S::kSlots) & 1;
+        slot0 %= S::kSlots;
+    }
+    if (lane == 0 && issued) {  // every product has completed before the tensor memory is freed
+        umma_commit(&sm.drain);
+        drainp(&sm.drain, 0);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax warpgroups
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 32 columns of this thread's lane, without the wait.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Scales this thread's row of O by f (rare).
+template <int D>
+__device__ __noinline__ void rescale_row(uint32_t tO, float f) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(tO + c, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= f;
+        tmem_st32(tO + c, o);
+    }
+}
+
+template <int D>
+__device__ void softmax_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd, int total, uint32_t tm, int warp, int lane) {
+    const int b = warp >> 2, row = (warp & 3) * 32 + lane;  // row tile, row in it
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tm + b * kTileP + lanes, tO = tm + 2 * kTileP + b * D + lanes;
+    const float c2 = p.scale * kLog2e;
+    uint32_t n = 0;  // key tiles this warpgroup has done
+    const int rounds = rounds_of(total);
+    for (int r = 0; r < rounds; ++r) {
+        Unit u;
+        if (!get_unit(p, r, total, &u)) return;
+        const int nk = u.of(b);
+        if (!nk) continue;
+        float m = neg_inf(), l = 0.f;  // reference maximum (base 2, scaled) and sum
+#pragma unroll 1
+        for (int j = 0; j < nk; ++j, ++n) {
+            if (!waitp(&sm.sfull[b], n & 1, bd)) return;
+            tc_fence_after();
+            float s[kTileP];
+#pragma unroll
+            for (int i = 0; i < kTileP; i += 32) tmem_ld32_async(tS + i, s + i);
+            tmem_ld_wait();
+            if (j == nk - 1) {  // the diagonal tile
+#pragma unroll
+                for (int i = 0; i < kTileP; ++i)
+                    if (i > row) s[i] = neg_inf();
+            }
+            float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < kTileP - 4; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[kTileP - 4 + e]);
+            const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+            bool grow = false;
+            float f = 1.f;
+            if (m == neg_inf()) {
+                m = mt;
+            } else if (mt - m > kRescaleLog2P) {
+                f = ex2_approx(m - mt);
+                l *= f;
+                m = mt;
+                grow = true;
+            }
+            if (__any_sync(0xffffffffu, grow)) {  // (a row grows only behind an earlier tile's P V)
+                if (!waitp(&sm.pvdone[b], (n - 1) & 1, bd)) return;
+                tc_fence_after();
+                rescale_row<D>(tO, f);
+            }
+            const float nb = m == neg_inf() ? 0.f : -m;
+            const float2 k2 = make_float2(c2, c2), b2 = make_float2(nb, nb);
+            float2 l4[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pw[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float2 x = ffma2(make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), k2, b2);
+                    const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    l4[i & 3] = h == 0 && i < 4 ? e : fadd2(l4[i & 3], e);
+                    pw[i] = pack_bf16x2(e.x, e.y);
+                }
+                tmem_st32u(tS + 32 * h, pw);
+            }
+            const float2 ls = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+            l += ls.x + ls.y;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.pfull[b]);
+        }
+        // the unit's rows
+        if (!waitp(&sm.pvdone[b], (n - 1) & 1, bd)) return;
+        tc_fence_after();
+        const int i = u.q0 + b * kTileP + row;
+        const bool live = i < u.len;
+        const long long at = ((long long)u.row0 + i) * p.Hq + u.h;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tO + c, o);
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4 *>(p.out + at * D + c + e) =
+                        make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                   pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ofree[b]);
+        if (live && p.lse) p.lse[at] = l > 0.f ? m * 0.6931471805599453f + logf(l) : (l == 0.f ? neg_inf() : l);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsP, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_p[];
+    SmemP<D> &sm = *reinterpret_cast<SmemP<D> *>(smem_p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.qfull[i], 1);
+            mbar_init(&sm.qempty[i], 1);
+            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.pfull[i], 4);
+            mbar_init(&sm.pvdone[i], 1);
+            mbar_init(&sm.ofree[i], 4);
+        }
+        for (int i = 0; i < SmemP<D>::kSlots; ++i) {
+            mbar_init(&sm.kvfull[i], 1);
+            mbar_init(&sm.kvempty[i], 1);
+        }
+        mbar_init(&sm.cexit, kSoftmaxWarps + 1);
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem, kTmemColsP);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;
+    pdl_wait_prerequisites();  // the tiles are the planner's
+    pdl_launch_dependents();
+    const int total = *reinterpret_cast<volatile int *>(&p.hdr->num_tiles) * p.Hq;
+    const BoundsP bd{&sm.abort, &p.hdr->err, p.wait_ns};
+    if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        softmax_role<D>(p, sm, bd, total, tm, warp, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.cexit);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegsP));
+        if (warp == kSoftmaxWarps) {
+            mma_role<D>(p, sm, bd, total, tm, lane);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&sm.cexit);
+        } else if (warp == kSoftmaxWarps + 1 && lane == 0) {
+            load_role<D>(p, sm, bd, total);
+        }
+        __syncwarp();
+    }
+    if (warp == 0) {  // everyone is done with the tensor memory
+        drainp(&sm.cexit, 0);
+        tc_fence_after();
+        tmem_dealloc(tm, kTmemColsP);
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Token rows of `heads` x D bf16, `stride` elements apart.  Tokens behind the last read as zeros.
+cudaError_t token_map(CUtensorMap *m, const uint16_t *base, int n, int heads, int D, long long stride) {
+    static const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(driver_entry("cuTensorMapEncodeTiled", 12000));
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)n};
+    const cuuint64_t step[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, kTileP}, one[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(base), dim, step, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch_t(const PromptParams &p, int grid, cudaLaunchConfig_t &cfg) {
+    static unsigned long long configured[kMaxDevices] = {};  // launch attributes, once per device context
+    int dev = 0;
+    unsigned long long ctx = 0;
+    cudaError_t e = current_device_context(&dev, &ctx);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (ctx == 0 || __atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE) != ctx) {
+        e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SmemP<D>));
+        if (e != cudaSuccess) return e;
+        e = current_device_context(&dev, &ctx);  // (the call above made a context current)
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&configured[dev], ctx, __ATOMIC_RELEASE);
+    }
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreadsP);
+    cfg.dynamicSmemBytes = sizeof(SmemP<D>);
+    return cudaLaunchKernelEx(&cfg, prompt_kernel<D>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs &a, int nsm, cudaStream_t st) {
-    PromptHeader *hdr = reinterpret_cast<PromptHeader *>(a.ws);
+    PromptParams p;
+    cudaError_t e = token_map(&p.q, a.q, a.n, a.Hq, a.D, a.q_stride);
+    if (e == cudaSuccess) e = token_map(&p.k, a.k, a.n, a.Hkv, a.D, a.k_stride);
+    if (e == cudaSuccess) e = token_map(&p.v, a.v, a.n, a.Hkv, a.D, a.v_stride);
+    if (e != cudaSuccess) return e;
+    p.hdr = reinterpret_cast<PromptHeader *>(a.ws);
     PromptTile *tiles = reinterpret_cast<PromptTile *>(a.ws + sizeof(PromptHeader));
+    p.tiles = tiles;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.Hq = a.Hq;
+    p.G = a.Hq / a.Hkv;
+    p.scale = a.scale;
+    p.wait_ns = a.wait_ns;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -137,13 +592,12 @@ cudaError_t launch_prompt(const PromptArgs &a, int nsm, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_plan, a.seq_off, a.B, a.n, a.max_len,
-                                       (int)prompt_max_tiles(a.B, a.n), hdr, tiles);
+    const int room = (int)prompt_max_tiles(a.B, a.n);
+    e = cudaLaunchKernelEx(&cfg, prompt_plan, a.seq_off, a.B, a.n, a.max_len, room, p.hdr, tiles);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(nsm * 8);
-    cfg.blockDim = dim3(256);
-    return a.D == 128 ? cudaLaunchKernelEx(&cfg, prompt_kernel<128>, a, (const PromptHeader *)hdr, (const PromptTile *)tiles)
-                      : cudaLaunchKernelEx(&cfg, prompt_kernel<64>, a, (const PromptHeader *)hdr, (const PromptTile *)tiles);
+    const long long units = (long long)room * a.Hq;
+    const int grid = (int)(units < nsm ? units : nsm);
+    return a.D == 128 ? launch_t<128>(p, grid, cfg) : launch_t<64>(p, grid, cfg);
 }
 
 }  // namespace pillar
