@@ -624,11 +624,12 @@ PILLAR_API int pillar_block_map(const pillar_shape_t *shape, const int32_t *req_
  * position req_len[b] - n_b + i.  For the new rows x of one (block, KV head),
  * a = max |x| and e the smallest integer >= -126 with a <= 448 * 2^e:
  *   scale' = 2^e when row 0 of the block is among them, else max(scale, 2^e)
- *   codes  = x / scale' rounded to the nearest e4m3 (ties to even); the block's
- *            earlier rows become code * scale / scale' rounded the same way
- * Rows of the block behind the last new one are left as they were, and a
- * block without new rows is not touched.  A call with the same new rows again
- * leaves what the first one did.  A block that gets new rows must belong to one
+ *   codes  = x / scale' rounded to the nearest e4m3 (ties to even); where the
+ *            block holds earlier rows and its scale grew, all of its other rows
+ *            become code * scale / scale' rounded the same way
+ * Otherwise the other rows of the block are left as they were, and a block
+ * without new rows is not touched.  A call with the same new rows again leaves
+ * what the first one did.  A block that gets new rows must belong to one
  * request only.
  *
  *   k_new, v_new  bf16, row i at i * k_stride (v_stride) elements: [Hkv, D] each,

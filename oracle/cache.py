@@ -128,8 +128,8 @@ def kv8_append(codes, scale, new, req_len, new_off, table):
                 r = lo % BLOCK
                 if r:
                     s = max(s, scale[blk, h])
-                    if s > scale[blk, h]:
-                        codes[blk, h, :r] = e4m3_encode(e4m3_decode(codes[blk, h, :r]) * (scale[blk, h] / s))
+                    if s > scale[blk, h]:  # the block's other rows under the larger scale
+                        codes[blk, h] = e4m3_encode(e4m3_decode(codes[blk, h]) * (scale[blk, h] / s))
                 codes[blk, h, r:r + hi - lo] = e4m3_encode(x / s)
                 scale[blk, h] = s
     return codes, scale

@@ -6,11 +6,12 @@
 //     e      = the smallest integer >= -126 with a <= 448 * 2^e
 //     scale' = 2^e                    when the block's first row is among them
 //            = max(scale, 2^e)        when it holds earlier rows
-//     code   = rne_e4m3(x / scale'),  earlier rows: rne_e4m3(code * scale / scale')
+//     code   = rne_e4m3(x / scale'),  and where the scale grew, the block's other rows:
+//              rne_e4m3(code * scale / scale')
 // The scale is a power of two: e4m3 is a floating-point format, so a tighter
 // scale would gain at most one of its eighteen binades and no precision, while
 // with a power of two the division is exact, each value is rounded once, and
-// rounding earlier rows again changes only those that leave the normal range.
+// rounding other rows again changes only values that leave the normal range.
 //
 // One warp per (block with new rows, head, K or V): the block's new rows are
 // at most 16 x 256 bytes, held in registers as one load of 16 bytes per lane
@@ -122,9 +123,11 @@ __device__ void append_block(const Kv8AppendArgs &a, const Owner &o, int h, bool
         const float old = good ? before : 0.f;
         if (old >= s) {
             s = old;
-        } else {  // the earlier rows under the larger scale
+        } else {  // the block's other rows under the larger scale
             const float ratio = old / s;
-            for (int i = lane * 16; i < o.row * D; i += 32 * 16) {
+            for (int i = lane * 16; i < kBlock * D; i += 32 * 16) {
+                const int r = i / D;
+                if (r >= o.row && r < o.row + o.rows) continue;
                 uint4 w = *reinterpret_cast<const uint4 *>(dst + i);
                 uint32_t *u = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
