@@ -378,57 +378,69 @@ def pillar_kv_reload(shape, host_k, host_v, slots, k_pool, v_pool, device_flags=
 # --------------------------------------------------------------- cache blocks
 
 class _Types:
-    """Element types the calls below take, by name (torch is imported on the first call)."""
+    """Element types the calls below take, and torch's accessors of the current device and stream (torch is imported on
+    the first use; the raw accessors cost a tenth of the objects')."""
 
     def __getattr__(self, name):
         import torch
         self.i32, self.i64, self.f32 = (torch.int32,), (torch.int64,), (torch.float32,)
         self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 bits travel in 16-bit integers too
         self.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+        torch.cuda.init()
+        self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         return self.__dict__[name]
 
 
 _T = _Types()
 
 
-def _current_device():
-    import torch
-    return torch.cuda.current_device()
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _T.stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _layout(name, x, dtypes, shape, dev):
+def _misfit(name, x, dtypes, shape, dev):
     if x.dtype not in dtypes:
         raise ValueError(f"{name}: {x.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if len(x.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, x.shape)):
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
-    if not x.is_cuda or x.device.index != dev:
-        raise ValueError(f"{name}: on {x.device}, expected the current CUDA device")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if not x.is_cuda or x.get_device() != dev:
+        raise ValueError(f"{name}: on {x.device}, expected the current CUDA device ({dev})")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _arg(name, x, dtypes, shape, dev):
-    """Pointer of a CUDA tensor whose element type, shape (None: any extent), layout and device are as given: these calls
-    index their arrays by the sizes of other ones, so a tensor that does not fit is refused here."""
-    _layout(name, x, dtypes, shape, dev)
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return x.data_ptr()
+    """Pointer of a CUDA tensor whose element type, shape, layout and device are as given: these calls index their arrays by
+    the sizes of other ones, so a tensor that does not fit is refused here."""
+    if x.dtype in dtypes and x.shape == shape and x.get_device() == dev and x.is_contiguous():
+        return x.data_ptr()
+    _misfit(name, x, dtypes, shape, dev)
 
 
-def _rows(name, x, heads, D, dev, rows=None):
+def _dim(name, x, i, ndim):
+    """Extent i of a tensor whose extents the call goes by."""
+    if x.ndim != ndim:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {ndim} dimensions")
+    return x.shape[i]
+
+
+def _rows(name, x, rows, heads, D, dev):
     """Pointer and token stride of [rows, heads, D] bf16 whose tokens may lie apart (a slice of a fused projection)."""
-    _layout(name, x, _T.bf16, (rows, heads, D), dev)
-    st = x.stride()
-    if x.numel() == 0:
+    if x.dtype not in _T.bf16 or x.shape != (rows, heads, D) or x.get_device() != dev:
+        _misfit(name, x, _T.bf16, (rows, heads, D), dev)
+    if x.is_contiguous():
         return x.data_ptr(), 0
-    if st[2] != 1 or (heads > 1 and st[1] != D) or (x.shape[0] > 1 and st[0] < heads * D):
+    st = x.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != D) or (rows > 1 and st[0] < heads * D):
         raise ValueError(f"{name}: strides {st}, expected each token's {heads} x {D} values to be contiguous")
-    return x.data_ptr(), st[0] if x.shape[0] > 1 else 0
+    return x.data_ptr(), st[0] if rows > 1 else 0
 
 
 def _workspace(x, dev):
-    if not x.is_cuda or x.device.index != dev or not x.is_contiguous():
+    if x.get_device() != dev or not x.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on the current CUDA device")
-    return x.data_ptr(), x.numel() * x.element_size()
+    return x.data_ptr(), x.nbytes
 
 
 def pillar_block_map_workspace_bytes(shape: PillarShape) -> int:
@@ -443,16 +455,18 @@ def pillar_block_map(shape, req_len, prev_len, block_table, free_ring, free_stat
                      new_off, new_slots, workspace, stream=None):
     """Blocks for a batch whose lengths go from prev_len to req_len: takes them from and gives them back to the free
     ring, and writes the block table's new entries, the slot table and the new tokens' slots."""
-    dev, B = _current_device(), shape.B
+    dev, B = _T.device(), shape.B
     ws, ws_bytes = _workspace(workspace, dev)
+    width, slots, new = (_dim("block_table", block_table, 1, 2), _dim("slot_table", slot_table, 0, 1),
+                         _dim("new_slots", new_slots, 0, 1))
     st = load().pillar_block_map(
         ctypes.byref(shape), _arg("req_len", req_len, _T.i32, (B,), dev), _arg("prev_len", prev_len, _T.i32, (B,), dev),
-        _arg("block_table", block_table, _T.i32, (B, None), dev), block_table.shape[1],
+        _arg("block_table", block_table, _T.i32, (B, width), dev), width,
         _arg("free_ring", free_ring, _T.i32, (shape.num_slots // KV_BLOCK,), dev),
         _arg("free_state", free_state, _T.i32, (2,), dev), _arg("granted_len", granted_len, _T.i32, (B,), dev),
-        _arg("kv_off", kv_off, _T.i64, (B + 1,), dev), _arg("slot_table", slot_table, _T.i32, (None,), dev),
-        slot_table.numel(), _arg("new_off", new_off, _T.i32, (B + 1,), dev),
-        _arg("new_slots", new_slots, _T.i32, (None,), dev), new_slots.numel(), ws, ws_bytes, _stream(stream))
+        _arg("kv_off", kv_off, _T.i64, (B + 1,), dev), _arg("slot_table", slot_table, _T.i32, (slots,), dev), slots,
+        _arg("new_off", new_off, _T.i32, (B + 1,), dev),
+        _arg("new_slots", new_slots, _T.i32, (new,), dev), new, ws, ws_bytes, _raw_stream(stream, dev))
     if st:
         raise PillarError("pillar_block_map", st)
 
@@ -468,41 +482,46 @@ def pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_poo
                       device_flags=None, stream=None):
     """The new tokens' K/V rows ([n, Hkv, D] bf16, tokens may lie apart) as e4m3 codes under the scales of their blocks;
     request b's rows new_off[b] .. new_off[b+1]-1 are its last positions."""
-    dev, B = _current_device(), shape.B
-    kp, ks = _rows("k_new", k_new, shape.Hkv, shape.D, dev)
-    vp, vs = _rows("v_new", v_new, shape.Hkv, shape.D, dev, k_new.shape[0])
+    dev, B = _T.device(), shape.B
+    n, width = _dim("k_new", k_new, 0, 3), _dim("block_table", block_table, 1, 2)
+    kp, ks = _rows("k_new", k_new, n, shape.Hkv, shape.D, dev)
+    vp, vs = _rows("v_new", v_new, n, shape.Hkv, shape.D, dev)
     st = load().pillar_kv8_append(
-        ctypes.byref(shape), kp, ks, vp, vs, k_new.shape[0], _arg("req_len", req_len, _T.i32, (B,), dev),
-        _arg("new_off", new_off, _T.i32, (B + 1,), dev), _arg("block_table", block_table, _T.i32, (B, None), dev),
-        block_table.shape[1], *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
-        None if device_flags is None else _arg("device_flags", device_flags, _T.i32, (1,), dev), _stream(stream))
+        ctypes.byref(shape), kp, ks, vp, vs, n, _arg("req_len", req_len, _T.i32, (B,), dev),
+        _arg("new_off", new_off, _T.i32, (B + 1,), dev), _arg("block_table", block_table, _T.i32, (B, width), dev),
+        width, *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
+        None if device_flags is None else _arg("device_flags", device_flags, _T.i32, (1,), dev),
+        _raw_stream(stream, dev))
     if st:
         raise PillarError("pillar_kv8_append", st)
 
 
 def _kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev):
-    return (_arg("q", q, _T.bf16, (None, shape.Hq, shape.D), dev),
+    width = _dim("block_table", block_table, 1, 2)
+    return (_arg("q", q, _T.bf16, (_dim("q", q, 0, 3), shape.Hq, shape.D), dev),
             *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
-            _arg("block_table", block_table, _T.i32, (shape.B, None), dev), block_table.shape[1])
+            _arg("block_table", block_table, _T.i32, (shape.B, width), dev), width)
 
 
 def _kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev):
-    return (_arg("out", out, _T.bf16, tuple(q.shape), dev),
-            None if verify_logits is None else _arg("verify_logits", verify_logits, _T.f32, (None,), dev),
-            _arg("verify_lse", verify_lse, _T.f32, (None, shape.Hq, shape.k + 1), dev), *_workspace(workspace, dev))
+    return (_arg("out", out, _T.bf16, q.shape, dev),
+            None if verify_logits is None else
+            _arg("verify_logits", verify_logits, _T.f32, (_dim("verify_logits", verify_logits, 0, 1),), dev),
+            _arg("verify_lse", verify_lse, _T.f32, (_dim("verify_lse", verify_lse, 0, 3), shape.Hq, shape.k + 1), dev),
+            *_workspace(workspace, dev))
 
 
 def pillar_attn_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, req_mode, req_len, sparse_idx, sparse_cnt,
                     out, verify_logits, verify_lse, workspace, stream=None):
     """The unified draft/verify step over the 8-bit cache; verify_logits None: no dump.  (The sizes of q, out, the logits
     and the LSEs follow from modes and lengths that only the device knows, as in pillar_attn_unified.)"""
-    dev, B = _current_device(), shape.B
+    dev, B = _T.device(), shape.B
     st = load().pillar_attn_kv8(
         ctypes.byref(shape), *_kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev),
         _arg("req_mode", req_mode, _T.i32, (B,), dev), _arg("req_len", req_len, _T.i32, (B,), dev),
         _arg("sparse_idx", sparse_idx, _T.i32, (B, shape.Hkv, shape.max_sparse), dev),
         _arg("sparse_cnt", sparse_cnt, _T.i32, (B, shape.Hkv), dev),
-        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _stream(stream))
+        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _raw_stream(stream, dev))
     if st:
         raise PillarError("pillar_attn_kv8", st)
 
@@ -510,11 +529,11 @@ def pillar_attn_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, r
 def pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
                         verify_lse, workspace, stream=None):
     """pillar_attn_kv8 on the plan that pillar_attn_plan left in the workspace."""
-    dev = _current_device()
+    dev = _T.device()
     st = load().pillar_attn_run_kv8(
         ctypes.byref(shape), *_kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev),
         _arg("sparse_idx", sparse_idx, _T.i32, (shape.B, shape.Hkv, shape.max_sparse), dev),
-        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _stream(stream))
+        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _raw_stream(stream, dev))
     if st:
         raise PillarError("pillar_attn_run_kv8", st)
 
@@ -532,15 +551,15 @@ def pillar_prompt_attn_workspace_bytes(shape: PillarShape, n: int) -> int:
 def pillar_prompt_attn(shape, q, k, v, seq_off, out, lse, workspace, stream=None):
     """Causal attention over prompts packed one after another ([n, heads, D] bf16; tokens may lie apart); lse [n, Hq] fp32
     or None."""
-    dev, n = _current_device(), q.shape[0]
-    qp, qs = _rows("q", q, shape.Hq, shape.D, dev)
-    kp, ks = _rows("k", k, shape.Hkv, shape.D, dev, n)
-    vp, vs = _rows("v", v, shape.Hkv, shape.D, dev, n)
+    dev, n = _T.device(), _dim("q", q, 0, 3)
+    qp, qs = _rows("q", q, n, shape.Hq, shape.D, dev)
+    kp, ks = _rows("k", k, n, shape.Hkv, shape.D, dev)
+    vp, vs = _rows("v", v, n, shape.Hkv, shape.D, dev)
     st = load().pillar_prompt_attn(
         ctypes.byref(shape), qp, qs, kp, ks, vp, vs, n, _arg("seq_off", seq_off, _T.i32, (shape.B + 1,), dev),
         _arg("out", out, _T.bf16, (n, shape.Hq, shape.D), dev),
         None if lse is None else _arg("lse", lse, _T.f32, (n, shape.Hq), dev), *_workspace(workspace, dev),
-        _stream(stream))
+        _raw_stream(stream, dev))
     if st:
         raise PillarError("pillar_prompt_attn", st)
 

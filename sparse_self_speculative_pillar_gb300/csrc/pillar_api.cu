@@ -75,13 +75,16 @@ int check_shape(const pillar_shape_t *s) {
     // section holds, per work item, (k+1)*G partial rows of D fp32 values (+ LSE), and a
     // (request, KV head) has at most max(max_len / verify chunk, max_sparse / draft chunk) + 1
     // items.  Shapes whose bound passes 2^50 bytes are refused rather than wrapped.
-    const long double vc = s->verify_chunk > 0 ? s->verify_chunk : kTileKeys;
-    const long double dc = s->draft_chunk > 0 ? s->draft_chunk : kTileKeys;
-    const long double per_unit = std::max((long double)s->max_len / vc, (long double)s->max_sparse / dc) + 2.0L;
-    const long double rows = (long double)(s->k + 1) * G;
-    const long double bound = (long double)s->B * s->Hkv * per_unit * (rows * (s->D + 1) * 4.0L + 64.0L) +
-                              (long double)s->B * 64.0L + 65536.0L;
-    if (bound > 1125899906842624.0L) return PILLAR_ERR_ARG;  // 2^50
+    const auto bound = [s, G](auto one) {
+        using F = decltype(one);
+        const F vc = s->verify_chunk > 0 ? s->verify_chunk : kTileKeys;
+        const F dc = s->draft_chunk > 0 ? s->draft_chunk : kTileKeys;
+        const F per_unit = std::max((F)s->max_len / vc, (F)s->max_sparse / dc) + 2;
+        const F rows = (F)(s->k + 1) * G;
+        return (F)s->B * s->Hkv * per_unit * (rows * (s->D + 1) * 4 + 64) + (F)s->B * 64 + 65536;
+    };
+    // (in double first: long double is emulated on some hosts, microseconds a call)
+    if (bound(1.0) > 562949953421312.0 && bound(1.0L) > 1125899906842624.0L) return PILLAR_ERR_ARG;  // 2^49, 2^50
     return PILLAR_OK;
 }
 
@@ -527,15 +530,8 @@ static int attn_kv8_checks(const pillar_shape_t *shape, const uint16_t *q, const
     return PILLAR_OK;
 }
 
-int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool, const uint8_t *v8_pool,
-                        const float *k_scale, const float *v_scale, const int32_t *block_table, int32_t max_blocks,
-                        const int32_t *sparse_idx, uint16_t *out, float *verify_logits, float *verify_lse,
-                        void *workspace, size_t ws_bytes, void *stream) {
-    Kv8Cache c{k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, 0};
-    const int st = attn_kv8_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
-    if (st != PILLAR_OK) return st;
-    const pillar_shape_t &s = *shape;
-    if (s.B == 0) return PILLAR_OK;
+static int run_kv8(const pillar_shape_t &s, const uint16_t *q, Kv8Cache c, const int32_t *sparse_idx, uint16_t *out,
+                   float *verify_logits, float *verify_lse, void *workspace, void *stream) {
     c.num_blocks = pool_blocks(s);
     const int nsm = sm_count();
     if (nsm <= 0) return PILLAR_ERR_CUDA;
@@ -555,8 +551,17 @@ int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const ui
     aa.max_sparse = s.max_sparse;
     aa.schedule = s.schedule;
     aa.scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / std::sqrt((float)s.D);
-    aa.wait_ns = s.wait_timeout_us > 0 ? (unsigned long long)s.wait_timeout_us * 1000ull : kWaitTimeoutNs;
     return launch_attn_kv8(aa, c, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool, const uint8_t *v8_pool,
+                        const float *k_scale, const float *v_scale, const int32_t *block_table, int32_t max_blocks,
+                        const int32_t *sparse_idx, uint16_t *out, float *verify_logits, float *verify_lse,
+                        void *workspace, size_t ws_bytes, void *stream) {
+    const Kv8Cache c{k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, 0};
+    const int st = attn_kv8_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
+    if (st != PILLAR_OK || shape->B == 0) return st;
+    return run_kv8(*shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, stream);
 }
 
 int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool, const uint8_t *v8_pool,
@@ -569,9 +574,8 @@ int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_
     const int st = attn_kv8_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
     if (st != PILLAR_OK) return st;
     const int sp = pillar_attn_plan(shape, req_mode, req_len, sparse_cnt, workspace, ws_bytes, stream);
-    if (sp != PILLAR_OK) return sp;
-    return pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, max_blocks, sparse_idx, out,
-                               verify_logits, verify_lse, workspace, ws_bytes, stream);
+    if (sp != PILLAR_OK || shape->B == 0) return sp;
+    return run_kv8(*shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, stream);
 }
 
 int pillar_prompt_attn_workspace_bytes(const pillar_shape_t *shape, int32_t n, size_t *bytes) {
