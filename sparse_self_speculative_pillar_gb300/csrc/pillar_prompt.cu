@@ -4,11 +4,12 @@
 //   out[i, h] = sum_{j <= i} softmax_j(scale q_ih . k_j,h/G) v_j,h/G   (j in i's sequence)
 //   lse[i, h] = log sum_{j <= i} e^(scale q_ih . k_j,h/G)
 //
-// A planner lists the sequences' 256-row tiles, those with the most keys first.
-// The attention kernel is persistent, one CTA per SM; CTA c takes units (tile,
-// head) c, 2 G - 1 - c, 2 G + c, ... of the G CTAs' rounds, so that the rounds'
-// slopes cancel.  A unit is two tiles of 128 query rows against the 128-key tiles
-// up to the diagonal:
+// A planner lists the sequences' row tiles, those with the most keys first.  The
+// attention kernel is persistent, one CTA per SM; CTA c takes units c, 2 G - 1 - c,
+// 2 G + c, ... of the G CTAs' rounds, so that the rounds' slopes cancel.  A unit is
+// two tiles of 128 query rows against the 128-key tiles up to the diagonal: the same
+// rows for two heads that share a KV head, or, when a group has an odd number of
+// heads, 256 consecutive rows of one:
 //   * a load thread brings Q, K and V tiles by TMA (128-byte swizzle; K and V through
 //     one ring, in the order in which they are used);
 //   * an MMA warp issues S_b = Q_b K^T (128 x 128, tcgen05, both operands in shared
@@ -18,7 +19,9 @@
 //   * two warpgroups, one per row tile, a row per thread: the whole row of scores
 //     in registers, its maximum, exponentials and sum without a shuffle, and
 //     bf16 probabilities back to tensor memory.  O is rescaled only when a row's
-//     maximum grew by more than 2^8.  At a unit's end they normalise and write O.
+//     maximum grew by more than 2^8.  At a unit's end they normalise O and write it
+//     through a 4 KB buffer a warp, so that eight lanes store 128 bytes of a row (each
+//     lane storing its own row, 16 bytes at a time, took 3000 to 4400 cycles a unit).
 // What bounds it: the tensor cores (4 D flops a visible pair; half of the diagonal
 // tile is computed and masked).  Keys behind a sequence's end lie in the next one:
 // their scores are behind the diagonal for every row that counts, and their values
@@ -36,8 +39,8 @@ constexpr int kPlanThreadsP = 1024;
 constexpr int kLevels = 1024;  // bins of the longest-first order
 
 // Lists the tiles, those with the most keys first.
-__global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off, int B, int n, int max_len, int room, PromptHeader *hdr,
-                                                             PromptTile *tiles) {
+__global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off, int B, int n, int max_len, int rows, int room,
+                                                             PromptHeader *hdr, PromptTile *tiles) {
     __shared__ int s_bin[kLevels];
     __shared__ int s_warp[32];
     __shared__ int s_bad;
@@ -48,7 +51,7 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
     if (tid == 0) s_bad = 0;
     __syncthreads();
     // bin of tile i of a sequence: larger i first
-    const int most = (max_len + kPromptRows - 1) / kPromptRows;
+    const int most = (max_len + rows - 1) / rows;
     int shift = 0;
     while ((most >> shift) >= kLevels) ++shift;
     auto level = [&](int i) { return kLevels - 1 - (i >> shift); };
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
         }
         *first = lo;
         *len = hi - lo;
-        return (hi - lo + kPromptRows - 1) / kPromptRows;
+        return (hi - lo + rows - 1) / rows;
     };
     int first = 0, len = 0;
     for (int b = wid; b < B; b += 32) {
@@ -102,7 +105,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreadsP = (kSoftmaxWarps + 4) * 32;  // and the MMA warp, the load warp, two idle ones
 constexpr uint32_t kSoftmaxRegs = 208, kOtherRegsP = 80;
 static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegsP <= kThreadsP * 168, "registers of the launch");
-constexpr int kTileP = 128;  // query rows of a row tile, keys of a key tile
+constexpr int kTileP = kPromptRows;  // query rows of a row tile, keys of a key tile
 constexpr uint32_t kTmemColsP = 512;
 constexpr float kRescaleLog2P = 8.f;
 
@@ -113,6 +116,8 @@ struct PromptParams {
     PromptHeader *hdr;
     const PromptTile *tiles;
     int Hq, G;
+    int rows;       // of a planned tile
+    int per_tile;   // units of a planned tile: Hq / 2 pairs of heads, or Hq heads
     float scale;
     unsigned long long wait_ns;
 };
@@ -120,9 +125,10 @@ struct PromptParams {
 template <int D>
 struct SmemP {
     static constexpr int kTileBytes = kTileP * D * 2;
-    static constexpr int kSlots = D == 128 ? 5 : 8;  // K and V tiles in shared memory
+    static constexpr int kSlots = D == 128 ? 4 : 6;  // K and V tiles in shared memory (three: 6 % slower on long prompts)
     alignas(1024) uint8_t q[2][kTileBytes];
     uint8_t kv[kSlots][kTileBytes];
+    uint8_t out[kSoftmaxWarps][32 * 128];  // 32 rows of 64 columns, on their way to memory
     uint64_t qfull[2], qempty[2], kvfull[kSlots], kvempty[kSlots];
     uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], cexit, drain;
     uint32_t tmem;
@@ -155,25 +161,34 @@ __device__ __forceinline__ void tma_load3(void *dst, const void *map, int x, int
         : "memory");
 }
 
-// A unit of a CTA.
+// A unit of a CTA: row tiles 0 and 1.
 struct Unit {
-    int row0, len, q0, h;  // the sequence's first row and length, the unit's first row in it, the query head
-    int na, nb;            // key tiles of the row tiles (nb 0: there is no second one)
-    __device__ __forceinline__ int nk() const { return nb ? nb : na; }
+    int row0, len;  // the sequence's first row and length
+    int q0, h;      // first row (in the sequence) and head of row tile 0
+    int dq, dh;     // what row tile 1 adds to them
+    int na, nb;     // key tiles of the row tiles (nb 0: there is no second one)
+    __device__ __forceinline__ int nk() const { return max(na, nb); }
     __device__ __forceinline__ int of(int b) const { return b ? nb : na; }
 };
 __device__ __forceinline__ bool get_unit(const PromptParams &p, int round, int total, Unit *u) {
     const int c = blockIdx.x, G = gridDim.x;
     const long long r = (long long)round * G + ((round & 1) ? G - 1 - c : c);
     if (r >= total) return false;
-    const int t = (int)(r / p.Hq);
-    const PromptTile x = p.tiles[t];
-    u->row0 = x.row0;
-    u->len = x.len;
-    u->q0 = x.tile * kPromptRows;
-    u->h = (int)(r - (long long)t * p.Hq);
-    u->na = 2 * x.tile + 1;
-    u->nb = u->q0 + kTileP < x.len ? u->na + 1 : 0;
+    const int t = (int)(r / p.per_tile), x = (int)(r - (long long)t * p.per_tile);
+    const PromptTile y = p.tiles[t];
+    u->row0 = y.row0;
+    u->len = y.len;
+    u->q0 = y.tile * p.rows;
+    u->na = u->q0 / kTileP + 1;
+    if (p.rows == kTileP) {
+        u->h = 2 * x;
+        u->dq = 0, u->dh = 1;
+        u->nb = u->na;
+    } else {
+        u->h = x;
+        u->dq = kTileP, u->dh = 0;
+        u->nb = u->q0 + kTileP < y.len ? u->na + 1 : 0;
+    }
     return true;
 }
 // (only the last round can be incomplete)
@@ -203,7 +218,7 @@ __device__ void load_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd
     auto query = [&](const Unit &u, int b) {
         ok = waitp(&sm.qempty[b], qph[b] ^ 1, bd);
         if (!ok) return;
-        tile(sm.q[b], &p.q, u.h, u.row0 + u.q0 + b * kTileP, &sm.qfull[b]);
+        tile(sm.q[b], &p.q, u.h + b * u.dh, u.row0 + u.q0 + b * u.dq, &sm.qfull[b]);
         qissued |= 1u << b;
         qparity = (qparity & ~(1u << b)) | (qph[b] << b);
         qph[b] ^= 1;
@@ -458,26 +473,37 @@ __device__ void softmax_role(const PromptParams &p, SmemP<D> &sm, const BoundsP 
         // the unit's rows
         if (!waitp(&sm.pvdone[b], (n - 1) & 1, bd)) return;
         tc_fence_after();
-        const int i = u.q0 + b * kTileP + row;
-        const bool live = i < u.len;
-        const long long at = ((long long)u.row0 + i) * p.Hq + u.h;
+        const int i0 = u.q0 + b * u.dq + (warp & 3) * 32, left = u.len - i0;  // this warp's first row; rows from there on
+        const int h = u.h + b * u.dh;
+        const long long at = ((long long)u.row0 + i0) * p.Hq + h;
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint8_t *buf = sm.out[warp];
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(tO + c, o);
-            if (live) {
+        for (int x = 0; x < D; x += 64) {
+            float o[64];
+            tmem_ld32_async(tO + x, o);
+            tmem_ld32_async(tO + x + 32, o + 32);
+            tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4 *>(p.out + at * D + c + e) =
-                        make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
-                                   pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+            for (int e = 0; e < 8; ++e)  // 16-byte pieces, XOR-ed with the row: no bank twice, either way
+                *reinterpret_cast<uint4 *>(buf + lane * 128 + ((e ^ (lane & 7)) * 16)) =
+                    make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                               pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                               pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int rr = 4 * q + (lane >> 3), ch = lane & 7;
+                const uint4 v = *reinterpret_cast<const uint4 *>(buf + rr * 128 + ((ch ^ (rr & 7)) * 16));
+                if (rr < left) *reinterpret_cast<uint4 *>(p.out + (at + (long long)rr * p.Hq) * D + x + ch * 8) = v;
             }
+            __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.ofree[b]);
-        if (live && p.lse) p.lse[at] = l > 0.f ? m * 0.6931471805599453f + logf(l) : (l == 0.f ? neg_inf() : l);
+        if (lane < left && p.lse)
+            p.lse[at + (long long)lane * p.Hq] = l > 0.f ? m * 0.6931471805599453f + logf(l) : (l == 0.f ? neg_inf() : l);
     }
 }
 
@@ -511,7 +537,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prompt_kernel(const __grid_const
     const uint32_t tm = sm.tmem;
     pdl_wait_prerequisites();  // the tiles are the planner's
     pdl_launch_dependents();
-    const int total = *reinterpret_cast<volatile int *>(&p.hdr->num_tiles) * p.Hq;
+    const int total = *reinterpret_cast<volatile int *>(&p.hdr->num_tiles) * p.per_tile;
     const BoundsP bd{&sm.abort, &p.hdr->err, p.wait_ns};
     if (warp < kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -590,6 +616,8 @@ cudaError_t launch_prompt(const PromptArgs &a, int nsm, cudaStream_t st) {
     p.lse = a.lse;
     p.Hq = a.Hq;
     p.G = a.Hq / a.Hkv;
+    p.rows = prompt_tile_rows(p.G);
+    p.per_tile = p.rows == kTileP ? a.Hq / 2 : a.Hq;
     p.scale = a.scale;
     p.wait_ns = a.wait_ns;
     cudaLaunchAttribute attr[1];
@@ -602,9 +630,9 @@ cudaError_t launch_prompt(const PromptArgs &a, int nsm, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int room = (int)prompt_max_tiles(a.B, a.n);
-    e = cudaLaunchKernelEx(&cfg, prompt_plan, a.seq_off, a.B, a.n, a.max_len, room, p.hdr, tiles);
+    e = cudaLaunchKernelEx(&cfg, prompt_plan, a.seq_off, a.B, a.n, a.max_len, p.rows, room, p.hdr, tiles);
     if (e != cudaSuccess) return e;
-    const long long units = (long long)room * a.Hq;
+    const long long units = (long long)room * p.per_tile;
     const int grid = (int)(units < nsm ? units : nsm);
     return a.D == 128 ? launch_t<128>(p, grid, cfg) : launch_t<64>(p, grid, cfg);
 }

@@ -7,7 +7,7 @@
 
 namespace pillar {
 
-constexpr int kPromptRows = 256;  // query rows of a unit: two tiles of 128
+constexpr int kPromptRows = 128;  // query rows of a row tile
 
 struct PromptHeader {
     int err;        // PILLAR_FLAG_* bits
@@ -16,13 +16,15 @@ struct PromptHeader {
 };
 static_assert(sizeof(PromptHeader) == 256, "header size");
 
-// 256 consecutive query rows of one sequence.
+// `rows` consecutive query rows of one sequence: one row tile, taken for two heads of a KV group at once, or
+// two row tiles of one head when the groups have no pairs.
 struct PromptTile {
     int row0;  // the sequence's first row
     int len;   // its length
-    int tile;  // rows 256 tile .. 256 tile + 255 of it
+    int tile;  // rows rows * tile .. rows * (tile + 1) - 1 of it
     int pad;
 };
+inline int prompt_tile_rows(int G) { return G % 2 == 0 ? kPromptRows : 2 * kPromptRows; }
 
 inline long long prompt_max_tiles(int B, int n) { return (long long)n / kPromptRows + B; }
 inline size_t prompt_ws_bytes(int B, int n) {
