@@ -170,29 +170,39 @@ struct Unit {
     __device__ __forceinline__ int nk() const { return max(na, nb); }
     __device__ __forceinline__ int of(int b) const { return b ? nb : na; }
 };
-__device__ __forceinline__ bool get_unit(const PromptParams &p, int round, int total, Unit *u) {
-    const int c = blockIdx.x, G = gridDim.x;
-    const long long r = (long long)round * G + ((round & 1) ? G - 1 - c : c);
-    if (r >= total) return false;
-    const int t = (int)(r / p.per_tile), x = (int)(r - (long long)t * p.per_tile);
-    const PromptTile y = p.tiles[t];
-    u->row0 = y.row0;
-    u->len = y.len;
-    u->q0 = y.tile * p.rows;
-    u->na = u->q0 / kTileP + 1;
-    if (p.rows == kTileP) {
-        u->h = 2 * x;
-        u->dq = 0, u->dh = 1;
-        u->nb = u->na;
-    } else {
-        u->h = x;
-        u->dq = kTileP, u->dh = 0;
-        u->nb = u->q0 + kTileP < y.len ? u->na + 1 : 0;
+// The units of a CTA in order; the record of the one after the next loads while the next is worked on.
+struct Units {
+    const PromptParams &p;
+    int total, round, t, x;  // units in all; the round, tile and place in the tile of `ahead`
+    PromptTile ahead;
+    __device__ __forceinline__ Units(const PromptParams &q, int n) : p(q), total(n), round(-1), t(-1) { fetch(); }
+    __device__ __forceinline__ void fetch() {
+        ++round;
+        const int c = blockIdx.x, G = gridDim.x;
+        const long long r = (long long)round * G + ((round & 1) ? G - 1 - c : c);
+        t = r < total ? (int)(r / p.per_tile) : -1;  // (only the last round can be incomplete)
+        x = (int)(r - (long long)t * p.per_tile);
+        if (t >= 0) ahead = p.tiles[t];
     }
-    return true;
-}
-// (only the last round can be incomplete)
-__device__ __forceinline__ int rounds_of(int total) { return (total + gridDim.x - 1) / gridDim.x; }
+    __device__ __forceinline__ bool next(Unit *u) {
+        if (t < 0) return false;
+        u->row0 = ahead.row0;
+        u->len = ahead.len;
+        u->q0 = ahead.tile * p.rows;
+        u->na = u->q0 / kTileP + 1;
+        if (p.rows == kTileP) {
+            u->h = 2 * x;
+            u->dq = 0, u->dh = 1;
+            u->nb = u->na;
+        } else {
+            u->h = x;
+            u->dq = kTileP, u->dh = 0;
+            u->nb = u->q0 + kTileP < ahead.len ? u->na + 1 : 0;
+        }
+        fetch();
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------ load thread
 
@@ -223,10 +233,8 @@ __device__ void load_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd
         qparity = (qparity & ~(1u << b)) | (qph[b] << b);
         qph[b] ^= 1;
     };
-    const int rounds = rounds_of(total);
-    for (int r = 0; r < rounds && ok; ++r) {
-        Unit u;
-        if (!get_unit(p, r, total, &u)) break;
+    Units units(p, total);
+    for (Unit u; ok && units.next(&u);) {
         query(u, 0);
         for (int j = 0; j < u.nk() && ok; ++j) {
             kv(&p.k, u.h / p.G, u.row0 + j * kTileP);
@@ -281,10 +289,8 @@ __device__ void mma_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd,
             umma_bf16_ts(tm + 2 * kTileP + b * D, tm + b * kTileP + ks * 8, dv + (uint64_t)(ks * 128), idO,
                          first && ks == 0 ? 0u : 1u);
     };
-    const int rounds = rounds_of(total);
-    for (int r = 0; r < rounds; ++r) {
-        Unit u;
-        if (!get_unit(p, r, total, &u)) break;
+    Units units(p, total);
+    for (Unit u; units.next(&u);) {
         const int nk = u.nk();
         uint32_t ph;
         int s = slot_of(0, &ph);
@@ -406,10 +412,8 @@ __device__ void softmax_role(const PromptParams &p, SmemP<D> &sm, const BoundsP 
     const uint32_t tS = tm + b * kTileP + lanes, tO = tm + 2 * kTileP + b * D + lanes;
     const float c2 = p.scale * kLog2e;
     uint32_t n = 0;  // key tiles this warpgroup has done
-    const int rounds = rounds_of(total);
-    for (int r = 0; r < rounds; ++r) {
-        Unit u;
-        if (!get_unit(p, r, total, &u)) return;
+    Units units(p, total);
+    for (Unit u; units.next(&u);) {
         const int nk = u.of(b);
         if (!nk) continue;
         float m = neg_inf(), l = 0.f;  // reference maximum (base 2, scaled) and sum
