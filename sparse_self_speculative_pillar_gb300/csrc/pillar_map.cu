@@ -7,16 +7,17 @@
 // in the slot table (kv_off) and its new tokens in new_slots (new_off).
 //
 // Two kernels:
-//   1. map_scan: one CTA, a thread per request (1024 at a time, with carries),
-//      two block scans -- the demand first, since it decides which requests
-//      are granted, then the other sums -- and the records the expansion
-//      needs.  It also advances the ring's state: the expansion works from
-//      the copy in the workspace.  Latency-bound.
-//   2. map_expand: slot_table[kv_off[b] + t] = block * 16 + t % 16, four slots
-//      per thread and store, 4096 per CTA tile; the requests of a tile are
-//      found by one warp (32-way search of kv_off) and shared.  A position at
-//      the start of a newly taken block also writes the block table's entry.
-//      Bound by the stores: 4 bytes per position.
+//   1. map_scan: one CTA, a thread per request (1024 at a time, with carries), one
+//      block scan of the four sums; only when the ring runs short does the demand
+//      decide first, with a scan of its own.  It writes the records that the
+//      expansion needs and advances the ring's state: the expansion works from the
+//      copy in the workspace.  Latency-bound.
+//   2. map_expand: slot_table[kv_off[b] + t] = block * 16 + t % 16.  A grid row of CTAs
+//      per request, a warp per 1024 positions: two coalesced loads of 32 blocks each,
+//      all in flight, then 16-byte stores whose block comes by shuffle.  (A flat grid
+//      over the slots, each tile searching its request, took 55 us for 17 million
+//      slots where this takes about 20.)  Blocks that were taken are entered into the
+//      table on the way.  Bound by the stores: 4 bytes per position.
 // The ring is first in, first out and never holds more than its size, so the
 // places popped in a call (from head) and the places pushed (from head +
 // count) are distinct: taking and giving need no order between them.
@@ -29,7 +30,7 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 constexpr int kExpandThreads = 256;
-constexpr int kExpandTile = 4096;  // slots per CTA tile: four int4 stores per thread
+constexpr int kWarpBlocks = 64;    // blocks a warp expands at a time
 constexpr int kBlock = PILLAR_KV_BLOCK;
 
 __device__ __forceinline__ long long warp_scan(long long x) {
@@ -87,14 +88,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
         if (len < 0 || len > most) bad |= PILLAR_FLAG_REQUEST, len = prev;
         const int m = (prev + kBlock - 1) / kBlock;
         int n = (len + kBlock - 1) / kBlock;
-        long long want[1] = {n > m ? n - m : 0}, wtot[1];
-        const long long own = want[0];
-        block_scan<1>(want, wtot);
-        const long long first = c_want + want[0];
-        if (own > 0 && first + own > count) bad |= PILLAR_FLAG_BLOCK, len = prev, n = m;
-        const int fresh = len > prev ? len - prev : 0, back = m > n ? m - n : 0;
-        long long v[4] = {len, fresh, back, n > m ? n - m : 0}, tot[4];
+        const long long own = n > m ? n - m : 0;
+        long long v[4] = {len, len > prev ? len - prev : 0, m > n ? m - n : 0, own}, tot[4];
+        long long fresh = v[1], back = v[2];
         block_scan<4>(v, tot);
+        c_want += tot[3];
+        if (c_want > count) {  // (the same in every thread) the ring runs short: who is granted?
+            const bool short_of = own > 0 && c_want - tot[3] + v[3] + own > count;
+            if (short_of) bad |= PILLAR_FLAG_BLOCK, len = prev, n = m;
+            fresh = len > prev ? len - prev : 0, back = m > n ? m - n : 0;
+            v[0] = len, v[1] = fresh, v[2] = back, v[3] = n > m ? n - m : 0;
+            block_scan<4>(v, tot);
+        }
         if (live) {
             const long long no = c_new + v[1];
             if (no + fresh > 0x7fffffffll) bad |= PILLAR_FLAG_COUNT;
@@ -113,7 +118,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
             a.kv_off[b] = r.kv_off;
             a.new_off[b] = r.new_off;
         }
-        c_want += wtot[0];
         c_len += tot[0];
         c_new += tot[1];
         c_give += tot[2];
@@ -140,126 +144,71 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
     }
 }
 
-// The last request whose offset is at or below x (the offsets ascend from 0;
-// x is below the total), by the whole warp: 32 probes a round.
-template <typename F>
-__device__ __forceinline__ int warp_find(int B, long long x, F off) {
-    int lo = 0, n = B;  // the answer lies in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int i = lo + (int)(threadIdx.x & 31) * step;
-        const unsigned le = __ballot_sync(0xffffffffu, i < lo + n && off(i) <= x);
-        const int k = 31 - __clz(le);  // (lane 0 probes lo, which holds)
-        const int end = lo + n;
-        lo += k * step;
-        n = min(step, end - lo);
-    }
-    return lo;
-}
-
-// The slot of position t of request b, its block taken from the ring when it
-// is new (and then entered into the table by the thread that writes it).
-struct Slots {
-    const MapArgs &a;
-    int head;
-    int *bad;
-    __device__ __forceinline__ int block(const MapRequest &r, int b, int i, bool enter) const {
-        int blk;
-        if (i < r.kept) {
-            blk = a.table[(size_t)b * a.max_blocks + i];
-        } else {
-            long long at = (long long)head + r.take + (i - r.kept);
-            if (at >= a.num_blocks) at -= a.num_blocks;
-            blk = a.ring[at];
-            if (enter) a.table[(size_t)b * a.max_blocks + i] = blk;
-        }
-        return blk;
-    }
-    __device__ __forceinline__ int slot(int blk, int t) const {
-        if (blk < 0 || blk >= a.num_blocks) {
-            *bad |= PILLAR_FLAG_SLOT;
-            return -1;
-        }
-        return blk * kBlock + (t & (kBlock - 1));
-    }
-};
-
 __global__ void __launch_bounds__(kExpandThreads) map_expand(const MapArgs a) {
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     MapHeader *hdr = reinterpret_cast<MapHeader *>(a.ws);
     const MapRequest *rec = reinterpret_cast<const MapRequest *>(a.ws + sizeof(MapHeader));
-    __shared__ int s_first;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = hdr->head, count = hdr->count;
     int bad = 0;
-    const Slots sl{a, hdr->head, &bad};
-    // --- the slot table.  Every block of every request is entered here, whatever the capacity.
-    const long long total = hdr->total;
-    for (long long t0 = (long long)blockIdx.x * kExpandTile; t0 < total; t0 += (long long)gridDim.x * kExpandTile) {
-        if (threadIdx.x < 32) {
-            const int f = warp_find(a.B, t0, [&](int i) { return rec[i].kv_off; });
-            if (threadIdx.x == 0) s_first = f;
-        }
-        __syncthreads();
-        int b = s_first;
-        __syncthreads();
-        MapRequest r = rec[b];
-        long long end = b + 1 < a.B ? rec[b + 1].kv_off : total;
-        int blk = -1, at = -1;  // the block of the last position
+    auto slot0 = [&](int blk) {  // first slot of a block
+        if (blk >= 0 && blk < a.num_blocks) return blk * kBlock;
+        bad |= PILLAR_FLAG_SLOT;
+        return -1;
+    };
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const MapRequest r = rec[b];
+        const int len = a.granted[b];
+        int *row = a.table + (size_t)b * a.max_blocks;
+        auto ring = [&](int i) {  // the i-th block, when it was taken
+            const long long at = (long long)head + r.take + (i - r.kept);
+            return a.ring[at >= a.num_blocks ? at - a.num_blocks : at];
+        };
+        for (int i0 = (blockIdx.y * (kExpandThreads / 32) + warp) * kWarpBlocks; i0 < r.blocks;
+             i0 += gridDim.y * (kExpandThreads / 32) * kWarpBlocks) {
+            int blk[kWarpBlocks / 32];
 #pragma unroll
-        for (int q = 0; q < kExpandTile / (4 * kExpandThreads); ++q) {
-            const long long i0 = t0 + ((long long)q * kExpandThreads + threadIdx.x) * 4;
-            if (i0 >= total) break;
-            int v[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const long long i = i0 + e;
-                if (i >= total) break;
-                while (i >= end) {  // (requests ahead, empty ones included)
-                    r = rec[++b];
-                    end = b + 1 < a.B ? rec[b + 1].kv_off : total;
-                    at = -1;
-                }
-                const int t = (int)(i - r.kv_off);
-                if (t / kBlock != at) {
-                    at = t / kBlock;
-                    blk = sl.block(r, b, at, (t & (kBlock - 1)) == 0);
-                }
-                v[e] = sl.slot(blk, t);
+            for (int q = 0; q < kWarpBlocks / 32; ++q) {
+                const int i = i0 + 32 * q + lane;
+                blk[q] = i >= r.blocks ? 0 : i < r.kept ? row[i] : ring(i);
             }
-            if (i0 + 4 <= min(total, a.slot_capacity)) {
-                *reinterpret_cast<int4 *>(a.slots + i0) = make_int4(v[0], v[1], v[2], v[3]);
-            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (i0 + e < total && i0 + e < a.slot_capacity) a.slots[i0 + e] = v[e];
+            for (int q = 0; q < kWarpBlocks / 32; ++q) {
+                const int i = i0 + 32 * q + lane;
+                if (i >= r.kept && i < r.blocks) row[i] = blk[q];
+                const int first = i < r.blocks ? slot0(blk[q]) : 0;
+                const int t0 = (i0 + 32 * q) * kBlock;  // position of the 32 blocks' first slot
+                const long long at = r.kv_off + t0;
+                if ((at & 3) == 0 && t0 + 32 * kBlock <= len && at + 32 * kBlock <= a.slot_capacity) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // eight blocks a store, four lanes each
+                        const int s = __shfl_sync(0xffffffffu, first, 8 * e + (lane >> 2)), o = (lane & 3) * 4;
+                        *reinterpret_cast<int4 *>(a.slots + at + 128 * e + 4 * lane) =
+                            s < 0 ? make_int4(-1, -1, -1, -1) : make_int4(s + o, s + o + 1, s + o + 2, s + o + 3);
+                    }
+                } else {
+#pragma unroll 4
+                    for (int e = 0; e < 16; ++e) {  // two blocks a store
+                        const int s = __shfl_sync(0xffffffffu, first, 2 * e + (lane >> 4)), t = 32 * e + lane;
+                        if (t0 + t < len && at + t < a.slot_capacity) a.slots[at + t] = s < 0 ? -1 : s + (lane & 15);
+                    }
+                }
             }
         }
-    }
-    // --- the new tokens' slots
-    const int warp = (int)((blockIdx.x * kExpandThreads + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    const int warps = (int)(gridDim.x * kExpandThreads >> 5);
-    const long long nnew = min(min(hdr->total_new, a.new_capacity), 0x7fffffffll);
-    for (long long i0 = (long long)warp * 32; i0 < nnew; i0 += (long long)warps * 32) {
-        int b = warp_find(a.B, i0, [&](int i) { return (long long)rec[i].new_off; });
-        const long long i = i0 + lane;
-        if (i < nnew) {
-            while (b + 1 < a.B && rec[b + 1].new_off <= i) ++b;
-            const MapRequest r = rec[b];
-            const int t = r.prev + (int)(i - r.new_off);
-            a.new_slots[i] = sl.slot(sl.block(r, b, t / kBlock, false), t);
-        }
-    }
-    // --- the blocks given back
-    const long long nback = hdr->released;
-    for (long long i0 = (long long)warp * 32; i0 < nback; i0 += (long long)warps * 32) {
-        int b = warp_find(a.B, i0, [&](int i) { return (long long)rec[i].give; });
-        const long long i = i0 + lane;
-        if (i < nback) {
-            while (b + 1 < a.B && rec[b].give_end <= i) ++b;
-            const MapRequest r = rec[b];
-            const int blk = a.table[(size_t)b * a.max_blocks + r.blocks + (int)(i - r.give)];
-            if (blk < 0 || blk >= a.num_blocks) bad |= PILLAR_FLAG_SLOT;
-            a.ring[((long long)hdr->head + hdr->count + i) % a.num_blocks] = blk;
+        if (blockIdx.y == 0) {
+            // the new tokens' slots
+            for (int i = threadIdx.x; i < len - r.prev && (long long)r.new_off + i < a.new_capacity; i += kExpandThreads) {
+                const int t = r.prev + i, j = t / kBlock, s = slot0(j < r.kept ? row[j] : ring(j));
+                a.new_slots[(long long)r.new_off + i] = s < 0 ? -1 : s + t % kBlock;
+            }
+            // the blocks given back
+            if (hdr->released)
+                for (int i = threadIdx.x; i < r.give_end - r.give; i += kExpandThreads) {
+                    const int blk = row[r.blocks + i];
+                    slot0(blk);
+                    a.ring[((long long)head + count + r.give + i) % a.num_blocks] = blk;
+                }
         }
     }
     if (bad) atomicOr(&hdr->err, bad);
@@ -279,11 +228,12 @@ cudaError_t launch_block_map(const MapArgs &a, int nsm, cudaStream_t st) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, map_scan, a);
     if (e != cudaSuccess) return e;
-    // as many CTAs as the batch could need at its longest, up to four per SM (the totals are on the device)
-    const long long most = (long long)a.B * a.max_len;
-    long long grid = (most + kExpandTile - 1) / kExpandTile;
-    grid = grid < 1 ? 1 : grid > 4ll * nsm ? 4ll * nsm : grid;
-    cfg.gridDim = dim3((unsigned)grid);
+    // per request, CTAs for its longest possible table, as long as that stays within 32 a SM
+    const int per_cta = kExpandThreads / 32 * kWarpBlocks * kBlock;
+    int rows = (int)(((long long)a.max_len + per_cta - 1) / per_cta);
+    const int most = 32 * nsm / a.B;
+    rows = rows < most ? rows : most;
+    cfg.gridDim = dim3((unsigned)(a.B < 65536 ? a.B : 65536), (unsigned)(rows < 1 ? 1 : rows < 65535 ? rows : 65535));
     cfg.blockDim = dim3(kExpandThreads);
     return cudaLaunchKernelEx(&cfg, map_expand, a);
 }
