@@ -7,16 +7,16 @@
 // in the slot table (kv_off) and its new tokens in new_slots (new_off).
 //
 // Two kernels:
-//   1. map_scan: one CTA, a thread per request (1024 at a time, with carries), one
+//   1. map_scan: one CTA, four requests a thread (4096 at a time, with carries), one
 //      block scan of the four sums; only when the ring runs short does the demand
 //      decide first, with a scan of its own.  It writes the records that the
 //      expansion needs and advances the ring's state: the expansion works from the
 //      copy in the workspace.  Latency-bound.
 //   2. map_expand: slot_table[kv_off[b] + t] = block * 16 + t % 16.  A grid row of CTAs
-//      per request, a warp per 1024 positions: two coalesced loads of 32 blocks each,
-//      all in flight, then 16-byte stores whose block comes by shuffle.  (A flat grid
-//      over the slots, each tile searching its request, took 55 us for 17 million
-//      slots where this takes about 20.)  Blocks that were taken are entered into the
+//      per request, a warp per 512 positions: one coalesced load of 32 blocks, then
+//      16-byte stores whose block comes by shuffle.  (A flat grid over the slots, each
+//      tile searching its request, took 55 us for 17 million slots where this takes
+//      9, with 67 MB to write.)  Blocks that were taken are entered into the
 //      table on the way.  Bound by the stores: 4 bytes per position.
 // The ring is first in, first out and never holds more than its size, so the
 // places popped in a call (from head) and the places pushed (from head +
@@ -29,9 +29,12 @@ namespace pillar {
 namespace {
 
 constexpr int kScanThreads = 1024;
+constexpr int kPerThread = 4;      // requests a scan thread takes
 constexpr int kExpandThreads = 256;
-constexpr int kWarpBlocks = 64;    // blocks a warp expands at a time
+constexpr int kWarpBlocks = 32;    // blocks a warp expands at a time (64: 5 % slower, 128: 15 %)
 constexpr int kBlock = PILLAR_KV_BLOCK;
+
+__device__ __forceinline__ int blocks_of(int len) { return (len + kBlock - 1) / kBlock; }
 
 __device__ __forceinline__ long long warp_scan(long long x) {
 #pragma unroll
@@ -79,44 +82,70 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
     __shared__ int s_bad;
     if (threadIdx.x == 0) s_bad = 0;
     long long c_want = 0, c_used = 0, c_len = 0, c_new = 0, c_give = 0;  // carries (the same in every thread)
-    for (int base = 0; base < a.B; base += kScanThreads) {
-        const int b = base + threadIdx.x;
-        const bool live = b < a.B;
-        int prev = live ? a.prev_len[b] : 0, len = live ? a.req_len[b] : 0;
-        const long long most = min((long long)a.max_len, (long long)a.max_blocks * kBlock);
-        if (prev < 0 || prev > most) bad |= PILLAR_FLAG_REQUEST, prev = 0, len = 0;
-        if (len < 0 || len > most) bad |= PILLAR_FLAG_REQUEST, len = prev;
-        const int m = (prev + kBlock - 1) / kBlock;
-        int n = (len + kBlock - 1) / kBlock;
-        const long long own = n > m ? n - m : 0;
-        long long v[4] = {len, len > prev ? len - prev : 0, m > n ? m - n : 0, own}, tot[4];
-        long long fresh = v[1], back = v[2];
+    const long long most = min((long long)a.max_len, (long long)a.max_blocks * kBlock);
+    for (int base = 0; base < a.B; base += kScanThreads * kPerThread) {
+        const int b0 = base + threadIdx.x * kPerThread;
+        int prev[kPerThread], len[kPerThread];
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            prev[i] = b0 + i < a.B ? a.prev_len[b0 + i] : 0;
+            len[i] = b0 + i < a.B ? a.req_len[b0 + i] : 0;
+        }
+        long long v[4] = {0, 0, 0, 0}, tot[4];  // positions, new tokens, blocks given back, blocks taken
+        auto add = [&](int i) {
+            const int m = blocks_of(prev[i]), n = blocks_of(len[i]);
+            v[0] += len[i];
+            v[1] += max(len[i] - prev[i], 0);
+            v[2] += max(m - n, 0);
+            v[3] += max(n - m, 0);
+        };
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            if (prev[i] < 0 || prev[i] > most) bad |= PILLAR_FLAG_REQUEST, prev[i] = 0, len[i] = 0;
+            if (len[i] < 0 || len[i] > most) bad |= PILLAR_FLAG_REQUEST, len[i] = prev[i];
+            add(i);
+        }
         block_scan<4>(v, tot);
+        const long long before = c_want;
         c_want += tot[3];
-        if (c_want > count) {  // (the same in every thread) the ring runs short: who is granted?
-            const bool short_of = own > 0 && c_want - tot[3] + v[3] + own > count;
-            if (short_of) bad |= PILLAR_FLAG_BLOCK, len = prev, n = m;
-            fresh = len > prev ? len - prev : 0, back = m > n ? m - n : 0;
-            v[0] = len, v[1] = fresh, v[2] = back, v[3] = n > m ? n - m : 0;
+        if (c_want > count) {  // (the same in every thread) the ring runs short: the first whose blocks do not fit and
+                               // all later ones that need some stay as they are
+            long long want = before + v[3];
+            v[0] = v[1] = v[2] = v[3] = 0;
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) {
+                const int own = max(blocks_of(len[i]) - blocks_of(prev[i]), 0);
+                want += own;
+                if (own > 0 && want > count) bad |= PILLAR_FLAG_BLOCK, len[i] = prev[i];
+                add(i);
+            }
             block_scan<4>(v, tot);
         }
-        if (live) {
-            const long long no = c_new + v[1];
-            if (no + fresh > 0x7fffffffll) bad |= PILLAR_FLAG_COUNT;
-            MapRequest r;
-            r.kv_off = c_len + v[0];
-            r.new_off = (int)min(no, 0x7fffffffll);
-            r.prev = prev;
-            r.blocks = n;
-            r.kept = min(n, m);
-            r.take = (int)(c_used + v[3]);  // (the granted requests' demands come first)
-            r.give = (int)min(c_give + v[2], 0x7fffffffll);
-            r.give_end = (int)min(c_give + v[2] + back, 0x7fffffffll);
-            r.pad = 0;
-            rec[b] = r;
-            a.granted[b] = len;
-            a.kv_off[b] = r.kv_off;
-            a.new_off[b] = r.new_off;
+        long long kv = c_len + v[0], no = c_new + v[1], give = c_give + v[2], take = c_used + v[3];
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int b = b0 + i, m = blocks_of(prev[i]), n = blocks_of(len[i]), fresh = max(len[i] - prev[i], 0);
+            if (b < a.B) {
+                if (no + fresh > 0x7fffffffll) bad |= PILLAR_FLAG_COUNT;
+                MapRequest r;
+                r.kv_off = kv;
+                r.new_off = (int)min(no, 0x7fffffffll);
+                r.prev = prev[i];
+                r.blocks = n;
+                r.kept = min(n, m);
+                r.take = (int)take;  // (the granted requests' demands come first)
+                r.give = (int)min(give, 0x7fffffffll);
+                r.give_end = (int)min(give + max(m - n, 0), 0x7fffffffll);
+                r.len = len[i];
+                rec[b] = r;
+                a.granted[b] = len[i];
+                a.kv_off[b] = kv;
+                a.new_off[b] = r.new_off;
+            }
+            kv += len[i];
+            no += fresh;
+            give += max(m - n, 0);
+            take += max(n - m, 0);
         }
         c_len += tot[0];
         c_new += tot[1];
@@ -159,7 +188,7 @@ __global__ void __launch_bounds__(kExpandThreads) map_expand(const MapArgs a) {
     };
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const MapRequest r = rec[b];
-        const int len = a.granted[b];
+        const int len = r.len;
         int *row = a.table + (size_t)b * a.max_blocks;
         auto ring = [&](int i) {  // the i-th block, when it was taken
             const long long at = (long long)head + r.take + (i - r.kept);

@@ -28,7 +28,7 @@ struct MapRequest {
     int take;       // its first block from the ring: head + take
     int give;       // its first released block: pushed at head + count + give
     int give_end;   // give + the blocks it releases
-    int pad;
+    int len;        // the granted length
 };
 
 inline size_t map_ws_bytes(int B) {
