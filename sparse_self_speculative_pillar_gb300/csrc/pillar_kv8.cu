@@ -62,6 +62,15 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
+// The larger magnitudes of two pairs of bf16 values; a NaN stays one.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(d) : "r"(m), "r"(x));
+    return d;
+}
+// The low bf16 value of a pair, by a multiplication: the shifts and masks of this kernel keep the ALU busy.
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w * 65536u); }
+
 struct Owner {
     int token;  // the first of the block's new rows
     int block;
@@ -91,14 +100,11 @@ __device__ void append_block(const Kv8AppendArgs &a, const Owner &o, int h, bool
         const int r = i * RW + rl;
         x[i] = r < o.rows ? __ldg(reinterpret_cast<const uint4 *>(src + r * stride)) : make_uint4(0, 0, 0, 0);
     }
-    // the largest magnitude, as bits: positive bf16 values order as integers
+    // the largest magnitude, then as bits: positive bf16 values order as integers, NaN last
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        mx = __vmaxu2(mx, x[i].x & 0x7fff7fffu);
-        mx = __vmaxu2(mx, x[i].y & 0x7fff7fffu);
-        mx = __vmaxu2(mx, x[i].z & 0x7fff7fffu);
-        mx = __vmaxu2(mx, x[i].w & 0x7fff7fffu);
+        mx = max_abs2(max_abs2(max_abs2(max_abs2(mx, x[i].x), x[i].y), x[i].z), x[i].w);
     }
     uint32_t amax = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
     bool odd = false;
@@ -141,23 +147,29 @@ __device__ void append_block(const Kv8AppendArgs &a, const Owner &o, int h, bool
     }
     // multiplying by 1/s is exact for the powers of two that this kernel writes; a scale that came
     // from elsewhere divides
-    const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0;
-    const float inv = exact ? 1.f / s : 1.f;
+    uint8_t *out = dst + (size_t)(o.row + rl) * D + c * 8;
+    if (!odd && (__float_as_uint(s) & 0x7fffffu) == 0) {
+        const float inv = 1.f / s;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int r = i * RW + rl;
-        if (r >= o.rows) continue;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t c2[4];
+        for (int i = 0; i < NL; ++i) {
+            if (i * RW + rl >= o.rows) continue;
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t c2[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float lo = bf16lo(w[q]), hi = bf16hi(w[q]);
-            if (odd) lo = clean(lo), hi = clean(hi);
-            if (!exact) lo = __fdiv_rn(lo, s), hi = __fdiv_rn(hi, s);
-            c2[q] = e4m3x2(lo * inv, hi * inv);
+            for (int q = 0; q < 4; ++q) c2[q] = e4m3x2(low_of(w[q]) * inv, bf16hi(w[q]) * inv);
+            *reinterpret_cast<uint2 *>(out + i * RW * D) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
         }
-        *reinterpret_cast<uint2 *>(dst + (size_t)(o.row + r) * D + c * 8) =
-            make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
+    } else {  // (rare: not unrolled, the rows read again)
+#pragma unroll 1
+        for (int r = rl; r < o.rows; r += RW) {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + r * stride));
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            uint32_t c2[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                c2[q] = e4m3x2(__fdiv_rn(clean(low_of(w[q])), s), __fdiv_rn(clean(bf16hi(w[q])), s));
+            *reinterpret_cast<uint2 *>(out + (r - rl) * D) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
+        }
     }
     if (lane == 0) {
         if (o.row == 0 || s != before) *scale = s;
@@ -166,31 +178,45 @@ __device__ void append_block(const Kv8AppendArgs &a, const Owner &o, int h, bool
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsPerCta) kv8_append_kernel(const Kv8AppendArgs a, int rows) {
+__global__ void __launch_bounds__(kThreadsPerCta, 4) kv8_append_kernel(const Kv8AppendArgs a, int rows) {
     __shared__ Owner s_own[kMaxCtaRows];
     __shared__ int s_n;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const long long t = (long long)blockIdx.x * rows + lane;
+        const int t0 = blockIdx.x * rows, t = t0 + lane;
+        const int all = min(a.n, __ldg(a.new_off + a.B));
+        // the request of row t0: 32 offsets a round
+        int lo = 0;
+        for (int n = a.B; n > 1;) {  // the last offset at or below t0 is one of n from lo on
+            const int step = (n + 31) / 32, i = lo + lane * step;
+            const unsigned le = __ballot_sync(0xffffffffu, lane * step < n && __ldg(a.new_off + i) <= t0);
+            const int k = max(31 - __clz(le), 0);
+            n = min(step, n - k * step);
+            lo += k * step;
+        }
+        // the others' by the offsets that follow it (more than 32 requests begin within 16 rows only when some are empty)
+        const int behind = lo + 1 + lane <= a.B ? __ldg(a.new_off + lo + 1 + lane) : 0x7fffffff;
+        int b = lo;
+        for (int i = 0; i < rows; ++i) {
+            const int at = __popc(__ballot_sync(0xffffffffu, behind <= t0 + i));
+            if (lane == i) b = lo + at;
+        }
+        if (lane < rows)
+            for (b = min(b, a.B - 1); b + 1 < a.B && __ldg(a.new_off + b + 1) <= t;) ++b;
         bool own = false;
         Owner o = {};
         int bad = 0;
-        if (lane < rows && t < a.n && t < a.new_off[a.B]) {
-            int lo = 0, hi = a.B - 1;  // the last request whose offset is at or below t
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.new_off[mid] <= t) lo = mid; else hi = mid - 1;
-            }
-            const int first = a.new_off[lo], end = a.new_off[lo + 1], len = a.req_len[lo];
+        if (lane < rows && t < all) {
+            const int first = __ldg(a.new_off + b), end = __ldg(a.new_off + b + 1), len = __ldg(a.req_len + b);
             const long long pos = (long long)len - end + t;
             if (first < 0 || t < first || t >= end || end > a.n || len > a.max_len || len - (end - first) < 0 ||
                 pos / kBlock >= a.max_blocks) {
                 bad = PILLAR_FLAG_REQUEST;
             } else if (pos % kBlock == 0 || t == first) {
-                o.token = (int)t;
+                o.token = t;
                 o.row = (int)(pos % kBlock);
-                o.rows = min(kBlock - o.row, end - (int)t);
-                o.block = a.table[(size_t)lo * a.max_blocks + pos / kBlock];
+                o.rows = min(kBlock - o.row, end - t);
+                o.block = a.table[(size_t)b * a.max_blocks + pos / kBlock];
                 if (o.block < 0 || o.block >= a.num_blocks) bad = PILLAR_FLAG_SLOT;
                 else own = true;
             }

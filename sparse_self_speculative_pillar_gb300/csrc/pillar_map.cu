@@ -7,16 +7,18 @@
 // in the slot table (kv_off) and its new tokens in new_slots (new_off).
 //
 // Two kernels:
-//   1. map_scan: one CTA, four requests a thread (4096 at a time, with carries), one
+//   1. map_scan: one CTA, two requests a thread (2048 at a time, with carries), one
 //      block scan of the four sums; only when the ring runs short does the demand
 //      decide first, with a scan of its own.  It writes the records that the
-//      expansion needs and advances the ring's state: the expansion works from the
+//      expansion needs beyond the call's own arrays (8 bytes a request: with
+//      whole records one SM took as long to write them as for all the rest), and
+//      advances the ring's state: the expansion works from the
 //      copy in the workspace.  Latency-bound.
 //   2. map_expand: slot_table[kv_off[b] + t] = block * 16 + t % 16.  A grid row of CTAs
 //      per request, a warp per 512 positions: one coalesced load of 32 blocks, then
-//      16-byte stores whose block comes by shuffle.  (A flat grid over the slots, each
-//      tile searching its request, took 55 us for 17 million slots where this takes
-//      9, with 67 MB to write.)  Blocks that were taken are entered into the
+//      16-byte stores whose blocks come by shuffle.  (A flat grid over the slots, each
+//      tile searching its request, took 55 us for 11.6 million slots where this takes
+//      13, 3.6 TB/s.)  Blocks that were taken are entered into the
 //      table on the way.  Bound by the stores: 4 bytes per position.
 // The ring is first in, first out and never holds more than its size, so the
 // places popped in a call (from head) and the places pushed (from head +
@@ -29,9 +31,8 @@ namespace pillar {
 namespace {
 
 constexpr int kScanThreads = 1024;
-constexpr int kPerThread = 4;      // requests a scan thread takes
+constexpr int kPerThread = 2;      // requests a scan thread takes
 constexpr int kExpandThreads = 256;
-constexpr int kWarpBlocks = 32;    // blocks a warp expands at a time (64: 5 % slower, 128: 15 %)
 constexpr int kBlock = PILLAR_KV_BLOCK;
 
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBlock - 1) / kBlock; }
@@ -127,20 +128,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
             const int b = b0 + i, m = blocks_of(prev[i]), n = blocks_of(len[i]), fresh = max(len[i] - prev[i], 0);
             if (b < a.B) {
                 if (no + fresh > 0x7fffffffll) bad |= PILLAR_FLAG_COUNT;
-                MapRequest r;
-                r.kv_off = kv;
-                r.new_off = (int)min(no, 0x7fffffffll);
-                r.prev = prev[i];
-                r.blocks = n;
-                r.kept = min(n, m);
-                r.take = (int)take;  // (the granted requests' demands come first)
-                r.give = (int)min(give, 0x7fffffffll);
-                r.give_end = (int)min(give + max(m - n, 0), 0x7fffffffll);
-                r.len = len[i];
-                rec[b] = r;
+                // (the granted requests' demands come first in the ring)
+                rec[b] = MapRequest{(int)take, (int)min(give, 0x7fffffffll)};
                 a.granted[b] = len[i];
                 a.kv_off[b] = kv;
-                a.new_off[b] = r.new_off;
+                a.new_off[b] = (int)min(no, 0x7fffffffll);
             }
             kv += len[i];
             no += fresh;
@@ -161,8 +153,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
         hdr->err = s_bad;
         hdr->head = head;
         hdr->count = count;
-        hdr->total = c_len;
-        hdr->total_new = c_new;
         hdr->released = ring_ok ? c_give : 0;
         a.kv_off[a.B] = c_len;
         a.new_off[a.B] = (int)min(c_new, 0x7fffffffll);
@@ -186,55 +176,63 @@ __global__ void __launch_bounds__(kExpandThreads) map_expand(const MapArgs a) {
         bad |= PILLAR_FLAG_SLOT;
         return -1;
     };
+    const int most = (int)min((long long)a.max_len, (long long)a.max_blocks * kBlock);
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const MapRequest r = rec[b];
-        const int len = r.len;
+        const int len = a.granted[b], given = a.prev_len[b];
+        const long long off = a.kv_off[b];
+        const int prev = given < 0 || given > most ? 0 : given;
+        const int blocks = blocks_of(len), had = blocks_of(prev), kept = min(blocks, had);
         int *row = a.table + (size_t)b * a.max_blocks;
-        auto ring = [&](int i) {  // the i-th block, when it was taken
-            const long long at = (long long)head + r.take + (i - r.kept);
+        auto block = [&](int i) {  // (those past `kept` are being taken)
+            if (i < kept) return row[i];
+            const long long at = (long long)head + r.take + (i - kept);
             return a.ring[at >= a.num_blocks ? at - a.num_blocks : at];
         };
-        for (int i0 = (blockIdx.y * (kExpandThreads / 32) + warp) * kWarpBlocks; i0 < r.blocks;
-             i0 += gridDim.y * (kExpandThreads / 32) * kWarpBlocks) {
-            int blk[kWarpBlocks / 32];
+        // output aligned to four slots: `lead` single ones, then 16-byte stores, which may span two blocks
+        const int lead = (int)(-off & 3);
+        for (int i0 = (blockIdx.y * (kExpandThreads / 32) + warp) * 32; i0 < blocks;
+             i0 += gridDim.y * (kExpandThreads / 32) * 32) {
+            const int i = i0 + lane;
+            const int blk = i < blocks ? block(i) : 0, behind = i0 + 32 < blocks ? block(i0 + 32) : 0;
+            if (i >= kept && i < blocks) row[i] = blk;
+            const int first = i < blocks ? slot0(blk) : 0, next = i0 + 32 < blocks ? slot0(behind) : 0;
+            const int t0 = i0 * kBlock;
+            int *out = a.slots + off + t0;
+            const int n = (int)max(0ll, min((long long)len - t0, a.slot_capacity - off - t0));  // slots to write from t0 on
+            const int s0 = __shfl_sync(0xffffffffu, first, 0);
+            if (i0 == 0 && lane < lead && lane < n) out[lane] = s0 < 0 ? -1 : s0 + lane;
 #pragma unroll
-            for (int q = 0; q < kWarpBlocks / 32; ++q) {
-                const int i = i0 + 32 * q + lane;
-                blk[q] = i >= r.blocks ? 0 : i < r.kept ? row[i] : ring(i);
-            }
+            for (int e = 0; e < 4; ++e) {
+                const int t = lead + 128 * e + 4 * lane, j = t / kBlock, j3 = (t + 3) / kBlock;
+                const int sa = __shfl_sync(0xffffffffu, first, j & 31), sb = __shfl_sync(0xffffffffu, first, j3 & 31);
+                const int xa = j < 32 ? sa : next, xb = j3 < 32 ? sb : next;
+                int v[4];
 #pragma unroll
-            for (int q = 0; q < kWarpBlocks / 32; ++q) {
-                const int i = i0 + 32 * q + lane;
-                if (i >= r.kept && i < r.blocks) row[i] = blk[q];
-                const int first = i < r.blocks ? slot0(blk[q]) : 0;
-                const int t0 = (i0 + 32 * q) * kBlock;  // position of the 32 blocks' first slot
-                const long long at = r.kv_off + t0;
-                if ((at & 3) == 0 && t0 + 32 * kBlock <= len && at + 32 * kBlock <= a.slot_capacity) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {  // eight blocks a store, four lanes each
-                        const int s = __shfl_sync(0xffffffffu, first, 8 * e + (lane >> 2)), o = (lane & 3) * 4;
-                        *reinterpret_cast<int4 *>(a.slots + at + 128 * e + 4 * lane) =
-                            s < 0 ? make_int4(-1, -1, -1, -1) : make_int4(s + o, s + o + 1, s + o + 2, s + o + 3);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const int x = (t + q) / kBlock == j ? xa : xb;
+                    v[q] = x < 0 ? -1 : x + (t + q) % kBlock;
+                }
+                if (t + 4 <= n) {
+                    *reinterpret_cast<int4 *>(out + t) = make_int4(v[0], v[1], v[2], v[3]);
                 } else {
-#pragma unroll 4
-                    for (int e = 0; e < 16; ++e) {  // two blocks a store
-                        const int s = __shfl_sync(0xffffffffu, first, 2 * e + (lane >> 4)), t = 32 * e + lane;
-                        if (t0 + t < len && at + t < a.slot_capacity) a.slots[at + t] = s < 0 ? -1 : s + (lane & 15);
-                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (t + q < n) out[t + q] = v[q];
                 }
             }
         }
         if (blockIdx.y == 0) {
             // the new tokens' slots
-            for (int i = threadIdx.x; i < len - r.prev && (long long)r.new_off + i < a.new_capacity; i += kExpandThreads) {
-                const int t = r.prev + i, j = t / kBlock, s = slot0(j < r.kept ? row[j] : ring(j));
-                a.new_slots[(long long)r.new_off + i] = s < 0 ? -1 : s + t % kBlock;
+            const int no = a.new_off[b];
+            for (int i = threadIdx.x; i < len - prev && (long long)no + i < a.new_capacity; i += kExpandThreads) {
+                const int t = prev + i, s = slot0(block(t / kBlock));
+                a.new_slots[(long long)no + i] = s < 0 ? -1 : s + t % kBlock;
             }
             // the blocks given back
             if (hdr->released)
-                for (int i = threadIdx.x; i < r.give_end - r.give; i += kExpandThreads) {
-                    const int blk = row[r.blocks + i];
+                for (int i = threadIdx.x; i < had - blocks; i += kExpandThreads) {
+                    const int blk = row[blocks + i];
                     slot0(blk);
                     a.ring[((long long)head + count + r.give + i) % a.num_blocks] = blk;
                 }
@@ -257,10 +255,11 @@ cudaError_t launch_block_map(const MapArgs &a, int nsm, cudaStream_t st) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, map_scan, a);
     if (e != cudaSuccess) return e;
-    // per request, CTAs for its longest possible table, as long as that stays within 32 a SM
-    const int per_cta = kExpandThreads / 32 * kWarpBlocks * kBlock;
+    // per request, CTAs for its longest possible table, as long as that stays within 16 a SM
+    // (2048 requests of 8000 positions: 17.6 us a call with 16, 18.5 with 32, 21.8 with 64)
+    const int per_cta = kExpandThreads * kBlock;
     int rows = (int)(((long long)a.max_len + per_cta - 1) / per_cta);
-    const int most = 32 * nsm / a.B;
+    const int most = 16 * nsm / a.B;
     rows = rows < most ? rows : most;
     cfg.gridDim = dim3((unsigned)(a.B < 65536 ? a.B : 65536), (unsigned)(rows < 1 ? 1 : rows < 65535 ? rows : 65535));
     cfg.blockDim = dim3(kExpandThreads);

@@ -7,28 +7,19 @@
 
 namespace pillar {
 
-// What the scan leaves for the expansion: one record for the call, one per request.
+// What the scan leaves for the expansion beside the call's own arrays: one record for the call, one per request.
 struct MapHeader {
     int err;          // PILLAR_FLAG_* bits
     int head, count;  // the ring's state when the call began
     int pad;
-    long long total;      // positions of the batch (kv_off[B])
-    long long total_new;  // new tokens (new_off[B])
-    long long released;   // blocks given back
-    long long pad2[27];   // keeps the records 256-byte aligned
+    long long released;  // blocks given back
+    long long pad2[29];  // keeps the records 256-byte aligned
 };
 static_assert(sizeof(MapHeader) == 256, "header size");
 
 struct MapRequest {
-    long long kv_off;
-    int new_off;
-    int prev;       // length before (0 when it was bad)
-    int blocks;     // blocks of the granted length
-    int kept;       // blocks it already had that stay: min(blocks, ceil(prev / 16))
-    int take;       // its first block from the ring: head + take
-    int give;       // its first released block: pushed at head + count + give
-    int give_end;   // give + the blocks it releases
-    int len;        // the granted length
+    int take;  // its first block from the ring: head + take
+    int give;  // its first released block: pushed at head + count + give
 };
 
 inline size_t map_ws_bytes(int B) {
