@@ -263,3 +263,19 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
         P.pillar_prompt_attn(c.shape, d["q"].transpose(1, 2).contiguous().transpose(1, 2), *good[1:], d["ws"])
     with pytest.raises(P.PillarError):
         P.pillar_prompt_attn(c.shape, *good, d["ws"][:256])
+
+
+@pytest.mark.gpu
+def test_a_wait_that_runs_out_is_flagged_and_the_next_call_is_right():
+    """With a bound of a microsecond, less than any tile takes from memory, some wait of the pipeline gives up: the call
+    returns with PILLAR_FLAG_TIMEOUT, and the next one on the same buffers, with the default bound, is whole."""
+    c = Case(90, 8, 2, 128, [700, 300, 513])
+    d = c.device()
+    c.shape.wait_timeout_us = 1
+    c.call(d)
+    assert P.pillar_get_error(d["ws"]) == P.FLAG_TIMEOUT
+    c.shape.wait_timeout_us = 0
+    d["out"].fill_(0x7fc1)
+    d["lse"].fill_(SENTINEL)
+    c.call(d)
+    c.check(d)
