@@ -35,7 +35,8 @@ constexpr int kPerThread = 2;      // requests a scan thread takes
 constexpr int kExpandThreads = 256;
 constexpr int kBlock = PILLAR_KV_BLOCK;
 
-__device__ __forceinline__ int blocks_of(int len) { return (len + kBlock - 1) / kBlock; }
+// (len + 15 would pass 31 bits for the longest lengths)
+__device__ __forceinline__ int blocks_of(int len) { return len / kBlock + (len % kBlock != 0); }
 
 __device__ __forceinline__ long long warp_scan(long long x) {
 #pragma unroll

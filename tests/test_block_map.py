@@ -212,3 +212,20 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
         P.pillar_block_map(s, *good[:2], torch.zeros((2, 8), **i32)[:, ::2], *good[3:])
     with pytest.raises(P.PillarError):
         P.pillar_block_map(s, *good[:10], ws[:256])
+
+
+@pytest.mark.gpu
+def test_lengths_up_to_the_largest_int():
+    """A length whose rounding up to whole blocks passes 31 bits needs more blocks than any pool has: refused, nothing taken."""
+    most, B = 2 ** 31 - 1, 2
+    s = shape_of(B, 10, most)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros((B, 2 ** 27), dtype=torch.int32, device="cuda")
+    ring, state, granted = i32(list(range(10))), i32([0, 10]), i32([SENTINEL] * B)
+    kv_off, new_off = torch.zeros(B + 1, dtype=torch.int64, device="cuda"), i32([0] * (B + 1))
+    slots, new = i32([SENTINEL] * 64), i32([SENTINEL] * 64)
+    ws = torch.empty(P.pillar_block_map_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    P.pillar_block_map(s, i32([20, most]), i32([0, 0]), table, ring, state, granted, kv_off, slots, new_off, new, ws)
+    assert P.pillar_get_error(ws) == P.FLAG_BLOCK
+    assert granted.tolist() == [20, 0] and state.tolist() == [2, 8] and kv_off.tolist() == [0, 20, 20]
+    assert slots.tolist()[:21] == list(range(20)) + [SENTINEL] and table[:, :3].tolist() == [[0, 1, 0], [0, 0, 0]]
