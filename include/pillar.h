@@ -598,7 +598,8 @@ PILLAR_API int pillar_block_map_workspace_bytes(const pillar_shape_t *shape, siz
  *                slot -1 (PILLAR_FLAG_SLOT).
  * Only shape->B, max_len and num_slots are used (the whole shape is checked).
  * All arrays are device memory, 4-byte aligned (kv_off 8, slot_table 16) and
- * must not overlap.  Asynchronous on `stream`; allocates nothing.  Returns
+ * must not overlap (granted_len in the place of prev_len or req_len is
+ * PILLAR_ERR_ARG).  Asynchronous on `stream`; allocates nothing.  Returns
  * PILLAR_OK, PILLAR_ERR_ARG, PILLAR_ERR_WORKSPACE or PILLAR_ERR_CUDA.
  */
 PILLAR_API int pillar_block_map(const pillar_shape_t *shape, const int32_t *req_len, const int32_t *prev_len,

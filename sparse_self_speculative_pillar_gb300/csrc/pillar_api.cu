@@ -433,6 +433,8 @@ int pillar_block_map(const pillar_shape_t *shape, const int32_t *req_len, const 
         !aligned(free_state, 4) || !aligned(granted_len, 4) || !aligned(slot_table, 16) || !aligned(new_slots, 4))
         return PILLAR_ERR_ARG;
     if (!workspace || !aligned(workspace, 256) || ws_bytes < map_ws_bytes(shape->B)) return PILLAR_ERR_WORKSPACE;
+    // (the lengths granted and those before are both read after the first are written)
+    if (shape->B > 0 && (granted_len == prev_len || granted_len == req_len)) return PILLAR_ERR_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (shape->B == 0) {  // an empty batch: its offsets are one zero each
         if (cudaMemsetAsync(workspace, 0, sizeof(int), cs) != cudaSuccess ||

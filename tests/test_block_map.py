@@ -229,3 +229,13 @@ def test_lengths_up_to_the_largest_int():
     assert P.pillar_get_error(ws) == P.FLAG_BLOCK
     assert granted.tolist() == [20, 0] and state.tolist() == [2, 8] and kv_off.tolist() == [0, 20, 20]
     assert slots.tolist()[:21] == list(range(20)) + [SENTINEL] and table[:, :3].tolist() == [[0, 1, 0], [0, 0, 0]]
+
+
+def test_granted_lengths_in_the_place_of_the_lengths_read_are_refused():
+    lib, s = P.load(), shape_of(2, 8, 64)
+    at = [ctypes.c_void_p(256 * (i + 1)) for i in range(16)]
+    args = [at[0], at[1], at[2], 4, at[3], at[4], at[5], at[6], at[7], 64, at[8], at[9], 64, at[10], 1 << 20, None]
+    for other in (0, 1):
+        wrong = list(args)
+        wrong[6] = wrong[other]
+        assert lib.pillar_block_map(ctypes.byref(s), *wrong) == -1
