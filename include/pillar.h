@@ -710,9 +710,9 @@ PILLAR_API int pillar_prompt_attn_workspace_bytes(const pillar_shape_t *shape, i
  *   n             tokens in q, k, v, out and lse
  *   seq_off       [B+1] int32, ascending, within [0, n].  A sequence whose
  *                 offsets descend, leave [0, n] or are more than max_len apart
- *                 is skipped (PILLAR_FLAG_REQUEST); so is what exceeds the
- *                 workspace when sequences overlap.  Empty ones are allowed.
- *                 Rows of no sequence are left as they were.
+ *                 is skipped (PILLAR_FLAG_REQUEST); so are all when they
+ *                 overlap by more than the workspace has room for.  Empty ones
+ *                 are allowed.  Rows of no sequence are left as they were.
  *   out           [n, Hq, D] bf16
  *   lse           [n, Hq] fp32, or NULL
  *   workspace     pillar_prompt_attn_workspace_bytes bytes, 256-byte aligned; its

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
     __shared__ int s_bin[kLevels];
     __shared__ int s_warp[32];
     __shared__ int s_bad;
+    __shared__ long long s_tiles[32];
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
     if (tid == 0) s_bad = 0;
     __syncthreads();
     // bin of tile i of a sequence: larger i first
-    const int most = (max_len + rows - 1) / rows;
+    const int most = (min(max_len, n) - 1) / rows + 1;
     int shift = 0;
     while ((most >> shift) >= kLevels) ++shift;
     auto level = [&](int i) { return kLevels - 1 - (i >> shift); };
@@ -63,14 +64,27 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
         }
         *first = lo;
         *len = hi - lo;
-        return (hi - lo + rows - 1) / rows;
+        return (hi - lo) / rows + ((hi - lo) % rows != 0);
     };
     int first = 0, len = 0;
-    for (int b = wid; b < B; b += 32) {
+    long long mine = 0;  // tiles of this warp's sequences
+    for (int b = wid; b < B && mine <= room; b += 32) {
         const int nt = tiles_of(b, &first, &len);
-        for (int i = lane; i < nt; i += 32) atomicAdd(&s_bin[level(i)], 1);
+        mine += nt;
+        for (int i = lane; i < nt && mine <= room; i += 32) atomicAdd(&s_bin[level(i)], 1);
     }
+    if (lane == 0) s_tiles[wid] = mine;
     __syncthreads();
+    const long long part = s_tiles[lane];
+    const long long total = ((long long)__reduce_add_sync(0xffffffffu, (unsigned)(part >> 16)) << 16) +
+                            __reduce_add_sync(0xffffffffu, (unsigned)part & 0xffffu);
+    if (total > room) {  // only sequences that overlap list more than there is room for
+        if (tid == 0) {
+            hdr->num_tiles = 0;
+            hdr->err = PILLAR_FLAG_REQUEST;
+        }
+        return;
+    }
     const int own = s_bin[tid];
     int x = own;
 #pragma unroll
@@ -80,23 +94,18 @@ __global__ void __launch_bounds__(kPlanThreadsP) prompt_plan(const int *seq_off,
     }
     if (lane == 31) s_warp[wid] = x;
     __syncthreads();
-    int before = 0;
-    for (int i = 0; i < wid; ++i) before += s_warp[i];
+    const int before = (int)__reduce_add_sync(0xffffffffu, lane < wid ? (unsigned)s_warp[lane] : 0u);
     s_bin[tid] = before + x - own;
     __syncthreads();
     for (int b = wid; b < B; b += 32) {
         const int nt = tiles_of(b, &first, &len);
         for (int i = lane; i < nt; i += 32) {
-            const int at = atomicAdd(&s_bin[level(i)], 1);
-            if (at < room) tiles[at] = PromptTile{first, len, i, 0};
-            else s_bad = PILLAR_FLAG_REQUEST;  // (overlapping sequences list more than there is room for)
+            tiles[atomicAdd(&s_bin[level(i)], 1)] = PromptTile{first, len, i, 0};
         }
     }
     __syncthreads();
     if (tid == 0) {
-        int total = 0;
-        for (int i = 0; i < 32; ++i) total += s_warp[i];
-        hdr->num_tiles = min(total, room);
+        hdr->num_tiles = (int)total;
         hdr->err = s_bad;
     }
 }
@@ -144,6 +153,27 @@ struct BoundsP {
 };
 __device__ __forceinline__ bool waitp(uint64_t *bar, uint32_t parity, const BoundsP &b) {
     return mbar_wait(bar, parity, b.abort, b.err, b.ns);
+}
+// The same for a whole warp, whose lanes have to go the same way, since what follows is done by the warp as one.  They test
+// the barrier in one instruction; a phase that one lane has seen complete is complete for the others' next test, because it
+// cannot end again without this warp; and giving up is put to the vote of those still waiting.  (A vote after every wait
+// instead took 3 to 5 % of the long prompts' time.)
+__device__ __forceinline__ bool waitw(uint64_t *bar, uint32_t parity, const BoundsP &b) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    const uint32_t cadence = b.ns < 1000000ull ? 0u : 63u;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & cadence) == 0) {
+            const bool over = global_timer_ns() - t0 > b.ns;
+            const unsigned waiting = __activemask();
+            if (__any_sync(waiting, over || *b.abort)) {
+                if (__any_sync(waiting, over)) atomicOr(b.err, PILLAR_FLAG_TIMEOUT);
+                *b.abort = 1;
+                return false;
+            }
+        }
+    }
 }
 // Bounded wait for copies or products already in flight, whatever the pipeline's bound and the abort flag say.
 __device__ __forceinline__ void drainp(uint64_t *bar, uint32_t parity) {
@@ -294,10 +324,10 @@ __device__ void mma_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd,
         const int nk = u.nk();
         uint32_t ph;
         int s = slot_of(0, &ph);
-        bool ok = waitp(&sm.kvfull[s], ph, bd);
+        bool ok = waitw(&sm.kvfull[s], ph, bd);
         for (int b = 0; b < 2 && ok; ++b) {
             if (!u.of(b)) continue;
-            ok = waitp(&sm.qfull[b], qph[b], bd);
+            ok = waitw(&sm.qfull[b], qph[b], bd);
             if (!ok) break;
             qph[b] ^= 1;
             tc_fence_after();
@@ -311,7 +341,7 @@ __device__ void mma_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd,
         if (ok && elect_one()) umma_commit(&sm.kvempty[s]);
         for (int j = 0; j < nk && ok; ++j) {
             const int vs = slot_of(2 * j + 1, &ph);
-            ok = waitp(&sm.kvfull[vs], ph, bd);
+            ok = waitw(&sm.kvfull[vs], ph, bd);
             if (!ok) break;
             const int tail = u.len - j * kTileP;  // keys of the sequence in this tile
             if (tail < kTileP) {
@@ -327,11 +357,11 @@ __device__ void mma_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd,
             for (int b = 0; b < 2 && ok; ++b) {
                 if (j >= u.of(b)) continue;
                 if (j == 0) {  // O of this row tile has been read out
-                    ok = waitp(&sm.ofree[b], oph[b] ^ 1, bd);
+                    ok = waitw(&sm.ofree[b], oph[b] ^ 1, bd);
                     if (!ok) break;
                     oph[b] ^= 1;
                 }
-                ok = waitp(&sm.pfull[b], pph[b], bd);
+                ok = waitw(&sm.pfull[b], pph[b], bd);
                 if (!ok) break;
                 pph[b] ^= 1;
                 tc_fence_after();
@@ -341,7 +371,7 @@ __device__ void mma_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd,
                 }
                 if (j + 1 < u.of(b)) {
                     if (!have_k) {
-                        ok = waitp(&sm.kvfull[ks], ph, bd);
+                        ok = waitw(&sm.kvfull[ks], ph, bd);
                         if (!ok) break;
                         have_k = true;
                         tc_fence_after();
@@ -419,7 +449,7 @@ __device__ void softmax_role(const PromptParams &p, SmemP<D> &sm, const BoundsP 
         float m = neg_inf(), l = 0.f;  // reference maximum (base 2, scaled) and sum
 #pragma unroll 1
         for (int j = 0; j < nk; ++j, ++n) {
-            if (!waitp(&sm.sfull[b], n & 1, bd)) return;
+            if (!waitw(&sm.sfull[b], n & 1, bd)) return;
             tc_fence_after();
             float s[kTileP];
 #pragma unroll
@@ -449,7 +479,7 @@ __device__ void softmax_role(const PromptParams &p, SmemP<D> &sm, const BoundsP 
                 grow = true;
             }
             if (__any_sync(0xffffffffu, grow)) {  // (a row grows only behind an earlier tile's P V)
-                if (!waitp(&sm.pvdone[b], (n - 1) & 1, bd)) return;
+                if (!waitw(&sm.pvdone[b], (n - 1) & 1, bd)) return;
                 tc_fence_after();
                 rescale_row<D>(tO, f);
             }
@@ -475,7 +505,7 @@ __device__ void softmax_role(const PromptParams &p, SmemP<D> &sm, const BoundsP 
             if (lane == 0) mbar_arrive(&sm.pfull[b]);
         }
         // the unit's rows
-        if (!waitp(&sm.pvdone[b], (n - 1) & 1, bd)) return;
+        if (!waitw(&sm.pvdone[b], (n - 1) & 1, bd)) return;
         tc_fence_after();
         const int i0 = u.q0 + b * u.dq + (warp & 3) * 32, left = u.len - i0;  // this warp's first row; rows from there on
         const int h = u.h + b * u.dh;

@@ -279,3 +279,28 @@ def test_a_wait_that_runs_out_is_flagged_and_the_next_call_is_right():
     d["lse"].fill_(SENTINEL)
     c.call(d)
     c.check(d)
+
+
+@pytest.mark.gpu
+def test_a_largest_length_beyond_every_sequence():
+    c = Case(91, 4, 1, 64, [700, 40, 1200])
+    c.shape.max_len = 2 ** 31 - 1
+    d = c.device()
+    c.call(d)
+    c.check(d)
+
+
+@pytest.mark.gpu
+def test_sequences_that_overlap_beyond_the_workspace_are_skipped():
+    """Offsets up and down again: every other sequence is all of the rows, far more tiles than n rows can have."""
+    c = Case(92, 2, 1, 64, [20] * 64)
+    off = np.zeros(65, np.int64)
+    off[1::2] = c.off[-1]
+    d = c.device()
+    d["off"].copy_(torch.tensor(off, dtype=torch.int32))
+    c.call(d)
+    assert P.pillar_get_error(d["ws"]) == P.FLAG_REQUEST
+    assert torch.all(d["out"] == 0x7fc1) and torch.all(d["lse"] == SENTINEL)
+    d["off"].copy_(torch.tensor(c.off, dtype=torch.int32))
+    c.call(d)
+    c.check(d)
