@@ -17,10 +17,11 @@
 //     (mma with e4m3 operands would take the codes as they are, but this GPU
 //     converts them to f16 inside the instruction, for every use: measured 590 to
 //     700 pairs a cycle and SM with operands that change, 960 with f16 ones; a
-//     kernel on it took 448 us where this one takes the time stated below.
-//     tcgen05 has native e4m3, but 64 or 128 rows at a time, with scores and
-//     probabilities passing through tensor memory; a draft request has at most
-//     eight rows, and a tile's bytes arrive every 0.36 us.)
+//     kernel on it took 447 us where this one takes 234.  tcgen05 takes the codes
+//     as they are, with the keys on its M and queries and probabilities split into
+//     two and three e4m3 values: a kernel of specialised warps on it took 250 us,
+//     and 202 for the second batch below; its roles' code did not fit the
+//     instruction cache together, and it is not kept.)
 //   * The keys are the m of m16n8k16, the query rows its n: S^T = K Q^T and
 //     O^T = V^T P^T.  A tile of eight rows wastes little, its O^T is 32 registers a
 //     lane, and above all an operand made of K or V serves every row tile of its
@@ -46,8 +47,11 @@
 // through shared memory at the item's end; meanwhile the other CTA's loads keep
 // coming.  (The time of a step is the latency of its chain of conversions, products
 // and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row tiles
-// hide it better than eight warps of three or four, which one CTA with a loader warp
-// of its own had; 448 against 470 us, and one loader warp was the limit next.)
+// hide it better than eight to twelve of three, which one CTA with loader warps of its
+// own had: 345 us against 234.)
+// Measured (32 heads on 8, D = 128): 64 single rows over contexts of 1000 to 30000
+// tokens 234 us, 4.2 TB/s of cache or 0.62 of a copy's rate; 128 requests with contexts of
+// 6144 to 10240, one ninth of them verify with 9 tokens, 254 us, 0.28.
 #include "pillar_device.cuh"
 
 namespace pillar {

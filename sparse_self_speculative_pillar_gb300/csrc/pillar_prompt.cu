@@ -23,7 +23,11 @@
 //     through a 4 KB buffer a warp, so that eight lanes store 128 bytes of a row (each
 //     lane storing its own row, 16 bytes at a time, took 3000 to 4400 cycles a unit).
 // What bounds it: the tensor cores (4 D flops a visible pair; half of the diagonal
-// tile is computed and masked).  Keys behind a sequence's end lie in the next one:
+// tile is computed and masked): 16384 tokens, 32 heads on 8, D = 128 take 1481 us,
+// 1.49 PFLOP/s of visible pairs, 0.79 of a library matrix product's rate; S reads both operands
+// from shared memory.  Short sequences (24 of 1 to 2047 tokens, the same heads: 73 us) are
+// bound by each unit's ends, D = 64 (12 of 300 to 4100, four heads on one: 55 us) by
+// the exponentials.  Keys behind a sequence's end lie in the next one:
 // their scores are behind the diagonal for every row that counts, and their values
 // are zeroed in shared memory, since 0 * NaN would carry over.
 #include <cuda.h>  // CUtensorMap
