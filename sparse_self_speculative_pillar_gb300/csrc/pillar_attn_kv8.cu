@@ -125,14 +125,19 @@ struct Smem8 {
     int item;                          // index of the item after this one
 };
 
-// How an item's row tiles and keys are shared out: groups of `share` warps, `tiles` row tiles each.
+// How an item's row tiles are shared out: `groups` of warps, `tiles` row tiles each (the last may have fewer).  A group's
+// warps share the keys; three groups have three, three and two of them.
 struct Split {
-    int tiles, share;
+    int tiles, groups;
+    uint32_t firsts, owners;  // four bits each: a group's first warp, a warp's group
+    __device__ __forceinline__ int first(int gr) const { return (firsts >> (4 * gr)) & 15; }
+    __device__ __forceinline__ int of(int warp) const { return (owners >> (4 * warp)) & 15; }
 };
+static_assert(kWarps8 == 8 && kMaxRows == 64 && kWarpTiles == 2, "one to four groups of eight warps");
 __device__ __forceinline__ Split split_of(int rows) {
-    const int nrt = (rows + 7) / 8;
-    if (nrt <= 2) return {nrt, kWarps8};
-    return nrt <= 4 ? Split{2, kWarps8 / 2} : Split{2, kWarps8 / 4};
+    if (rows <= 16) return {rows <= 8 ? 1 : 2, 1, 0x80u, 0u};
+    if (rows <= 32) return {2, 2, 0x840u, 0x11110000u};
+    return rows <= 48 ? Split{2, 3, 0x8630u, 0x22111000u} : Split{2, 4, 0x86420u, 0x33221100u};
 }
 
 // Byte offset of 16-byte chunk c of row r.  K: the two rows that eight lanes read together differ in bit 1
@@ -560,11 +565,12 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         Part pt;
         pt.rows = w.verify ? p.M : p.G;
         const Split sp = split_of(pt.rows);
-        pt.share = sp.share;
-        pt.kg = warp & (sp.share - 1);
-        pt.row0 = warp / sp.share * sp.tiles * 8;
+        const int gr = sp.of(warp);
+        pt.kg = warp - sp.first(gr);
+        pt.share = sp.first(gr + 1) - sp.first(gr);
+        pt.row0 = gr * sp.tiles * 8;
         pt.sure = w.verify ? w.L - (p.k + 1) : 0x7fffffff;
-        if (warp < kWarps8 / sp.share * sp.tiles) stage_queries<D>(p, w, sm, warp, pt.rows);
+        if (warp < sp.groups * sp.tiles) stage_queries<D>(p, w, sm, warp, pt.rows);  // (rows of the groups' last tiles that there are not, too)
         __syncthreads();
         Acc<D> a;
         a.wsc = 0x1p126f;
@@ -582,7 +588,6 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a.o[t][i][e] = 0.f;
         }
-        const bool active = pt.row0 < pt.rows;
         const uint2(*q)[D / 16][32] = &sm.q[pt.row0 / 8];
         const RowInfo *rinfo = sm.rows + pt.row0;
         const bool dump = w.verify && p.logits;
@@ -605,18 +610,16 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 blk_r = block(pos_b);
                 pos_b = position(t + 5);
             }
-            if (active) {
 #pragma unroll 1
-                for (int q16 = pt.kg; q16 < kStep / 16; q16 += pt.share) {
-                    const int k0 = t * kStep + 16 * q16;
-                    if (k0 >= w.n) break;
-                    const unsigned vis = (sm.mask[t % kPairs][q16 >> 1] >> (16 * (q16 & 1))) & 0xffffu;
-                    const int pos0 = w.verify ? w.begin + k0 : 0;
-                    const bool all = vis == 0xffffu && (!w.verify || pos0 + 15 <= pt.sure);
-                    const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages8];
-                    if (sp.tiles == 1) keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
-                    else keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
-                }
+            for (int q16 = pt.kg; q16 < kStep / 16; q16 += pt.share) {
+                const int k0 = t * kStep + 16 * q16;
+                if (k0 >= w.n) break;
+                const unsigned vis = (sm.mask[t % kPairs][q16 >> 1] >> (16 * (q16 & 1))) & 0xffffu;
+                const int pos0 = w.verify ? w.begin + k0 : 0;
+                const bool all = vis == 0xffffu && (!w.verify || pos0 + 15 <= pt.sure);
+                const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages8];
+                if (sp.tiles == 1) keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
+                else keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
             }
         }
         if (tid == 0 && sm.item < num_items) {  // (a short item: the rest of the next one's records)
@@ -655,23 +658,22 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
             }
             __syncthreads();
             constexpr int C4 = D / 4;  // four dimensions a thread
-            const int groups = kWarps8 / pt.share;
-            for (int x = tid; x < groups * 8 * C4; x += kThreads8) {
+            for (int x = tid; x < sp.groups * 8 * C4; x += kThreads8) {
                 const int gr = x / (8 * C4), y = x - gr * 8 * C4, lr = y / C4, d = (y - lr * C4) * 4;
-                const int row = (gr * sp.tiles + t) * 8 + lr, w0 = gr * pt.share;
+                const int row = (gr * sp.tiles + t) * 8 + lr, w0 = sp.first(gr), share = sp.first(gr + 1) - w0;
                 if (row >= pt.rows) continue;
                 float mx = neg_inf(), l = 0.f;
-                for (int s = 0; s < pt.share; ++s) mx = fmaxf(mx, smx[w0 + s][lr]);
+                for (int s = 0; s < share; ++s) mx = fmaxf(mx, smx[w0 + s][lr]);
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (mx > neg_inf()) {
-                    for (int s = 0; s < pt.share; ++s) {
+                    for (int s = 0; s < share; ++s) {
                         const float f = ex2_approx((smx[w0 + s][lr] - mx) * kLog2e);
                         const float4 o = *reinterpret_cast<const float4 *>(&so[w0 + s][lr][d]);
                         l += f * sl[w0 + s][lr];
                         v.x += f * o.x, v.y += f * o.y, v.z += f * o.z, v.w += f * o.w;
                     }
                 } else {
-                    for (int s = 0; s < pt.share; ++s) l += sl[w0 + s][lr];  // 0, or a NaN
+                    for (int s = 0; s < share; ++s) l += sl[w0 + s][lr];  // 0, or a NaN
                 }
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
