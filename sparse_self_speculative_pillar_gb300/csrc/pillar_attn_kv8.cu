@@ -17,10 +17,10 @@
 //     (mma with e4m3 operands would take the codes as they are, but this GPU
 //     converts them to f16 inside the instruction, for every use: measured 590 to
 //     700 pairs a cycle and SM with operands that change, 960 with f16 ones; a
-//     kernel on it took 447 us where this one takes 234.  tcgen05 takes the codes
+//     kernel on it took 447 us where this one takes 238.  tcgen05 takes the codes
 //     as they are, with the keys on its M and queries and probabilities split into
 //     two and three e4m3 values: a kernel of specialised warps on it took 250 us,
-//     and 202 for the second batch below; its roles' code did not fit the
+//     and 202 for the second batch below (this one: 237); its roles' code did not fit the
 //     instruction cache together, and it is not kept.)
 //   * The keys are the m of m16n8k16, the query rows its n: S^T = K Q^T and
 //     O^T = V^T P^T.  A tile of eight rows wastes little, its O^T is 32 registers a
@@ -43,15 +43,16 @@
 //     a vote of the warp finds out: no reductions on most steps.
 // Two CTAs of eight warps per SM work through items of the planner's queue, 128
 // keys at a time out of a ring of 64-key stages that all threads fill.  The warps
-// share an item's row tiles, up to two each, and its keys, 16 at a time, and join
+// share an item's row tiles, two each, and its keys, 16 at a time, and join
 // through shared memory at the item's end; meanwhile the other CTA's loads keep
-// coming.  (The time of a step is the latency of its chain of conversions, products
+// coming.  (Five or six row tiles are three groups of three, three and two warps: in
+// four groups of two, one of them idle, the second batch below took 254 us.)  (The time of a step is the latency of its chain of conversions, products
 // and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row tiles
 // hide it better than eight to twelve of three, which one CTA with loader warps of its
-// own had: 345 us against 234.)
+// own had: 345 us against 238.)
 // Measured (32 heads on 8, D = 128): 64 single rows over contexts of 1000 to 30000
-// tokens 234 us, 4.2 TB/s of cache or 0.62 of a copy's rate; 128 requests with contexts of
-// 6144 to 10240, one ninth of them verify with 9 tokens, 254 us, 0.28.
+// tokens 238 us, 4.1 TB/s of cache or 0.61 of a copy's rate; 128 requests with contexts of
+// 6144 to 10240, one ninth of them verify with 9 tokens, 237 us, 0.30.
 #include "pillar_device.cuh"
 
 namespace pillar {
@@ -125,19 +126,18 @@ struct Smem8 {
     int item;                          // index of the item after this one
 };
 
-// How an item's row tiles are shared out: `groups` of warps, `tiles` row tiles each (the last may have fewer).  A group's
-// warps share the keys; three groups have three, three and two of them.
+// How an item's row tiles are shared out: `groups` of warps, `tiles` row tiles each.  A group's warps share the keys; of
+// three groups the last has two warps, the others three.
 struct Split {
     int tiles, groups;
-    uint32_t firsts, owners;  // four bits each: a group's first warp, a warp's group
-    __device__ __forceinline__ int first(int gr) const { return (firsts >> (4 * gr)) & 15; }
-    __device__ __forceinline__ int of(int warp) const { return (owners >> (4 * warp)) & 15; }
+    __device__ __forceinline__ int of(int warp) const { return warp * groups / kWarps8; }
+    __device__ __forceinline__ int first(int gr) const { return groups == 3 ? 3 * gr : gr * (kWarps8 / groups); }
+    __device__ __forceinline__ int warps(int gr) const { return groups == 3 ? (gr == 2 ? 2 : 3) : kWarps8 / groups; }
 };
 static_assert(kWarps8 == 8 && kMaxRows == 64 && kWarpTiles == 2, "one to four groups of eight warps");
 __device__ __forceinline__ Split split_of(int rows) {
-    if (rows <= 16) return {rows <= 8 ? 1 : 2, 1, 0x80u, 0u};
-    if (rows <= 32) return {2, 2, 0x840u, 0x11110000u};
-    return rows <= 48 ? Split{2, 3, 0x8630u, 0x22111000u} : Split{2, 4, 0x86420u, 0x33221100u};
+    const int nrt = (rows + 7) / 8;
+    return {min(nrt, kWarpTiles), (nrt + kWarpTiles - 1) / kWarpTiles};
 }
 
 // Byte offset of 16-byte chunk c of row r.  K: the two rows that eight lanes read together differ in bit 1
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         const Split sp = split_of(pt.rows);
         const int gr = sp.of(warp);
         pt.kg = warp - sp.first(gr);
-        pt.share = sp.first(gr + 1) - sp.first(gr);
+        pt.share = sp.warps(gr);
         pt.row0 = gr * sp.tiles * 8;
         pt.sure = w.verify ? w.L - (p.k + 1) : 0x7fffffff;
         if (warp < sp.groups * sp.tiles) stage_queries<D>(p, w, sm, warp, pt.rows);  // (rows of the groups' last tiles that there are not, too)
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
             constexpr int C4 = D / 4;  // four dimensions a thread
             for (int x = tid; x < sp.groups * 8 * C4; x += kThreads8) {
                 const int gr = x / (8 * C4), y = x - gr * 8 * C4, lr = y / C4, d = (y - lr * C4) * 4;
-                const int row = (gr * sp.tiles + t) * 8 + lr, w0 = sp.first(gr), share = sp.first(gr + 1) - w0;
+                const int row = (gr * sp.tiles + t) * 8 + lr, w0 = sp.first(gr), share = sp.warps(gr);
                 if (row >= pt.rows) continue;
                 float mx = neg_inf(), l = 0.f;
                 for (int s = 0; s < share; ++s) mx = fmaxf(mx, smx[w0 + s][lr]);
