@@ -281,3 +281,55 @@ def test_a_step_captured_whole_and_replayed():
             assert torch.equal(made[0][n], made[1][n]), n
         for lp in (eager, graph):
             assert P.pillar_get_error(lp.map_ws) == 0 and P.pillar_get_error(lp.ws) == 0 and int(lp.flags) == 0
+
+
+def test_pools_and_strides_past_32_bits():
+    """The same blocks at the start of a small pool and at the end of one of 5 GB; the same prompt rows packed and 8 MB apart."""
+    heads, dim, lens, far = 8, 128, [300, 130, 77], 300000
+    g = np.random.default_rng(5)
+    n, nb = sum(lens), [-(-x // 16) for x in lens]
+    near = sum(nb)
+    rowset = lambda h: torch.from_numpy(f32_to_bf16_bits(g.standard_normal((n, h, dim)).astype(np.float32)).view(np.int16)).cuda()  # noqa: E731
+    k, v, q = rowset(heads), rowset(heads), rowset(16)
+    off, length = dev(np.concatenate([[0], np.cumsum(lens)]), torch.int32), dev(lens, torch.int32)
+    mode, lists = dev([1, 0, 1], torch.int32), dev(g.integers(0, 130, (3, heads, 40)), torch.int32)
+    q8 = q[:2 * 4 + 1].contiguous()
+    results = []
+    for blocks in (near, far):
+        table = np.full((3, max(nb)), -1)
+        at = blocks - near
+        for b in range(3):
+            table[b, :nb[b]] = np.arange(at, at + nb[b])
+            at += nb[b]
+        s = P.make_shape(B=3, Hq=16, Hkv=heads, D=dim, k=3, max_sparse=40, max_len=300, num_slots=blocks * 16)
+        k8, v8 = (torch.empty((blocks, heads, 16, dim), dtype=torch.uint8, device="cuda") for _ in "kv")
+        ks, vs = (torch.empty((blocks, heads), device="cuda") for _ in "kv")
+        t, flags = dev(table, torch.int32), dev([0], torch.int32)
+        P.pillar_kv8_append(s, k, v, length, off, t, k8, v8, ks, vs, flags)
+        out, lse = torch.zeros_like(q8), torch.zeros((2, 16, 4), device="cuda")
+        logits = torch.zeros(16 * 4 * (lens[0] + lens[2]), device="cuda")
+        ws = torch.empty(P.pillar_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+        P.pillar_attn_kv8(s, q8, k8, v8, ks, vs, t, mode, length, lists, dev(np.full((3, heads), 40), torch.int32), out, logits, lse, ws)
+        assert int(flags) == 0 and P.pillar_get_error(ws) == 0
+        results.append((ks[blocks - near:].clone(), out, logits, lse))
+        del k8, v8, ks, vs
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    s, stride = PA.shape_of(3, 16, heads, dim, 300), 1 << 22
+    ws = torch.empty(P.pillar_prompt_attn_workspace_bytes(s, n), dtype=torch.uint8, device="cuda")
+    outs = []
+    for apart in (False, True):
+        rows3 = []
+        for x in (q, k, v):
+            if apart:
+                wide = torch.empty((n - 1) * stride + x.shape[1] * dim, dtype=torch.int16, device="cuda")
+                y = wide.as_strided(x.shape, (stride, dim, 1))
+                y.copy_(x)
+                x = y
+            rows3.append(x)
+        out, lse = torch.zeros((n, 16, dim), dtype=torch.int16, device="cuda"), torch.zeros((n, 16), device="cuda")
+        P.pillar_prompt_attn(s, *rows3, off, out, lse, ws)
+        assert P.pillar_get_error(ws) == 0
+        outs.append((out, lse))
+        del rows3
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
