@@ -64,6 +64,7 @@ constexpr int kWarps8 = kThreads8 / 32;
 constexpr int kStages8 = 5;         // 64-key stages: two being read, three in flight
 constexpr int kStep = 128;          // keys between two barriers
 constexpr int kPairs = 4;           // steps whose rows are resolved ahead
+constexpr int kLead = 4;            // steps before its end at which an item's successor is taken from the queue
 constexpr int kMaxTiles = kMaxRows / 8;  // row tiles of an item
 constexpr int kWarpTiles = 2;       // row tiles of a warp, at most
 constexpr int kBlk = PILLAR_KV_BLOCK;
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         cp16(smem_u32(&sm.ahead.unit), p.unit + unit, 16);
         cp8(smem_u32(&sm.ahead.logit_off), p.logit_off + b);
     };
-    int done = 0;  // how far thread 0 is with the next item: 0 nothing, 1 its item record, 2 all of them
+    int next = 0, done = 0;  // how far thread 0 is with the next item: 0 nothing, 1 its index, 2 its item record, 3 all of them
     if (tid == 0) {
         const int it = atomicAdd(&p.hdr->item_counter, 1);
         sm.item = it;
@@ -474,7 +475,6 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
             copy_unit();
             cp_commit();
             cp_wait<0>();
-            done = 2;
         }
     }
     __syncthreads();
@@ -495,7 +495,6 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
             w.verify = n.req.mode == 1;
             w.logit_off = w.verify ? n.logit_off : 0;
             sm.w = w;
-            sm.item = atomicAdd(&p.hdr->item_counter, 1);  // the item after this one
             done = 0;
         }
         __syncthreads();
@@ -594,9 +593,10 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         for (int t = 0; t < steps; ++t) {
             cp_wait<1>();
             __syncthreads();  // stages 2t and 2t+1 are in shared memory, and those of step t-1 are free
-            if (tid == 0 && done < 2 && sm.item < num_items) {  // the next item's records, one link a step
-                if (done == 0) copy_item(sm.item);
-                else copy_unit();
+            // the next item, one link a step; not before it is needed, so that no item waits behind a long one
+            if (tid == 0 && t + kLead >= steps && done < 3) {
+                if (done == 0) next = atomicAdd(&p.hdr->item_counter, 1);
+                else if (next < num_items) done == 1 ? copy_item(next) : copy_unit();
                 ++done;
             }
 #pragma unroll
@@ -622,16 +622,19 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 else keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
             }
         }
-        if (tid == 0 && sm.item < num_items) {  // (a short item: the rest of the next one's records)
-            cp_wait<0>();
-            if (done == 0) {
-                copy_item(sm.item);
-                cp_commit();
+        if (tid == 0) {  // (a short item: the rest of the next one's records)
+            if (done == 0) next = atomicAdd(&p.hdr->item_counter, 1);
+            sm.item = next;
+            if (next < num_items) {
                 cp_wait<0>();
+                if (done <= 1) {
+                    copy_item(next);
+                    cp_commit();
+                    cp_wait<0>();
+                }
+                if (done <= 2) copy_unit();
+                cp_commit();
             }
-            if (done < 2) copy_unit();
-            done = 2;
-            cp_commit();
         }
         // --- the item's rows: the warps that shared the keys of a row tile join, one tile of each group at a time
         const float unw = 1.f / a.wsc;
