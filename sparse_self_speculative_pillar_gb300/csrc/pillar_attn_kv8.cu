@@ -123,8 +123,8 @@ struct Smem8 {
     int row[kPairs][kStep];            // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
     unsigned mask[kPairs][kStep / 32]; // which of 32 keys there are
     Ahead ahead;
-    Work w;
-    int item;                          // index of the item after this one
+    Work w[2];                         // this item and the next, in turn
+    int item;                          // index of the next one
 };
 
 // How an item's row tiles are shared out: `groups` of warps, `tiles` row tiles each.  A group's warps share the keys; of
@@ -463,6 +463,20 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         cp16(smem_u32(&sm.ahead.unit), p.unit + unit, 16);
         cp8(smem_u32(&sm.ahead.logit_off), p.logit_off + b);
     };
+    auto open_item = [&](Work &w) {  // from the records ahead
+        const Ahead &n = sm.ahead;
+        w.b = n.item.unit / p.Hkv;
+        w.g = n.item.unit - w.b * p.Hkv;
+        w.begin = n.item.begin;
+        w.n = n.item.end - n.item.begin;
+        w.L = n.req.len;
+        w.q_off = n.req.q_off;
+        w.vidx = n.req.vidx;
+        w.nsplit = n.unit.nsplit;
+        w.rec = n.unit.rec_base + n.item.split * n.unit.rec_rows;
+        w.verify = n.req.mode == 1;
+        w.logit_off = w.verify ? n.logit_off : 0;
+    };
     int next = 0, done = 0;  // how far thread 0 is with the next item: 0 nothing, 1 its index, 2 its item record, 3 all of them
     if (tid == 0) {
         const int it = atomicAdd(&p.hdr->item_counter, 1);
@@ -475,48 +489,40 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
             copy_unit();
             cp_commit();
             cp_wait<0>();
+            open_item(sm.w[0]);
         }
     }
     __syncthreads();
-    while (sm.item < num_items) {
-        __syncthreads();  // everyone has read the item's index
-        if (tid == 0) {
-            const Ahead &n = sm.ahead;
-            Work w;
-            w.b = n.item.unit / p.Hkv;
-            w.g = n.item.unit - w.b * p.Hkv;
-            w.begin = n.item.begin;
-            w.n = n.item.end - n.item.begin;
-            w.L = n.req.len;
-            w.q_off = n.req.q_off;
-            w.vidx = n.req.vidx;
-            w.nsplit = n.unit.nsplit;
-            w.rec = n.unit.rec_base + n.item.split * n.unit.rec_rows;
-            w.verify = n.req.mode == 1;
-            w.logit_off = w.verify ? n.logit_off : 0;
-            sm.w = w;
-            done = 0;
+    auto position = [&](const Work &w, int t) {  // of key tid of step t; -1: no such key
+        const int i = t * kStep + tid;
+        if (i >= w.n) return -1;
+        if (w.verify) return w.begin + i;
+        const int pos = __ldg(p.sparse_idx + ((size_t)w.b * p.Hkv + w.g) * p.max_sparse + w.begin + i);
+        if (pos < 0 || pos >= w.L) {
+            bad |= PILLAR_FLAG_INDEX;
+            return -1;
         }
-        __syncthreads();
-        const Work &w = sm.w;
+        return pos;
+    };
+    auto block = [&](const Work &w, int pos) {
+        return pos >= 0 && pos / kBlk < p.c.max_blocks ? __ldg(p.c.table + (size_t)w.b * p.c.max_blocks + pos / kBlk) : -1;
+    };
+    // the positions of an item's first steps: looked up while the item before is being joined
+    int pos[5];
+    const bool finds = tid < kStep;
+    auto positions = [&](const Work &w) {
+        const bool any = finds && sm.item < num_items;
+#pragma unroll
+        for (int t = 0; t < 5; ++t) pos[t] = any ? position(w, t) : -1;
+    };
+    positions(sm.w[0]);
+    for (int turn = 0; sm.item < num_items; turn ^= 1) {
+        const Work &w = sm.w[turn];
+        done = 0;
         const int steps = (w.n + kStep - 1) / kStep;
         // --- the loads.  Thread tid < 128 finds key tid of each step: its position, its block, its row of the
         // pools, one link of that chain a step, so that each has a step's time to arrive.  The rows go
         // through shared memory to the copies, in which the 16-byte pieces of a row belong to adjacent lanes.
-        auto position = [&](int t) {  // of key tid of step t; -1: no such key
-            const int i = t * kStep + tid;
-            if (i >= w.n) return -1;
-            if (w.verify) return w.begin + i;
-            const int pos = __ldg(p.sparse_idx + ((size_t)w.b * p.Hkv + w.g) * p.max_sparse + w.begin + i);
-            if (pos < 0 || pos >= w.L) {
-                bad |= PILLAR_FLAG_INDEX;
-                return -1;
-            }
-            return pos;
-        };
-        auto block = [&](int pos) {
-            return pos >= 0 && pos / kBlk < p.c.max_blocks ? __ldg(p.c.table + (size_t)w.b * p.c.max_blocks + pos / kBlk) : -1;
-        };
         auto resolve = [&](int t, int pos, int blk) {  // (the first four warps, whole)
             const bool ok = pos >= 0 && blk >= 0 && blk < p.c.num_blocks;
             if (pos >= 0 && !ok) bad |= PILLAR_FLAG_SLOT;
@@ -545,12 +551,10 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
             }
         };
         int pos_r = -1, blk_r = -1, pos_b = -1;
-        if (tid < kStep) {
-            int pos[5], blk[4];
+        if (finds) {
+            int blk[4];
 #pragma unroll
-            for (int t = 0; t < 5; ++t) pos[t] = position(t);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) blk[t] = block(pos[t]);
+            for (int t = 0; t < 4; ++t) blk[t] = block(w, pos[t]);
 #pragma unroll
             for (int t = 0; t < 3; ++t) resolve(t, pos[t], blk[t]);
             pos_r = pos[3], blk_r = blk[3], pos_b = pos[4];
@@ -604,11 +608,11 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 if (s < 2 * steps) fetch(s);
                 cp_commit();
             }
-            if (tid < kStep) {
+            if (finds) {
                 resolve(t + 3, pos_r, blk_r);
                 pos_r = pos_b;
-                blk_r = block(pos_b);
-                pos_b = position(t + 5);
+                blk_r = block(w, pos_b);
+                pos_b = position(w, t + 5);
             }
 #pragma unroll 1
             for (int q16 = pt.kg; q16 < kStep / 16; q16 += pt.share) {
@@ -634,6 +638,8 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 }
                 if (done <= 2) copy_unit();
                 cp_commit();
+                cp_wait<0>();
+                open_item(sm.w[turn ^ 1]);
             }
         }
         // --- the item's rows: the warps that shared the keys of a row tile join, one tile of each group at a time
@@ -642,10 +648,12 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         float(*smx)[8] = reinterpret_cast<float(*)[8]>(so + kWarps8), (*sl)[8] = smx + kWarps8;
         static_assert(sizeof(float) * kWarps8 * 8 * (D + 6) <= sizeof(sm.stage), "the join fits into the stages");
         cp_wait<0>();
+        __syncthreads();  // (the keys are done with, the next item is there)
+        positions(sm.w[turn ^ 1]);
 #pragma unroll
         for (int t = 0; t < kWarpTiles; ++t) {
             if (t >= sp.tiles) break;
-            __syncthreads();
+            if (t > 0) __syncthreads();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float *dst = &so[warp][2 * c + e][g * (D / 8)];
