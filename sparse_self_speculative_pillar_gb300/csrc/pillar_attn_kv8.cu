@@ -17,10 +17,10 @@
 //     (mma with e4m3 operands would take the codes as they are, but this GPU
 //     converts them to f16 inside the instruction, for every use: measured 590 to
 //     700 pairs a cycle and SM with operands that change, 960 with f16 ones; a
-//     kernel on it took 447 us where this one takes 238.  tcgen05 takes the codes
+//     kernel on it took 447 us where this one takes 233.  tcgen05 takes the codes
 //     as they are, with the keys on its M and queries and probabilities split into
 //     two and three e4m3 values: a kernel of specialised warps on it took 250 us,
-//     and 202 for the second batch below (this one: 237); its roles' code did not fit the
+//     and 202 for the second batch below (this one: 200); its roles' code did not fit the
 //     instruction cache together, and it is not kept.)
 //   * The keys are the m of m16n8k16, the query rows its n: S^T = K Q^T and
 //     O^T = V^T P^T.  A tile of eight rows wastes little, its O^T is 32 registers a
@@ -49,10 +49,11 @@
 // four groups of two, one of them idle, the second batch below took 254 us.)  (The time of a step is the latency of its chain of conversions, products
 // and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row tiles
 // hide it better than eight to twelve of three, which one CTA with loader warps of its
-// own had: 345 us against 238.)
+// own had: 345 us against 233.)
 // Measured (32 heads on 8, D = 128): 64 single rows over contexts of 1000 to 30000
-// tokens 238 us, 4.1 TB/s of cache or 0.61 of a copy's rate; 128 requests with contexts of
-// 6144 to 10240, one ninth of them verify with 9 tokens, 237 us, 0.30.
+// tokens 233 us, 4.2 TB/s of cache or 0.62 of a copy's rate (without the products 134 / 170 of
+// that, without the copies 145 / 170); 128 requests with contexts of 6144 to 10240, one ninth of
+// them verify with 9 tokens, 200 us, 0.36: the products' side alone is nearly all of it.
 #include "pillar_device.cuh"
 
 namespace pillar {
@@ -64,7 +65,8 @@ constexpr int kWarps8 = kThreads8 / 32;
 constexpr int kStages8 = 5;         // 64-key stages: two being read, three in flight
 constexpr int kStep = 128;          // keys between two barriers
 constexpr int kPairs = 4;           // steps whose rows are resolved ahead
-constexpr int kLead = 4;            // steps before its end at which an item's successor is taken from the queue
+constexpr int kLead = 3;            // steps before its end at which an item's successor is taken from the queue (at its start,
+                                    // it waits behind a long item: 237 us for the second batch above where this then took 214)
 constexpr int kMaxTiles = kMaxRows / 8;  // row tiles of an item
 constexpr int kWarpTiles = 2;       // row tiles of a warp, at most
 constexpr int kBlk = PILLAR_KV_BLOCK;
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         }
         const uint2(*q)[D / 16][32] = &sm.q[pt.row0 / 8];
         const RowInfo *rinfo = sm.rows + pt.row0;
-        const bool dump = w.verify && p.logits;
+        const bool dump = w.verify && p.logits, one = pt.rows - pt.row0 <= 8;
         for (int t = 0; t < steps; ++t) {
             cp_wait<1>();
             __syncthreads();  // stages 2t and 2t+1 are in shared memory, and those of step t-1 are free
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 const int pos0 = w.verify ? w.begin + k0 : 0;
                 const bool all = vis == 0xffffu && (!w.verify || pos0 + 15 <= pt.sure);
                 const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages8];
-                if (sp.tiles == 1) keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
+                if (one) keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
                 else keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
             }
         }
