@@ -45,15 +45,18 @@
 // keys at a time out of a ring of 64-key stages that all threads fill.  The warps
 // share an item's row tiles, two each, and its keys, 16 at a time, and join
 // through shared memory at the item's end; meanwhile the other CTA's loads keep
-// coming.  (Five or six row tiles are three groups of three, three and two warps: in
-// four groups of two, one of them idle, the second batch below took 254 us.)  (The time of a step is the latency of its chain of conversions, products
-// and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row tiles
-// hide it better than eight to twelve of three, which one CTA with loader warps of its
-// own had: 345 us against 233.)
+// coming.  Five or six row tiles are three groups of three, three and two warps (in
+// four groups of two, one of them idle, the second batch below took 254 us where
+// this took 237).  The time of a step is the latency of its chain of conversions,
+// products and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row
+// tiles hide it better than eight to twelve of three, which one CTA with loader warps
+// of its own had (345 us against 233).
 // Measured (32 heads on 8, D = 128): 64 single rows over contexts of 1000 to 30000
-// tokens 233 us, 4.2 TB/s of cache or 0.62 of a copy's rate (without the products 134 / 170 of
-// that, without the copies 145 / 170); 128 requests with contexts of 6144 to 10240, one ninth of
-// them verify with 9 tokens, 200 us, 0.36: the products' side alone is nearly all of it.
+// tokens 233 us, 4.2 TB/s of cache or 0.62 of a copy's rate; 128 requests with contexts
+// of 6144 to 10240, one ninth of them verify with 9 tokens, 200 us, 0.36.  Copies of this
+// kernel that leave out the products, or the copies, say which side it is: 134 and
+// 145 of 170 us for single rows over 4000 to 6000 tokens, 100 and 222 of 238 for the
+// second batch (before its last two steps).
 #include "pillar_device.cuh"
 
 namespace pillar {
