@@ -17,7 +17,7 @@
 //     (mma with e4m3 operands would take the codes as they are, but this GPU
 //     converts them to f16 inside the instruction, for every use: measured 590 to
 //     700 pairs a cycle and SM with operands that change, 960 with f16 ones; a
-//     kernel on it took 447 us where this one takes 233.  tcgen05 takes the codes
+//     kernel on it took 447 us where this one takes 211.  tcgen05 takes the codes
 //     as they are, with the keys on its M and queries and probabilities split into
 //     two and three e4m3 values: a kernel of specialised warps on it took 250 us,
 //     and 202 for the second batch below (this one: 200); its roles' code did not fit the
@@ -41,7 +41,8 @@
 //     least 2^7 for the row's largest probability at the largest scale.  A row's
 //     reference maximum moves only when a score passes it by more than 2^8, which
 //     a vote of the warp finds out: no reductions on most steps.
-// Two CTAs of eight warps per SM work through items of the planner's queue, 128
+// Two CTAs of eight warps per SM (three where items have at most eight rows: 211 us
+// against 233 for the first batch below) work through items of the planner's queue, 128
 // keys at a time out of a ring of 64-key stages that all threads fill.  The warps
 // share an item's row tiles, two each, and its keys, 16 at a time, and join
 // through shared memory at the item's end; meanwhile the other CTA's loads keep
@@ -50,13 +51,13 @@
 // this took 237).  The time of a step is the latency of its chain of conversions,
 // products and exponentials, about 3000 cycles for 32 keys: sixteen warps of two row
 // tiles hide it better than eight to twelve of three, which one CTA with loader warps
-// of its own had (345 us against 233).
+// of its own had (345 us against 233 with two CTAs).
 // Measured (32 heads on 8, D = 128): 64 single rows over contexts of 1000 to 30000
-// tokens 233 us, 4.2 TB/s of cache or 0.62 of a copy's rate; 128 requests with contexts
+// tokens 211 us, 4.6 TB/s of cache or 0.69 of a copy's rate; 128 requests with contexts
 // of 6144 to 10240, one ninth of them verify with 9 tokens, 200 us, 0.36.  Copies of this
 // kernel that leave out the products, or the copies, say which side it is: 134 and
-// 145 of 170 us for single rows over 4000 to 6000 tokens, 100 and 222 of 238 for the
-// second batch (before its last two steps).
+// 145 of 170 us for single rows over 4000 to 6000 tokens (two CTAs), 100 and 222 of 238
+// for the second batch (before its last two steps).
 #include "pillar_device.cuh"
 
 namespace pillar {
@@ -65,13 +66,19 @@ namespace {
 
 constexpr int kThreads8 = 256;
 constexpr int kWarps8 = kThreads8 / 32;
-constexpr int kStages8 = 5;         // 64-key stages: two being read, three in flight
 constexpr int kStep = 128;          // keys between two barriers
 constexpr int kPairs = 4;           // steps whose rows are resolved ahead
 constexpr int kLead = 3;            // steps before its end at which an item's successor is taken from the queue (at its start,
                                     // it waits behind a long item: 237 us for the second batch above where this then took 214)
-constexpr int kMaxTiles = kMaxRows / 8;  // row tiles of an item
-constexpr int kWarpTiles = 2;       // row tiles of a warp, at most
+// The kernel's two forms.  Where an item has at most eight rows (kOne: plain decoding, short drafts) a warp's accumulators
+// are half as many, and three CTAs of four stages fit on an SM.
+template <bool kOne>
+struct Form {
+    static constexpr int kCtas = kOne ? 3 : 2;
+    static constexpr int kStages = kOne ? 4 : 5;        // 64-key stages: two being read, the others in flight
+    static constexpr int kItemTiles = kOne ? 1 : kMaxRows / 8;  // row tiles of an item
+    static constexpr int kTiles = kOne ? 1 : 2;         // row tiles of a warp, at most
+};
 constexpr int kBlk = PILLAR_KV_BLOCK;
 constexpr float kGrowLog2 = 8.f;    // a row's reference maximum moves once a score passes it by more than 2^8
 constexpr float kWeight = 128.f;    // weight of a probability of 1 at the largest value scale: times 2^8 it is 2^15
@@ -119,10 +126,10 @@ struct Stage8 {
     float ks[kTileKeys], vs[kTileKeys];
 };
 
-template <int D>
+template <int D, bool kOne>
 struct Smem8 {
-    Stage8<D> stage[kStages8];
-    uint2 q[kMaxTiles][D / 16][32];    // query operands: row tile, step, lane
+    Stage8<D> stage[Form<kOne>::kStages];
+    uint2 q[Form<kOne>::kItemTiles][D / 16][32];    // query operands: row tile, step, lane
     float fac[kMaxRows];               // per row: logit = sum * fac * ks
     RowInfo rows[kMaxRows];
     int row[kPairs][kStep];            // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
@@ -140,10 +147,10 @@ struct Split {
     __device__ __forceinline__ int first(int gr) const { return groups == 3 ? 3 * gr : gr * (kWarps8 / groups); }
     __device__ __forceinline__ int warps(int gr) const { return groups == 3 ? (gr == 2 ? 2 : 3) : kWarps8 / groups; }
 };
-static_assert(kWarps8 == 8 && kMaxRows == 64 && kWarpTiles == 2, "one to four groups of eight warps");
+static_assert(kWarps8 == 8 && kMaxRows == 64 && Form<false>::kTiles == 2, "one to four groups of eight warps");
 __device__ __forceinline__ Split split_of(int rows) {
     const int nrt = (rows + 7) / 8;
-    return {min(nrt, kWarpTiles), (nrt + kWarpTiles - 1) / kWarpTiles};
+    return {min(nrt, 2), (nrt + 1) / 2};
 }
 
 // Byte offset of 16-byte chunk c of row r.  K: the two rows that eight lanes read together differ in bit 1
@@ -200,10 +207,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // Rows 2c and 2c + 1 of each row tile, as the eight lanes with this c hold them.
-template <int D>
+template <int D, int kTiles>
 struct Acc {
-    float o[kWarpTiles][D / 16][4];  // O^T: dimension of lane g and the next one, rows 2c and 2c + 1
-    float m[kWarpTiles][2], l[kWarpTiles][2], fac[kWarpTiles][2];  // reference maximum, this lane's part of the sum
+    float o[kTiles][D / 16][4];  // O^T: dimension of lane g and the next one, rows 2c and 2c + 1
+    float m[kTiles][2], l[kTiles][2], fac[kTiles][2];  // reference maximum, this lane's part of the sum
     float wsc, vmax;                 // weight of a probability = p * vs * wsc; largest |vs| so far
 };
 
@@ -217,10 +224,10 @@ struct Part {
 // 16 NK keys of a stage, from its row r0 on, for the first NT row tiles of a warp.  vis: which of 32 keys from
 // r0 on there are; all: the rows see every one; pos0: position of the first (verify); left: keys of the item from
 // the first one on.
-template <int D, int NT, int NK>
+template <int D, int NT, int NK, int kTiles>
 __device__ __forceinline__ void keys8(const Kv8Params &p, const Stage8<D> &st, int r0,
                                       unsigned vis, bool all, int pos0, int left, const uint2 (*q)[D / 16][32],
-                                      const RowInfo *rows, bool dump, Acc<D> &a) {
+                                      const RowInfo *rows, bool dump, Acc<D, kTiles> &a) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     float s[NK][NT][4];  // keys 16 h + 2 g and the next, rows 2c and 2c + 1
 #pragma unroll
@@ -404,8 +411,8 @@ __device__ __forceinline__ void store_lse(const Kv8Params &p, const Work &w, int
 
 // The f16 query operands of row tile t, by one warp: step j, lane (g, c): four elements of row 8 t + g, taken as the K
 // loads take bytes (64 (j / 4) + 16 c + 4 (j % 4) on).
-template <int D>
-__device__ __forceinline__ void stage_queries(const Kv8Params &p, const Work &w, Smem8<D> &sm, int t, int rows) {
+template <int D, bool kOne>
+__device__ __forceinline__ void stage_queries(const Kv8Params &p, const Work &w, Smem8<D, kOne> &sm, int t, int rows) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, row = t * 8 + g;
     uint4 x[D / 32];
 #pragma unroll
@@ -451,10 +458,11 @@ __device__ __forceinline__ void stage_queries(const Kv8Params &p, const Work &w,
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_constant__ Kv8Params p) {
+template <int D, bool kOne>
+__global__ void __launch_bounds__(kThreads8, Form<kOne>::kCtas) attn_kv8_kernel(const __grid_constant__ Kv8Params p) {
+    constexpr int kStages = Form<kOne>::kStages, kTiles = Form<kOne>::kTiles;
     extern __shared__ __align__(128) char smem[];
-    Smem8<D> &sm = *reinterpret_cast<Smem8<D> *>(smem);
+    Smem8<D, kOne> &sm = *reinterpret_cast<Smem8<D, kOne> *>(smem);
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -537,7 +545,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         };
         auto fetch = [&](int s) {  // 64-key stage s of the item
             constexpr int RL = D / 16, RP = kThreads8 / RL;  // lanes of a row, rows of a pass
-            Stage8<D> &st = sm.stage[s % kStages8];
+            Stage8<D> &st = sm.stage[s % kStages];
             const int *rows = sm.row[(s >> 1) % kPairs] + (s & 1) * kTileKeys;
             const int ch = tid % RL;
             const uint32_t kd = smem_u32(st.k), vd = smem_u32(st.v);
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         }
         __syncthreads();
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
+        for (int s = 0; s < kStages - 2; ++s) {
             if (s < 2 * steps) fetch(s);
             cp_commit();
         }
@@ -578,13 +586,13 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         pt.share = sp.warps(gr);
         pt.row0 = gr * sp.tiles * 8;
         pt.sure = w.verify ? w.L - (p.k + 1) : 0x7fffffff;
-        if (warp < sp.groups * sp.tiles) stage_queries<D>(p, w, sm, warp, pt.rows);  // (rows of the groups' last tiles that there are not, too)
+        if (warp < sp.groups * sp.tiles) stage_queries<D, kOne>(p, w, sm, warp, pt.rows);  // (rows of the groups' last tiles that there are not, too)
         __syncthreads();
-        Acc<D> a;
+        Acc<D, kTiles> a;
         a.wsc = 0x1p126f;
         a.vmax = 0.f;
 #pragma unroll
-        for (int t = 0; t < kWarpTiles; ++t) {
+        for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 a.m[t][e] = neg_inf();
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         const RowInfo *rinfo = sm.rows + pt.row0;
         const bool dump = w.verify && p.logits, one = pt.rows - pt.row0 <= 8;
         for (int t = 0; t < steps; ++t) {
-            cp_wait<1>();
+            cp_wait<kStages - 4>();
             __syncthreads();  // stages 2t and 2t+1 are in shared memory, and those of step t-1 are free
             // the next item, one link a step; not before it is needed, so that no item waits behind a long one
             if (tid == 0 && t + kLead >= steps && done < 3) {
@@ -609,7 +617,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 ++done;
             }
 #pragma unroll
-            for (int s = 2 * t + 3; s < 2 * t + 5; ++s) {
+            for (int s = 2 * t + kStages - 2; s < 2 * t + kStages; ++s) {
                 if (s < 2 * steps) fetch(s);
                 cp_commit();
             }
@@ -626,9 +634,14 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
                 const unsigned vis = (sm.mask[t % kPairs][q16 >> 1] >> (16 * (q16 & 1))) & 0xffffu;
                 const int pos0 = w.verify ? w.begin + k0 : 0;
                 const bool all = vis == 0xffffu && (!w.verify || pos0 + 15 <= pt.sure);
-                const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages8];
-                if (one) keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
-                else keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
+                const Stage8<D> &st = sm.stage[(2 * t + (q16 >> 2)) % kStages];
+                if constexpr (!kOne) {
+                    if (!one) {
+                        keys8<D, 2, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
+                        continue;
+                    }
+                }
+                keys8<D, 1, 1>(p, st, 16 * (q16 & 3), vis, all, pos0, w.n - k0, q, rinfo, dump, a);
             }
         }
         if (tid == 0) {  // (a short item: the rest of the next one's records)
@@ -656,7 +669,7 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
         __syncthreads();  // (the keys are done with, the next item is there)
         positions(sm.w[turn ^ 1]);
 #pragma unroll
-        for (int t = 0; t < kWarpTiles; ++t) {
+        for (int t = 0; t < kTiles; ++t) {
             if (t >= sp.tiles) break;
             if (t > 0) __syncthreads();
 #pragma unroll
@@ -702,10 +715,10 @@ __global__ void __launch_bounds__(kThreads8, 2) attn_kv8_kernel(const __grid_con
     if (bad) atomicOr(&p.hdr->err, bad);
 }
 
-template <int D>
+template <int D, bool kOne>
 cudaError_t launch_t(const Kv8Params &p, int nsm, cudaStream_t st) {
-    constexpr int kSmem = (int)sizeof(Smem8<D>);
-    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
+    constexpr int kSmem = (int)sizeof(Smem8<D, kOne>);
+    static_assert(Form<kOne>::kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
     static unsigned long long configured[kMaxDevices] = {};
     int dev = 0;
     unsigned long long ctx = 0;
@@ -713,7 +726,7 @@ cudaError_t launch_t(const Kv8Params &p, int nsm, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (ctx == 0 || __atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE) != ctx) {
-        e = cudaFuncSetAttribute(attn_kv8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(attn_kv8_kernel<D, kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         e = current_device_context(&dev, &ctx);  // (the calls above made a context current)
         if (e != cudaSuccess) return e;
@@ -723,13 +736,13 @@ cudaError_t launch_t(const Kv8Params &p, int nsm, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * nsm);
+    cfg.gridDim = dim3(Form<kOne>::kCtas * nsm);
     cfg.blockDim = dim3(kThreads8);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_kv8_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, attn_kv8_kernel<D, kOne>, p);
 }
 
 }  // namespace
@@ -756,7 +769,8 @@ cudaError_t launch_attn_kv8(const AttnArgs &a, const Kv8Cache &c, int nsm, cudaS
     p.M = (a.k + 1) * p.G;
     p.max_sparse = a.max_sparse;
     p.scale = a.scale;
-    const cudaError_t e = a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
+    const cudaError_t e = p.M <= 8 ? (a.D == 128 ? launch_t<128, true>(p, nsm, st) : launch_t<64, true>(p, nsm, st))
+                                : (a.D == 128 ? launch_t<128, false>(p, nsm, st) : launch_t<64, false>(p, nsm, st));
     return e == cudaSuccess ? launch_merge(a, nsm, st) : e;
 }
 
