@@ -276,12 +276,12 @@ __device__ void load_role(const PromptParams &p, SmemP<D> &sm, const BoundsP &bd
             if (ok) kv(&p.v, u.h / p.G, u.row0 + j * kTileP);
         }
     }
-    if (!ok) {  // every copy lands before the CTA can exit
-        for (int s = 0; s < S::kSlots; ++s)
-            if ((issued >> s) & 1) drainp(&sm.kvfull[s], (parity >> s) & 1);
-        for (int b = 0; b < 2; ++b)
-            if ((qissued >> b) & 1) drainp(&sm.qfull[b], (qparity >> b) & 1);
-    }
+    // Every copy lands before the CTA can exit, whoever gave up: another role can do so when this one has issued its last
+    // copies and waits for nothing more.  (Nothing else arrives on these barriers: a slot's last phase stays testable.)
+    for (int s = 0; s < S::kSlots; ++s)
+        if ((issued >> s) & 1) drainp(&sm.kvfull[s], (parity >> s) & 1);
+    for (int b = 0; b < 2; ++b)
+        if ((qissued >> b) & 1) drainp(&sm.qfull[b], (qparity >> b) & 1);
 }
 
 // ------------------------------------------------------------------ MMA warp

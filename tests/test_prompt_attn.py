@@ -304,3 +304,25 @@ def test_sequences_that_overlap_beyond_the_workspace_are_skipped():
     d["off"].copy_(torch.tensor(c.off, dtype=torch.int32))
     c.call(d)
     c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,lens", [(128, [256, 130, 1, 200] * 40), (64, [384, 140, 257, 60] * 40), (128, [37])])
+def test_calls_whose_last_copies_are_issued_before_a_wait_runs_out(D, lens):
+    """Units of so few key tiles that the load thread never waits for a slot: it has issued everything when the products' or the
+    softmax's wait gives up, and still sees its copies land before the CTA leaves its shared memory to the next one, here one
+    of a whole call that follows on the stream at once."""
+    c, e = Case(93, 4, 2, D, lens), Case(94, 4, 2, D, lens)
+    d, f, want = c.device(), e.device(), e.device()
+    e.call(want)
+    for _ in range(4):
+        c.shape.wait_timeout_us = 1
+        c.call(d)
+        e.call(f)
+        assert P.pillar_get_error(d["ws"]) & ~P.FLAG_TIMEOUT == 0 and P.pillar_get_error(f["ws"]) == 0
+        assert torch.equal(f["out"], want["out"]) and torch.equal(f["lse"], want["lse"])
+        f["out"].fill_(0x7fc1)
+        f["lse"].fill_(SENTINEL)
+    c.shape.wait_timeout_us = 0
+    c.call(d)
+    c.check(d)
