@@ -419,6 +419,7 @@ __device__ void loader(const AttnParams &p, const Ctx &c, int lane, int li) {
         if (info.it < 0) {
             ok = mbar_wait_80(&c.empty[stage], phase ^ 1, c.abort, c.err, c.wait_ns);
             if (ok) {
+                issued &= ~(1u << stage);  // its last copy has been read, and the record below ends another phase
                 cp_async_arrive_noinc(&c.full[stage]);
                 __syncwarp();
                 if (lane == 0) {
@@ -507,11 +508,10 @@ __device__ void loader(const AttnParams &p, const Ctx &c, int lane, int li) {
         __syncwarp();
         mbar_arrive(&c.rempty[rb]);  // every lane is done reading this row list
     }
-    if (!ok) {
-        // Let every copy this warp started land before the CTA can exit.
-        for (int s2 = 0; s2 < S::NSTAGE; ++s2)
-            if ((issued >> s2) & 1) drain_wait(&c.full[s2], (issued_par >> s2) & 1);
-    }
+    // Let every copy this warp started land before the CTA can exit, whoever gave up: the consumers or
+    // the MMA thread can do so when this warp has issued its last copies and waits for nothing more.
+    for (int s2 = 0; s2 < S::NSTAGE; ++s2)
+        if ((issued >> s2) & 1) drain_wait(&c.full[s2], (issued_par >> s2) & 1);
 }
 
 // ============================================================== MMA warp

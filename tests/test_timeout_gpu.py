@@ -50,3 +50,27 @@ def test_wait_bound_is_checked_on_the_host():
     g.attn()
     assert g.attn_flags() == 0
     np.testing.assert_equal(np.isfinite(g.host()["out"]).all(), True)
+
+
+def test_steps_whose_copies_are_all_issued_before_a_wait_runs_out():
+    """Contexts of so few tiles that the loaders have issued everything when a wait of the other roles gives up: they still see
+    their copies land before a CTA leaves its shared memory to the next one, here one of a whole step that follows on the stream
+    at once."""
+    w = W.generate(W.scaled("qwen3_8b", B=4, length_scale=0.02, seed_offset=11))
+    g, h, want = Gpu(w), Gpu(w), Gpu(w)
+    want.attn()
+    assert want.attn_flags() == 0
+    for _ in range(4):
+        g.shape.wait_timeout_us = 1
+        g.attn()
+        h.attn()
+        assert g.attn_flags() & ~P.FLAG_TIMEOUT == 0 and h.attn_flags() == 0
+        for name in ("out", "logits", "lse"):
+            assert torch.equal(getattr(h, name), getattr(want, name)), name
+        h.out.zero_()
+        h.logits.fill_(math.nan)
+        h.lse.fill_(math.nan)
+    g.shape.wait_timeout_us = 0
+    g.attn()
+    assert g.attn_flags() == 0
+    compare_attn(w, g.host(), run_oracle(w))
