@@ -251,7 +251,7 @@ __device__ void resolver(const AttnParams &p, const Ctx &c, int lane) {
     uint32_t eph = 0;
     int su = blockIdx.x, ss = 0;  // the naive joint batch's cursor
     for (int rb = 0;; rb = rb + 1 == kRowLists ? 0 : rb + 1) {
-        if (!mbar_wait(&c.rempty[rb], ((eph >> rb) & 1) ^ 1, c.abort, c.err, c.wait_ns)) return;
+        if (!mbar_wait_warp(&c.rempty[rb], ((eph >> rb) & 1) ^ 1, c.abort, c.err, c.wait_ns)) return;
         eph ^= 1u << rb;
         int it = 0;
         if (lane == 0) it = p.static_units ? static_next_item(p, num_items, su, ss) : atomicAdd(&p.hdr->item_counter, 1);
@@ -370,17 +370,17 @@ __device__ __forceinline__ void tma_gather4_hint(void *dst, const void *tmap, in
         : "memory");
 }
 
-// mbar_wait for the loader warps: the first test inline, the bounded polling out of line (a
+// mbar_wait_warp for the loader warps: the first test inline, the bounded polling out of line (a
 // function of their own: one called from warps at different register counts does not allocate;
 // measured on back-to-back steps, -0.5 us on the Qwen3-8B shape and -1.7 us on the stress batch,
 // while the same for the epilogue warps as well cost +9 us).
 __device__ __noinline__ bool mbar_wait_poll80(uint64_t *bar, uint32_t parity, volatile int *abort, int *err,
                                               unsigned long long limit_ns) {
-    return mbar_wait(bar, parity, abort, err, limit_ns);
+    return mbar_wait_warp(bar, parity, abort, err, limit_ns);
 }
 __device__ __forceinline__ bool mbar_wait_80(uint64_t *bar, uint32_t parity, volatile int *abort, int *err,
                                              unsigned long long limit_ns) {
-    return mbar_try_wait(bar, parity) || mbar_wait_poll80(bar, parity, abort, err, limit_ns);
+    return mbar_try_wait_warp(bar, parity) || mbar_wait_poll80(bar, parity, abort, err, limit_ns);
 }
 
 // ============================================================== loader warps
@@ -646,14 +646,14 @@ struct CState {
 // or not (instruction-fetch stalls; measured on the Qwen3-8B-shaped step, where the rare paths
 // below moved out of line, the visibility test made one 64-bit mask applied after one multiply
 // path and the division moved to the epilogue warps took the step from 202.7 to 197.2 us).
-// Hence mbar_wait for these warps: the first test inline, the bounded polling out of line.
+// Hence mbar_wait_warp for these warps: the first test inline, the bounded polling out of line.
 __device__ __noinline__ bool mbar_wait_poll(uint64_t *bar, uint32_t parity, volatile int *abort, int *err,
                                             unsigned long long limit_ns) {
-    return mbar_wait(bar, parity, abort, err, limit_ns);
+    return mbar_wait_warp(bar, parity, abort, err, limit_ns);
 }
 __device__ __forceinline__ bool mbar_wait_c(uint64_t *bar, uint32_t parity, volatile int *abort, int *err,
                                             unsigned long long limit_ns) {
-    return mbar_try_wait(bar, parity) || mbar_wait_poll(bar, parity, abort, err, limit_ns);
+    return mbar_try_wait_warp(bar, parity) || mbar_wait_poll(bar, parity, abort, err, limit_ns);
 }
 
 // Hands the next mailbox slot of this warp's quadrant to its epilogue warp
@@ -804,7 +804,7 @@ template <int D>
 __device__ __noinline__ bool rescale_o(uint64_t *sfree, uint32_t par, volatile int *abort, int *err,
                                        unsigned long long wait_ns, uint32_t taddr, float aa, float ab) {
     // O holds this item's earlier tiles (a grow needs one): the last P V must have completed
-    if (!mbar_wait(sfree, par, abort, err, wait_ns)) return false;
+    if (!mbar_wait_warp(sfree, par, abort, err, wait_ns)) return false;
     tc_fence_after();
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += 64) {
@@ -950,14 +950,14 @@ __device__ void epilogue_warp(const AttnParams &p, const Ctx &c, int q, int lane
     uint32_t odone = 0;  // bit b: parity of O buffer b's next completion
     for (uint32_t n = 0;; ++n) {
         const int slot = q * 2 + (int)(n & 1);
-        if (!mbar_wait(&c.epi_full[slot], (n >> 1) & 1, c.abort, c.err, c.wait_ns)) break;
+        if (!mbar_wait_warp(&c.epi_full[slot], (n >> 1) & 1, c.abort, c.err, c.wait_ns)) break;
         const EpiRec e = c.epi[slot];
         const float2 l = c.epi_l[slot * 32 + lane];  // (the division is done here, off the softmax warps' code)
         const float2 inv = make_float2(l.x > 0.f ? 1.f / l.x : 0.f, l.y > 0.f ? 1.f / l.y : 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.epi_empty[slot]);  // the record is copied: the slot may be reused
         if (e.stop) break;
-        if (!mbar_wait(&c.o_done[e.qb], (odone >> e.qb) & 1, c.abort, c.err, c.wait_ns)) break;
+        if (!mbar_wait_warp(&c.o_done[e.qb], (odone >> e.qb) & 1, c.abort, c.err, c.wait_ns)) break;
         odone ^= 1u << e.qb;
         tc_fence_after();
         ItemInfo in;

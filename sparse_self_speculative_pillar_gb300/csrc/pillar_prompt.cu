@@ -158,26 +158,8 @@ struct BoundsP {
 __device__ __forceinline__ bool waitp(uint64_t *bar, uint32_t parity, const BoundsP &b) {
     return mbar_wait(bar, parity, b.abort, b.err, b.ns);
 }
-// The same for a whole warp, whose lanes have to go the same way, since what follows is done by the warp as one.  They test
-// the barrier in one instruction; a phase that one lane has seen complete is complete for the others' next test, because it
-// cannot end again without this warp; and giving up is put to the vote of those still waiting.  (A vote after every wait
-// instead took 3 to 5 % of the long prompts' time.)
-__device__ __forceinline__ bool waitw(uint64_t *bar, uint32_t parity, const BoundsP &b) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
-    const uint32_t cadence = b.ns < 1000000ull ? 0u : 63u;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & cadence) == 0) {
-            const bool over = global_timer_ns() - t0 > b.ns;
-            const unsigned waiting = __activemask();
-            if (__any_sync(waiting, over || *b.abort)) {
-                if (__any_sync(waiting, over)) atomicOr(b.err, PILLAR_FLAG_TIMEOUT);
-                *b.abort = 1;
-                return false;
-            }
-        }
-    }
+__device__ __forceinline__ bool waitw(uint64_t *bar, uint32_t parity, const BoundsP &b) {  // by a whole warp
+    return mbar_wait_warp(bar, parity, b.abort, b.err, b.ns);
 }
 // Bounded wait for copies or products already in flight, whatever the pipeline's bound and the abort flag say.
 __device__ __forceinline__ void drainp(uint64_t *bar, uint32_t parity) {

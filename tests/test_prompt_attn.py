@@ -326,3 +326,21 @@ def test_calls_whose_last_copies_are_issued_before_a_wait_runs_out(D, lens):
     c.shape.wait_timeout_us = 0
     c.call(d)
     c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_waits_that_run_out_anywhere_in_the_pipeline(D):
+    """Bounds from one microsecond to more than the whole call takes, so that waits give up at the start, in the middle and
+    hardly at all: a warp goes on or gives up as one, and a whole call that follows at once is right."""
+    c, e = Case(95, 4, 2, D, [700, 1300, 5, 900] * 20), Case(96, 4, 2, D, [300, 41] * 30)
+    d, f, want = c.device(), e.device(), e.device()
+    e.call(want)
+    for bound in (1, 2, 3, 4, 6, 9, 13, 20, 30, 50, 400):
+        c.shape.wait_timeout_us = bound
+        c.call(d)
+        e.call(f)
+        assert P.pillar_get_error(d["ws"]) & ~P.FLAG_TIMEOUT == 0 and P.pillar_get_error(f["ws"]) == 0, bound
+        assert torch.equal(f["out"], want["out"]) and torch.equal(f["lse"], want["lse"]), bound
+        f["out"].fill_(0x7fc1)
+        f["lse"].fill_(SENTINEL)

@@ -74,3 +74,20 @@ def test_steps_whose_copies_are_all_issued_before_a_wait_runs_out():
     g.attn()
     assert g.attn_flags() == 0
     compare_attn(w, g.host(), run_oracle(w))
+
+
+def test_waits_that_run_out_anywhere_in_the_pipeline():
+    """Bounds from one microsecond to more than the whole step takes: a warp goes on or gives up as one, and a whole step that
+    follows at once is right."""
+    w, v = W.generate(W.scaled("qwen3_8b", B=24, length_scale=0.2, seed_offset=12)), W.generate(W.scaled("qwen3_8b", B=6, length_scale=0.03, seed_offset=13))
+    g, h, want = Gpu(w), Gpu(v), Gpu(v)
+    want.attn()
+    assert want.attn_flags() == 0
+    for bound in (1, 2, 3, 4, 6, 9, 13, 20, 30, 50, 400):
+        g.shape.wait_timeout_us = bound
+        g.attn()
+        h.attn()
+        assert g.attn_flags() & ~P.FLAG_TIMEOUT == 0 and h.attn_flags() == 0, bound
+        for name in ("out", "logits", "lse"):
+            assert torch.equal(getattr(h, name), getattr(want, name)), (bound, name)
+        h.out.zero_()
