@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(kThreadsPerCta, 4) kv8_append_kernel(const Kv8
         if (lane < rows && t < all) {
             const int first = __ldg(a.new_off + b), end = __ldg(a.new_off + b + 1), len = __ldg(a.req_len + b);
             const long long pos = (long long)len - end + t;
-            if (first < 0 || t < first || t >= end || end > a.n || len > a.max_len || len - (end - first) < 0 ||
+            // (len - (end - first) would pass 31 bits for the lowest lengths)
+            if (first < 0 || t < first || t >= end || end > a.n || len > a.max_len || len < end - first ||
                 pos / kBlock >= a.max_blocks) {
                 bad = PILLAR_FLAG_REQUEST;
             } else if (pos % kBlock == 0 || t == first) {

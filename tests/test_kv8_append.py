@@ -243,3 +243,21 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(P.PillarError):  # rows that do not start on 16 bytes
         P.pillar_kv8_append(s, wide, new, *good[2:])
     P.pillar_kv8_append(s, new[:0], new[:0], torch.tensor([0], **i32), torch.tensor([0, 0], **i32), *good[4:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1, 0, 2, -2 ** 31, -2 ** 31 + 1, -2 ** 31 + 2, -2 ** 31 + 3, 2 ** 31 - 1])
+def test_lengths_that_are_none(bad):
+    """Request 1's three new tokens under every kind of wrong length, the lowest ones among them, whose difference to the new
+    tokens passes 31 bits: flagged, its rows skipped, the others' as ever."""
+    lens, off, keep = [20, bad, 9], [0, 4, 7, 9], [0, 4, 4, 6]
+    g, table, pools, scales, total = cache(22, 3, 2, 64, [32, 48, 16])
+    x = bf16_bits_to_f32(f32_to_bf16_bits(g.standard_normal((9, 2, 64)).astype(np.float32)))
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(shape_of(3, 2, 64, total, 48), (x, x), (128, 128), lens, off, table, pools, scales, flags)
+    assert int(flags.item()) == P.FLAG_REQUEST
+    rows = x[[0, 1, 2, 3, 7, 8]].astype(np.float64)
+    for p, sc, (codes, scale) in zip(pools, scales, got):
+        want_c, want_s = C.kv8_append(p, sc, rows, [20, 3, 9], keep, table)
+        np.testing.assert_array_equal(scale, want_s)
+        np.testing.assert_array_equal(C.e4m3_decode(codes), C.e4m3_decode(want_c))
