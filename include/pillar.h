@@ -569,7 +569,9 @@ PILLAR_API int pillar_block_map_workspace_bytes(const pillar_shape_t *shape, siz
  * batch order, at its tail, so the result does not depend on timing.  When
  * the ring runs short, the first request whose blocks do not fit and every
  * later one that needs blocks keep prev_len (PILLAR_FLAG_BLOCK); the others
- * are served.
+ * are served.  When the blocks given back and those in the ring before the
+ * call are more than the pool has (the tables and the ring disagree), none is
+ * given back (PILLAR_FLAG_BLOCK): those blocks belong to nobody any more.
  *
  *   req_len,
  *   prev_len     [B] int32, in [0, max_len].  A bad req_len leaves the request

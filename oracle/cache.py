@@ -63,6 +63,9 @@ def block_map(req_len, prev_len, table, ring, state, max_len, num_blocks):
         kv_off.append(len(slots))
         new_slots += [slot(t) for t in range(p, n)]
         new_off.append(len(new_slots))
+    if ring_ok and count + given > num_blocks:  # the tables and the ring disagree: nothing is given back
+        bad.add("block")
+        push, given = [], 0
     if ring_ok:
         for i, blk in enumerate(push):
             if not 0 <= blk < num_blocks:

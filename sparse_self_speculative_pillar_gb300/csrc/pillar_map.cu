@@ -21,9 +21,11 @@
 //      tile searching its request, took 55 us for 11.6 million slots where this takes
 //      13, 3.6 TB/s.)  Blocks that were taken are entered into the
 //      table on the way.  Bound by the stores: 4 bytes per position.
-// The ring is first in, first out and never holds more than its size, so the
-// places popped in a call (from head) and the places pushed (from head +
-// count) are distinct: taking and giving need no order between them.
+// The ring is first in, first out, and blocks are given back only when those
+// in it before the call and those given back together fit (they always do
+// when the tables and the ring agree on who holds what), so the places popped
+// in a call (from head) and the places pushed (from head + count) are
+// distinct: taking and giving need no order between them.
 #include "pillar_device.cuh"
 #include "pillar_map.h"
 
@@ -146,8 +148,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
         c_give += tot[2];
         c_used += tot[3];
     }
-    const long long left = (long long)count - c_used + c_give;
-    if (left > a.num_blocks) bad |= PILLAR_FLAG_BLOCK;  // more given back than the pool has
+    // more given back than the ring has room for beside what it held: none is (a block would land in a place that is being
+    // popped)
+    const bool fits = count + c_give <= a.num_blocks;
+    if (!fits) bad |= PILLAR_FLAG_BLOCK;
     if (bad) atomicOr(&s_bad, bad);
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -155,12 +159,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) map_scan(const MapArgs a) {
         hdr->err = s_bad;
         hdr->head = head;
         hdr->count = count;
-        hdr->released = ring_ok ? c_give : 0;
+        hdr->released = ring_ok && fits ? c_give : 0;
         a.kv_off[a.B] = c_len;
         a.new_off[a.B] = (int)min(c_new, 0x7fffffffll);
         if (ring_ok) {
             a.state[0] = (int)((head + c_used) % a.num_blocks);
-            a.state[1] = (int)min(left, (long long)a.num_blocks);
+            a.state[1] = (int)(count - c_used + (fits ? c_give : 0));
         }
     }
 }

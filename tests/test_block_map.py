@@ -239,3 +239,32 @@ def test_granted_lengths_in_the_place_of_the_lengths_read_are_refused():
         wrong = list(args)
         wrong[6] = wrong[other]
         assert lib.pillar_block_map(ctypes.byref(s), *wrong) == -1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("count,took", [(8, 6), (7, 7), (10, 1), (6, 6), (9, 0)])
+def test_more_given_back_than_the_ring_has_room_for(count, took):
+    """Tables that hold blocks which the ring holds too: giving them back would write into places that the same call pops."""
+    table = np.array([[4, 5, 6, 7] + [SENTINEL] * 4, [SENTINEL] * 8])
+    for seed in range(3):
+        ring = np.random.default_rng(seed).permutation(10)
+        got, want, flags = play([0, 16 * took], [64, 0], table, ring, [7, count], 128, 10)
+        over = count + 4 > 10
+        assert flags == (P.FLAG_BLOCK if over else 0) and want["bad"] == ({"block"} if over else set())
+        check(got, want)
+        if over:
+            assert list(got["state"]) == [(7 + took) % 10, count - took]
+            np.testing.assert_array_equal(got["ring"], ring)
+
+
+@pytest.mark.gpu
+def test_many_more_given_back_than_the_ring_has_room_for():
+    """The same with hundreds of requests that give and take in one call: the outcome does not depend on timing."""
+    B, num = 600, 2000
+    table = np.tile(np.arange(9), (B, 1)) + 3 * np.arange(B)[:, None]
+    prev, req = np.where(np.arange(B) % 2, 0, 130), np.where(np.arange(B) % 2, 96, 0)
+    ring = np.random.default_rng(5).permutation(num)
+    for _ in range(3):
+        got, want, flags = play(req, prev, table, ring, [1999, num], 144, num)
+        assert flags == P.FLAG_BLOCK and want["bad"] == {"block"}
+        check(got, want)

@@ -95,3 +95,13 @@ def test_prompt_attention_closed_forms():
     assert np.all(out[5] == 0)                                            # behind the last sequence
     same, _ = C.prompt_attn(q, np.ones_like(k), v, [0, 6], 0.3)
     np.testing.assert_allclose(same[3, 0], v[:4, 0].mean(0))              # equal keys: the mean of what is seen
+
+
+def test_block_map_gives_nothing_back_that_the_ring_has_no_room_for():
+    """Request 0's four blocks are in the ring already: 8 + 4 are more than the 10 there are, whatever request 1 takes."""
+    table, ring = np.array([[4, 5, 6, 7, 0, 0], [0] * 6]), np.arange(10)
+    r = C.block_map([0, 96], [64, 0], table, ring, [7, 8], 96, 10)
+    assert r["bad"] == {"block"} and r["state"].tolist() == [3, 2] and np.array_equal(r["ring"], ring)
+    assert r["table"][1].tolist() == [7, 8, 9, 0, 1, 2] and r["granted"].tolist() == [0, 96]
+    r = C.block_map([0, 96], [64, 0], table, ring, [7, 6], 96, 10)
+    assert not r["bad"] and r["state"].tolist() == [3, 4] and r["ring"].tolist() == [0, 1, 2, 4, 5, 6, 7, 7, 8, 9]
