@@ -672,9 +672,11 @@ PILLAR_API int pillar_kv8_append(const pillar_shape_t *shape, const uint16_t *k_
  * 4.  The schedule is UNIFIED, DRAFT_ONLY or VERIFY_ONLY (PILLAR_ERR_ARG
  * otherwise); wait_timeout_us has no meaning here (nothing waits on the
  * device).  A block outside [0, num_slots / 16) or a position past
- * max_blocks is skipped and flagged PILLAR_FLAG_SLOT.  A NaN code or scale of
- * a key makes the rows of its request and KV head NaN that share a tile of 64
- * keys with it, whether they see it or not; pillar_kv8_append writes none.
+ * max_blocks is skipped and flagged PILLAR_FLAG_SLOT.  A NaN in q makes its
+ * row NaN.  A NaN scale of K, or code, does so to the rows of its request and
+ * KV head that see the key, a NaN scale of V to those that do not as well, a
+ * NaN code of V in its dimension; verify_lse is NaN where the scores are.  All
+ * that holds however the context is split.  pillar_kv8_append writes no NaN.
  *
  * pillar_attn_run_kv8 -- the same on the plan that pillar_attn_plan left in the
  * workspace (as pillar_attn_run): one plan for the layers of a model step.

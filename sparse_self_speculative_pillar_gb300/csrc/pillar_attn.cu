@@ -1156,9 +1156,13 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtasPerSm) merge_kernel(c
                 }
             }
             float bm = mx;
+            bool none = true;  // (a NaN record is not an empty one, though the maximum passes over it)
 #pragma unroll
-            for (int q = 0; q < kMergeBatch; ++q) bm = fmaxf(bm, ls[q]);
-            if (bm == neg_inf()) continue;
+            for (int q = 0; q < kMergeBatch; ++q) {
+                bm = fmaxf(bm, ls[q]);
+                none &= ls[q] == neg_inf();
+            }
+            if (none && bm == neg_inf()) continue;
             const float a = ex2_approx((mx - bm) * kLog2e);  // rescale what was merged so far (0 when empty)
             den *= a;
             o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
@@ -1173,7 +1177,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtasPerSm) merge_kernel(c
             }
             mx = bm;
         }
-        float lse = neg_inf();
+        float lse = den == 0.f ? neg_inf() : den;  // (a NaN sum stays one)
         if (den > 0.f) {
             const float inv = 1.f / den;
             o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);

@@ -377,3 +377,34 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
         P.pillar_attn_kv8(c.shape, *good, d["ws"].cpu())
     with pytest.raises(P.PillarError):
         P.pillar_attn_kv8(c.shape, *good, d["ws"][:512])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunk", [64, 2048])
+@pytest.mark.parametrize("what", ["query", "infinite query", "key scale", "value scale"])
+def test_a_nan_is_one_however_the_context_is_split(what, chunk):
+    """A NaN in what a row reads makes the row NaN, and its LSE where the scores are; the other rows are as without it.  Split,
+    some of a row's partial results (a scale) or all of them (its query) are NaN."""
+    c = Case(73, 8, 2, 64, 2, [700, 600, 90], [1, 0, 1], verify_chunk=chunk, draft_chunk=chunk)
+    c.cnt[1], c.idx[1, :, 7] = c.idx.shape[2], 40  # the lists name a position of the block that gets the scale
+    d, e = c.device(), c.device()
+    c.call(d)
+    assert P.pillar_get_error(d["ws"]) == 0
+    rows, heads, lse = np.zeros((c.T, 8), bool), slice(4, 8), np.zeros((2, 8, 3), bool)
+    if "query" in what:
+        bad = 0x7f80 if what.startswith("inf") else 0x7fc0
+        e["q"][1, 0] = e["q"][3, 5] = bad  # request 0's second row, head 0; the draft row, head 5
+        rows[1, 0] = rows[3, 5] = lse[0, 0, 1] = True
+    else:
+        e["ks" if what == "key scale" else "vs"][int(c.table[0, 2]), 1] = float("nan")
+        e["ks" if what == "key scale" else "vs"][int(c.table[1, 2]), 1] = float("nan")
+        rows[:4, heads] = True
+        lse[0, heads] = what == "key scale"
+    c.call(e)
+    assert P.pillar_get_error(e["ws"]) == 0
+    value = lambda x: torch.from_numpy(bf16_bits_to_f32(x["out"].cpu().numpy().view(np.uint16)))  # noqa: E731
+    got, want = value(e), value(d)
+    at, z = torch.from_numpy(rows), torch.from_numpy(lse)
+    assert torch.all(torch.isnan(got[at])) and torch.equal(got[~at], want[~at])
+    got, want = e["lse"].cpu(), d["lse"].cpu()
+    assert torch.all(torch.isnan(got[z])) and torch.equal(got[~z], want[~z])
