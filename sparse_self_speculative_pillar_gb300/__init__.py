@@ -425,6 +425,17 @@ def _dim(name, x, i, ndim):
     return x.shape[i]
 
 
+def _dim32(name, x, i, ndim):
+    """The same for an extent that the call takes as a 32-bit count (ctypes would wrap a larger one)."""
+    return _count32(name, _dim(name, x, i, ndim))
+
+
+def _count32(name, n):
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: {n}, more than a 32-bit count")
+    return n
+
+
 def _rows(name, x, rows, heads, D, dev):
     """Pointer and token stride of [rows, heads, D] bf16 whose tokens may lie apart (a slice of a fused projection)."""
     if x.dtype not in _T.bf16 or x.shape != (rows, heads, D) or x.get_device() != dev:
@@ -457,7 +468,7 @@ def pillar_block_map(shape, req_len, prev_len, block_table, free_ring, free_stat
     ring, and writes the block table's new entries, the slot table and the new tokens' slots."""
     dev, B = _T.device(), shape.B
     ws, ws_bytes = _workspace(workspace, dev)
-    width, slots, new = (_dim("block_table", block_table, 1, 2), _dim("slot_table", slot_table, 0, 1),
+    width, slots, new = (_dim32("block_table", block_table, 1, 2), _dim("slot_table", slot_table, 0, 1),
                          _dim("new_slots", new_slots, 0, 1))
     st = load().pillar_block_map(
         ctypes.byref(shape), _arg("req_len", req_len, _T.i32, (B,), dev), _arg("prev_len", prev_len, _T.i32, (B,), dev),
@@ -483,7 +494,7 @@ def pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_poo
     """The new tokens' K/V rows ([n, Hkv, D] bf16, tokens may lie apart) as e4m3 codes under the scales of their blocks;
     request b's rows new_off[b] .. new_off[b+1]-1 are its last positions."""
     dev, B = _T.device(), shape.B
-    n, width = _dim("k_new", k_new, 0, 3), _dim("block_table", block_table, 1, 2)
+    n, width = _dim32("k_new", k_new, 0, 3), _dim32("block_table", block_table, 1, 2)
     kp, ks = _rows("k_new", k_new, n, shape.Hkv, shape.D, dev)
     vp, vs = _rows("v_new", v_new, n, shape.Hkv, shape.D, dev)
     st = load().pillar_kv8_append(
@@ -497,7 +508,7 @@ def pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_poo
 
 
 def _kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev):
-    width = _dim("block_table", block_table, 1, 2)
+    width = _dim32("block_table", block_table, 1, 2)
     return (_arg("q", q, _T.bf16, (_dim("q", q, 0, 3), shape.Hq, shape.D), dev),
             *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
             _arg("block_table", block_table, _T.i32, (shape.B, width), dev), width)
@@ -542,7 +553,7 @@ def pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_tabl
 
 def pillar_prompt_attn_workspace_bytes(shape: PillarShape, n: int) -> int:
     out = ctypes.c_size_t(0)
-    st = load().pillar_prompt_attn_workspace_bytes(ctypes.byref(shape), int(n), ctypes.byref(out))
+    st = load().pillar_prompt_attn_workspace_bytes(ctypes.byref(shape), _count32("n", int(n)), ctypes.byref(out))
     if st:
         raise PillarError("pillar_prompt_attn_workspace_bytes", st)
     return int(out.value)
@@ -551,7 +562,7 @@ def pillar_prompt_attn_workspace_bytes(shape: PillarShape, n: int) -> int:
 def pillar_prompt_attn(shape, q, k, v, seq_off, out, lse, workspace, stream=None):
     """Causal attention over prompts packed one after another ([n, heads, D] bf16; tokens may lie apart); lse [n, Hq] fp32
     or None."""
-    dev, n = _T.device(), _dim("q", q, 0, 3)
+    dev, n = _T.device(), _dim32("q", q, 0, 3)
     qp, qs = _rows("q", q, n, shape.Hq, shape.D, dev)
     kp, ks = _rows("k", k, n, shape.Hkv, shape.D, dev)
     vp, vs = _rows("v", v, n, shape.Hkv, shape.D, dev)

@@ -268,3 +268,24 @@ def test_many_more_given_back_than_the_ring_has_room_for():
         got, want, flags = play(req, prev, table, ring, [1999, num], 144, num)
         assert flags == P.FLAG_BLOCK and want["bad"] == {"block"}
         check(got, want)
+
+
+def test_extents_past_32_bits_are_refused():
+    wide = lambda n: torch.empty((1, n), dtype=torch.int32, device="meta")  # noqa: E731
+    assert P._dim32("block_table", wide(2 ** 31 - 1), 1, 2) == 2 ** 31 - 1
+    for n in (2 ** 31, 2 ** 32 + 4):
+        with pytest.raises(ValueError):
+            P._dim32("block_table", wide(n), 1, 2)
+
+
+@pytest.mark.gpu
+def test_a_table_wider_than_32_bits_is_refused():
+    """2^32 + 4 entries a row (17 GB, never touched): taken as four, most of the requests' blocks would have no place."""
+    s = shape_of(1, 8, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws = torch.empty(P.pillar_block_map_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    small = [torch.zeros(1, **i32), torch.zeros(1, **i32), torch.empty((1, 2 ** 32 + 4), **i32), torch.zeros(8, **i32),
+             torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(2, dtype=torch.int64, device="cuda"),
+             torch.zeros(16, **i32), torch.zeros(2, **i32), torch.zeros(16, **i32), ws]
+    with pytest.raises(ValueError):
+        P.pillar_block_map(s, *small)

@@ -344,3 +344,12 @@ def test_waits_that_run_out_anywhere_in_the_pipeline(D):
         assert torch.equal(f["out"], want["out"]) and torch.equal(f["lse"], want["lse"]), bound
         f["out"].fill_(0x7fc1)
         f["lse"].fill_(SENTINEL)
+
+
+def test_token_counts_past_32_bits_are_refused():
+    s = shape_of(2, 4, 2, 64, 100)
+    for n in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            P.pillar_prompt_attn_workspace_bytes(s, n)
+    with pytest.raises(P.PillarError):
+        P.pillar_prompt_attn_workspace_bytes(s, -2 ** 31)
