@@ -408,3 +408,35 @@ def test_a_nan_is_one_however_the_context_is_split(what, chunk):
     assert torch.all(torch.isnan(got[at])) and torch.equal(got[~at], want[~at])
     got, want = e["lse"].cpu(), d["lse"].cpu()
     assert torch.all(torch.isnan(got[z])) and torch.equal(got[~z], want[~z])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,Hq,Hkv,k,lens,modes,chunks", [
+    (128, 4, 1, 0, [2048, 1999, 1025, 3000, 129], [1, 1, 1, 0, 1], dict(verify_chunk=2048, draft_chunk=2048)),
+    (128, 8, 2, 0, [2500, 1024, 1300, 3999, 64], [1, 1, 0, 1, 1], {}),
+    (128, 4, 2, 3, [1500, 700, 257, 64], [1, 0, 1, 1], dict(verify_chunk=64, draft_chunk=64)),
+    (128, 2, 2, 1, [2100, 1800, 333], [0, 1, 0], dict(verify_chunk=512, draft_chunk=128)),
+    (128, 8, 1, 0, [640, 641, 639, 900], [1, 1, 1, 1], dict(verify_chunk=640)),
+    (64, 8, 1, 0, [2500, 1300, 257], [1, 0, 1], dict(verify_chunk=256, draft_chunk=192)),
+    (64, 2, 1, 3, [1700, 2048], [1, 1], dict(verify_chunk=2048)),
+])
+def test_items_of_at_most_eight_rows_over_long_contexts(D, Hq, Hkv, k, lens, modes, chunks):
+    """Up to sixteen steps an item: the stages wrap, positions are resolved past the first steps, and split items join."""
+    c = Case(80, Hq, Hkv, D, k, lens, modes, **chunks)
+    d = c.device()
+    c.call(d)
+    c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,k", [(8, 0), (16, 3), (24, 2)])
+def test_more_items_than_ctas(Hq, k):
+    """Every CTA goes through several items, long and short ones, some of one step: each takes the next from the queue while
+    the present one runs."""
+    g = np.random.default_rng(81)
+    B = 90
+    lens = np.where(np.arange(B) % 4 == 0, g.integers(600, 1100, B), g.integers(k + 1, 140, B))
+    c = Case(81, Hq, 8, 128, k, lens, (np.arange(B) % 5 != 2).astype(int), verify_chunk=256)
+    d = c.device()
+    c.call(d)
+    c.check(d)
