@@ -1242,22 +1242,10 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-static EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return (EncodeTiledFn) nullptr;
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    return fn;
-}
-
 // A pool [num_slots, Hkv, D] bf16 as the 2-D tensor [num_slots * Hkv rows, D]:
 // boxes of 64 columns x 1 row (the gather4 shape), 128-byte swizzle.
 static cudaError_t pool_tensor_map(CUtensorMap *m, const void *pool, long long num_slots, int Hkv, int D) {
-    const EncodeTiledFn fn = encode_tiled();
+    static const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(driver_entry("cuTensorMapEncodeTiled", 12000));
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t gdim[2] = {(cuuint64_t)D, (cuuint64_t)num_slots * (cuuint64_t)Hkv};
     const cuuint64_t gstride[1] = {(cuuint64_t)D * 2};
