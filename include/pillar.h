@@ -668,6 +668,11 @@ PILLAR_API int pillar_kv8_append(const pillar_shape_t *shape, const uint16_t *k_
  *   verify_logits  as pillar_attn_unified writes them (so that
  *                  pillar_topk_select follows unchanged), or NULL: no dump
  *   workspace      pillar_attn_workspace_bytes
+ * A probability is rounded to f16 with its key's value scale in it, relative to
+ * the largest value scale among the keys before it in the context (the keys
+ * that its row does not see included): a key whose scale is 2^24 or more below
+ * that one's keeps eight bits of its weight, or fewer, and its part of the row's
+ * output is off by up to 2^-32 of the largest value among those keys.
  * Alignment: q, out and the pools 16 bytes, verify_logits 8, the other arrays
  * 4.  The schedule is UNIFIED, DRAFT_ONLY or VERIFY_ONLY (PILLAR_ERR_ARG
  * otherwise); wait_timeout_us has no meaning here (nothing waits on the

@@ -54,7 +54,10 @@
 // of its own had (345 us against 233 with two CTAs).
 // Measured (32 heads on 8, D = 128): 64 single rows over contexts of 1000 to 30000
 // tokens 211 us, 4.6 TB/s of cache or 0.69 of a copy's rate; 128 requests with contexts
-// of 6144 to 10240, one ninth of them verify with 9 tokens, 200 us, 0.36.  Copies of this
+// of 6144 to 10240, one ninth of them verify with 9 tokens, 200 us, 0.36: slower than the
+// bf16 step, which takes 170 on the same batch.  Drafts alone (the same lengths, lists of a
+// twentieth) take 61 us, the bf16 step 63; D = 64, the second batch 150 (150) and the first
+// 150 (352, with the dump that the bf16 step always writes).  Copies of this
 // kernel that leave out the products, or the copies, say which side it is: 134 and
 // 145 of 170 us for single rows over 4000 to 6000 tokens (two CTAs), 100 and 222 of 238
 // for the second batch (before its last two steps).

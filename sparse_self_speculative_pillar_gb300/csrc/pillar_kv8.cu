@@ -22,9 +22,12 @@
 // so that all blocks are in flight together; with many (a prompt) sixteen, so
 // that the request search is shared.  A prefill batch (32 prompts of 100 to 4000
 // tokens, 8 heads of 128 for K and for V: 2 bytes read and 1 written per
-// element) takes 32.7 us, 4.96 TB/s or 0.73 of a copy's rate: bound by the ALU,
-// then by HBM.  A decode step (128 requests) takes 10 us: launch and the latency
-// of the dependent loads (offsets, table, rows).
+// element) takes 32.7 us, 4.96 TB/s or 0.73 of a copy's rate.  No unit is full (ALU
+// 0.38, issue 0.49, HBM 0.55 of the peak rates in a cold launch): of 13.9 warps per issue 5.5
+// wait for loads and 2.7 for the first warp, whose chain of offsets, lengths and
+// table opens every CTA, and a CTA has two blocks' work a warp before it ends.  A
+// decode step (128 requests) takes 10 us: launch and the latency of the dependent
+// loads (offsets, table, rows).
 #include "pillar_device.cuh"
 #include "pillar_kv8.h"
 

@@ -6,8 +6,7 @@
 // start in the ring, where its released blocks go, where its positions start
 // in the slot table (kv_off) and its new tokens in new_slots (new_off).
 //
-// Two kernels:
-// A call for 2048 requests of 5700 positions each takes 19 us.
+// Two kernels, 19 us a call for 2048 requests of 1024 to 16384 positions (11.2 million):
 //   1. map_scan: one CTA, two requests a thread (2048 at a time, with carries), one
 //      block scan of the four sums; only when the ring runs short does the demand
 //      decide first, with a scan of its own.  It writes the records that the
@@ -18,9 +17,11 @@
 //   2. map_expand: slot_table[kv_off[b] + t] = block * 16 + t % 16.  A grid row of CTAs
 //      per request, a warp per 512 positions: one coalesced load of 32 blocks, then
 //      16-byte stores whose blocks come by shuffle.  (A flat grid over the slots, each
-//      tile searching its request, took 55 us for 11.6 million slots where this takes
-//      13, 3.6 TB/s.)  Blocks that were taken are entered into the
-//      table on the way.  Bound by the stores: 4 bytes per position.
+//      tile searching its request, took 55 us for those slots where this takes
+//      13, 3.5 TB/s.)  Blocks that were taken are entered into the
+//      table on the way.  It writes 4 bytes per position, at 0.52 of a copy's rate: with
+//      2048 requests each has one CTA, whose warps go through one to four
+//      dependent rounds of table line and stores.
 // The ring is first in, first out, and blocks are given back only when those
 // in it before the call and those given back together fit (they always do
 // when the tables and the ring agree on who holds what), so the places popped
@@ -262,7 +263,8 @@ cudaError_t launch_block_map(const MapArgs &a, int nsm, cudaStream_t st) {
     cudaError_t e = cudaLaunchKernelEx(&cfg, map_scan, a);
     if (e != cudaSuccess) return e;
     // per request, CTAs for its longest possible table, as long as that stays within 16 a SM
-    // (2048 requests of 8000 positions: 17.6 us a call with 16, 18.5 with 32, 21.8 with 64)
+    // (in a graph, 2048 requests of 1024 to 16384 positions: 17.8 us a call with 16, 18.7 with 32, 22.1 with 64; of 8000
+    // each: 19.1, 21.4 and 21.4; 256 of 8000: 6.8 with all three)
     const int per_cta = kExpandThreads * kBlock;
     int rows = (int)(((long long)a.max_len + per_cta - 1) / per_cta);
     const int most = 16 * nsm / a.B;

@@ -6,7 +6,8 @@
 //
 // A planner lists the sequences' row tiles, those with the most keys first.  The
 // attention kernel is persistent, one CTA per SM; CTA c takes units c, 2 G - 1 - c,
-// 2 G + c, ... of the G CTAs' rounds, so that the rounds' slopes cancel.  A unit is
+// 2 G + c, ... of the G CTAs' rounds: over many rounds their slopes cancel, over two
+// or three they do not (see below).  A unit is
 // two tiles of 128 query rows against the 128-key tiles up to the diagonal: the same
 // rows for two heads that share a KV head, or, when a group has an odd number of
 // heads, 256 consecutive rows of one:
@@ -18,16 +19,22 @@
 //     work, the tensor cores have the other's products;
 //   * two warpgroups, one per row tile, a row per thread: the whole row of scores
 //     in registers, its maximum, exponentials and sum without a shuffle, and
-//     bf16 probabilities back to tensor memory.  O is rescaled only when a row's
+//     bf16 probabilities back to tensor memory (the products take both operands in one
+//     type, and V's range needs bf16; the sum is of the unrounded ones.  It costs what
+//     the bf16 step pays too: 0.0018 to 0.0020 of the output's norm, where rounding the
+//     output alone costs 0.0015).  O is rescaled only when a row's
 //     maximum grew by more than 2^8.  At a unit's end they normalise O and write it
 //     through a 4 KB buffer a warp, so that eight lanes store 128 bytes of a row (each
 //     lane storing its own row, 16 bytes at a time, took 3000 to 4400 cycles a unit).
 // What bounds it: the tensor cores (4 D flops a visible pair; half of the diagonal
-// tile is computed and masked): 16384 tokens, 32 heads on 8, D = 128 take 1481 us,
-// 1.49 PFLOP/s of visible pairs, 0.79 of a library matrix product's rate; S reads both operands
-// from shared memory.  Short sequences (24 of 1 to 2047 tokens, the same heads: 73 us) are
-// bound by each unit's ends, D = 64 (12 of 300 to 4100, four heads on one: 55 us) by
-// the exponentials.  Keys behind a sequence's end lie in the next one:
+// tile is computed and masked): 16384 tokens, 32 heads on 8, D = 128 take 1473 to 1493 us,
+// 1.48 PFLOP/s of visible pairs, 0.79 of a library matrix product's rate; S reads both operands
+// from shared memory.  Batches of few rounds are bound by their longest CTA and by each
+// unit's ends: 24 sequences of 1 to 2047 tokens, the same heads, 73 us, where the busiest
+// CTA has 31 key tiles of two row tiles, the mean is 26, and an SM is active for 0.86 of
+// the longest's cycles; 12 of 300 to 4100, D = 64, four heads on one, 55 us, 37 against a
+// mean of 28, 0.79 of the cycles, the exponentials' pipe busy for 0.37 of an SM's own and
+// the tensor cores for 0.34.  Keys behind a sequence's end lie in the next one:
 // their scores are behind the diagonal for every row that counts, and their values
 // are zeroed in shared memory, since 0 * NaN would carry over.
 #include <cuda.h>  // CUtensorMap
