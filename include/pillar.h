@@ -70,7 +70,7 @@ extern "C" {
 #define PILLAR_FLAG_TIMEOUT 16      /* a bounded device wait gave up; outputs are incomplete */
 #define PILLAR_FLAG_TOPK 32         /* a Top-K budget exceeded max_topk (clamped) */
 #define PILLAR_FLAG_BLOCK 64        /* pillar_block_map: too few free blocks, or a bad free-ring state */
-#define PILLAR_FLAG_VALUE 128       /* pillar_kv8_append: a NaN, infinity or bad scale */
+#define PILLAR_FLAG_VALUE 128       /* pillar_kv8_append, pillar_kv4_append: a NaN, infinity or bad scale; 4 bits: past 61440 */
 
 typedef struct pillar_shape {
     int32_t B;             /* requests in the batch (>= 0) */
@@ -696,6 +696,109 @@ PILLAR_API int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, c
                                size_t ws_bytes, void *stream);
 PILLAR_API int pillar_attn_run_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k8_pool,
                                    const uint8_t *v8_pool, const float *k_scale, const float *v_scale,
+                                   const int32_t *block_table, int32_t max_blocks, const int32_t *sparse_idx,
+                                   uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
+                                   size_t ws_bytes, void *stream);
+
+/*
+ * pillar_kv8_read -- positions of the 8-bit cache as bf16 rows: a prefix for a
+ * call that takes bf16 keys, or a context on its way to the bf16 pools
+ * (pillar_kv_append).  Packed row out_off[b] + i is position first[b] + i of
+ * request b, value = code * scale rounded to bf16 (exact under the scales that
+ * pillar_kv8_append writes, but past the ends of bf16's range).
+ *
+ *   block_table   [B, max_blocks] int32
+ *   first         [B] int32, the requests' first positions
+ *   out_off       [B+1] int32, ascending from 0: the rows of each request
+ *   n             rows of k_out and v_out; rows at or past out_off[B] are left
+ *                 as they were
+ *   k_out, v_out  bf16, row i at i * k_stride (v_stride) elements: [Hkv, D] each,
+ *                 16-byte aligned rows (a stride is a multiple of 8, at least
+ *                 Hkv * D; 0 means Hkv * D).  They overlap nothing.
+ *   device_flags  device int32 or null, or-ed: PILLAR_FLAG_REQUEST for offsets or
+ *                 positions that do not fit together, n, max_len (the end of a
+ *                 request's rows) or max_blocks, PILLAR_FLAG_SLOT for a block
+ *                 outside the pool; the rows concerned are left as they were
+ * Only shape->B, Hkv, D, max_len and num_slots are used; Hkv * D is at most
+ * 2^26.  Pools are 16-byte aligned, the other arrays 4.  Asynchronous on
+ * `stream`; allocates nothing.  Returns PILLAR_OK, PILLAR_ERR_ARG or
+ * PILLAR_ERR_CUDA.
+ */
+PILLAR_API int pillar_kv8_read(const pillar_shape_t *shape, const uint8_t *k8_pool, const uint8_t *v8_pool,
+                               const float *k_scale, const float *v_scale, const int32_t *block_table,
+                               int32_t max_blocks, const int32_t *first, const int32_t *out_off, int32_t n,
+                               uint16_t *k_out, int64_t k_stride, uint16_t *v_out, int64_t v_stride,
+                               int32_t *device_flags, void *stream);
+
+/*
+ * The 4-bit cache.  K and V are held as e2m1 codes (sign, two exponent bits of
+ * bias 1, one fraction bit: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) with a scale
+ * byte for every PILLAR_KV4_GROUP neighbouring values of a row: value =
+ * code * scale.  A scale byte holds five exponent bits of bias 15 and three
+ * fraction bits, no sign: byte 8 e + m is (1 + m / 8) 2^(e - 15), or m 2^-17
+ * where e is 0.  4.5 bits a value; every value is exact in bf16 and f16.
+ *   k4_pool, v4_pool  [num_slots / 16, Hkv, 16, D / 2] bytes: dimension 2 i in the
+ *                     low half of byte i, 2 i + 1 in the high half
+ *   k_scale, v_scale  [num_slots / 16, Hkv, 16, D / 16] bytes
+ * Blocks and block tables are those of pillar_block_map.
+ */
+#define PILLAR_KV4_GROUP 16
+
+/*
+ * pillar_kv4_append -- rounds the new tokens' K and V rows into the cache.
+ * Request b's new tokens are its last ones, as in pillar_kv8_append.  For 16
+ * neighbouring values x of a row, with a = max |x|:
+ *   scale = the smallest scale s with a <= 6 s, at least 2^-17 and at most
+ *           10240 (six times that is the largest value held, 61440)
+ *   codes = x / s rounded to the nearest e2m1 value (ties to even), magnitudes
+ *           past 6 to 6; the sign of a code that stands for 0 has no meaning
+ * A row's codes and scales depend on that row alone: no other row is touched,
+ * and rows may be appended again (after a rollback) in any order.
+ *
+ * Arguments as pillar_kv8_append's.  device_flags: PILLAR_FLAG_REQUEST and
+ * PILLAR_FLAG_SLOT as there; PILLAR_FLAG_VALUE for a NaN (stored as 0), an
+ * infinity (stored as 6 s of its sign; the scale goes by the finite values) or
+ * a magnitude past 61440 (stored as 61440).
+ * Only shape->B, Hkv, D, max_len and num_slots are used; Hkv * D is at most
+ * 2^26.  k_new, v_new and the pools are 16-byte aligned, the scales 8, the other
+ * arrays 4.  Asynchronous on `stream`; allocates nothing.  Returns PILLAR_OK,
+ * PILLAR_ERR_ARG or PILLAR_ERR_CUDA.
+ */
+PILLAR_API int pillar_kv4_append(const pillar_shape_t *shape, const uint16_t *k_new, int64_t k_stride,
+                                 const uint16_t *v_new, int64_t v_stride, int32_t n, const int32_t *req_len,
+                                 const int32_t *new_off, const int32_t *block_table, int32_t max_blocks,
+                                 uint8_t *k4_pool, uint8_t *v4_pool, uint8_t *k_scale, uint8_t *v_scale,
+                                 int32_t *device_flags, void *stream);
+
+/*
+ * pillar_kv4_read -- positions of the 4-bit cache as bf16 rows (exact); the
+ * arguments are pillar_kv8_read's, the scales 8-byte aligned.
+ */
+PILLAR_API int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_pool, const uint8_t *v4_pool,
+                               const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table,
+                               int32_t max_blocks, const int32_t *first, const int32_t *out_off, int32_t n,
+                               uint16_t *k_out, int64_t k_stride, uint16_t *v_out, int64_t v_stride,
+                               int32_t *device_flags, void *stream);
+
+/*
+ * pillar_attn_kv4 -- the unified draft/verify step over the 4-bit cache:
+ * pillar_attn_kv8 with k4_pool, v4_pool and the scale bytes in the place of the
+ * 8-bit pools and scales (scales 8-byte aligned); every other argument, and
+ * what the call writes, flags and refuses, is as there.
+ *
+ * pillar_attn_run_kv4 -- the same on the plan that pillar_attn_plan left in the
+ * workspace (as pillar_attn_run): one plan for the layers of a model step.
+ *
+ * Returns PILLAR_OK, PILLAR_ERR_ARG, PILLAR_ERR_WORKSPACE or PILLAR_ERR_CUDA.
+ */
+PILLAR_API int pillar_attn_kv4(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k4_pool,
+                               const uint8_t *v4_pool, const uint8_t *k_scale, const uint8_t *v_scale,
+                               const int32_t *block_table, int32_t max_blocks, const int32_t *req_mode,
+                               const int32_t *req_len, const int32_t *sparse_idx, const int32_t *sparse_cnt,
+                               uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
+                               size_t ws_bytes, void *stream);
+PILLAR_API int pillar_attn_run_kv4(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k4_pool,
+                                   const uint8_t *v4_pool, const uint8_t *k_scale, const uint8_t *v_scale,
                                    const int32_t *block_table, int32_t max_blocks, const int32_t *sparse_idx,
                                    uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
                                    size_t ws_bytes, void *stream);

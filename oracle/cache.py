@@ -5,9 +5,12 @@ Element by element, with Python loops, sharing no code with the CUDA library:
   block_map     block tables and slot maps from request lengths
   kv8_append    new rows into the 8-bit cache (e4m3 codes, a power-of-two scale per block and KV head)
   attn_kv8      draft / verify attention over that cache
+  kv4_append    new rows into the 4-bit cache (e2m1 codes, a scale byte per 16 values of a row)
+  kv_read       positions of a cache as rows
+  attn_cache    draft / verify attention over a cache given by its values
   prompt_attn   causal attention over packed prompts
 
-Pinned by tests/test_cache_oracle_pins.py.
+Pinned by tests/test_cache_oracle_pins.py and tests/test_kv4_oracle_pins.py.
 """
 from __future__ import annotations
 
@@ -193,3 +196,121 @@ def prompt_attn(q, k, v, seq_off, scale):
             for i in range(int(a), int(e)):
                 out[i, h], lse[i, h], _ = _attend(q[i, h], k[int(a):i + 1, h // G], v[int(a):i + 1, h // G], scale)
     return out, lse
+
+
+# ---------------------------------------------------------------- the 4-bit cache
+
+GROUP = 16
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def scale4_table():
+    """Value of each of the 256 scale bytes: five exponent bits of bias 15, three fraction bits; 31 is infinity (fraction 0)
+    or NaN."""
+    v = np.empty(256)
+    for b in range(256):
+        e, m = b >> 3, b & 7
+        v[b] = m * 2.0 ** -17 if e == 0 else (math.inf if m == 0 else math.nan) if e == 31 else (8 + m) * 2.0 ** (e - 18)
+    return v
+
+
+SCALE4 = scale4_table()
+TOP4 = 226  # 10240: six times that is 61440
+
+
+def kv4_encode(x):
+    """A row [..., D] fp64 (finite) -> codes [..., D] 0 .. 15 and scale bytes [..., D / 16]."""
+    x = np.asarray(x, np.float64)
+    groups = x.reshape(x.shape[:-1] + (-1, GROUP))
+    byte = np.empty(groups.shape[:-1], np.uint8)
+    code = np.empty(groups.shape, np.uint8)
+    for i in np.ndindex(*byte.shape):
+        a = np.abs(groups[i]).max()
+        b = 1
+        while b < TOP4 and a > 6 * SCALE4[b]:
+            b += 1
+        byte[i] = b
+        for j, v in enumerate(groups[i]):
+            d = np.abs(E2M1 - min(abs(v) / SCALE4[b], 6.0))
+            near = [c for c in range(8) if d[c] == d.min()]
+            code[i + (j,)] = [c for c in near if len(near) == 1 or c % 2 == 0][0] | (8 if v < 0 else 0)
+    return code.reshape(x.shape), byte
+
+
+def kv4_codes(x):
+    """The codes nearest to values x within [-6, 6] (ties to the even one)."""
+    a = np.abs(x)
+    lo = np.searchsorted(E2M1, a, side="right") - 1
+    hi = np.minimum(lo + 1, 7)
+    dl, dh = a - E2M1[lo], E2M1[hi] - a
+    up = (dh < dl) | ((dh == dl) & (hi % 2 == 0))
+    return (np.where(up, hi, lo) | np.where(x < 0, 8, 0)).astype(np.uint8)
+
+
+def kv4_decode(codes, byte):
+    """codes [..., D] 0 .. 15, scale bytes [..., D / 16] -> values."""
+    with np.errstate(invalid="ignore"):
+        return np.where(codes & 8, -1.0, 1.0) * E2M1[codes & 7] * np.repeat(SCALE4[byte], GROUP, axis=-1)
+
+
+def kv4_pack(codes):
+    """Two codes a byte, the even dimension in the low half."""
+    return (codes[..., 0::2] | codes[..., 1::2] << 4).astype(np.uint8)
+
+
+def kv4_unpack(packed):
+    return np.stack([packed & 15, packed >> 4], -1).reshape(packed.shape[:-1] + (-1,))
+
+
+def kv4_append(codes, byte, new, req_len, new_off, table):
+    """codes [num_blocks, Hkv, 16, D] and scale bytes [num_blocks, Hkv, 16, D / 16] after the new rows [n, Hkv, D]."""
+    codes, byte = codes.copy(), byte.copy()
+    for b in range(len(req_len)):
+        n = int(new_off[b + 1]) - int(new_off[b])
+        for i in range(n):
+            t = int(req_len[b]) - n + i
+            c, s = kv4_encode(new[int(new_off[b]) + i])
+            blk = int(table[b, t // BLOCK])
+            codes[blk, :, t % BLOCK], byte[blk, :, t % BLOCK] = c, s
+    return codes, byte
+
+
+def kv_read(values, table, first, out_off, out):
+    """Rows out_off[b] + i of out [n, Hkv, D] become positions first[b] + i of request b, out of a cache given by its values
+    [num_blocks, Hkv, 16, D]."""
+    out = out.copy()
+    for b in range(len(first)):
+        for i in range(int(out_off[b + 1]) - int(out_off[b])):
+            t = int(first[b]) + i
+            out[int(out_off[b]) + i] = values[int(table[b, t // BLOCK]), :, t % BLOCK]
+    return out
+
+
+def attn_cache(q, k, v, table, req_mode, req_len, sparse_idx, sparse_cnt, k_tokens, scale):
+    """The draft / verify step over a block cache given by its values k, v [num_blocks, Hkv, 16, D] (see attn_kv8)."""
+    T, Hq, D = q.shape
+    nblk, Hkv = k.shape[:2]
+    G, row = Hq // Hkv, 0
+    out, logits, lse = np.zeros_like(q), [], []
+    for b in range(len(req_len)):
+        L, verify = int(req_len[b]), int(req_mode[b]) == 1
+        nq = k_tokens + 1 if verify else 1
+        dump, z = np.full((Hq, nq, L), -math.inf), np.full((Hq, nq), -math.inf)
+        for g in range(Hkv):
+            listed = range(L) if verify else [int(t) for t in sparse_idx[b, g, :int(sparse_cnt[b, g])]]
+            t = np.array([x for x in listed if 0 <= x < L and 0 <= int(table[b, x // BLOCK]) < nblk], np.int64)
+            blk = table[b, t // BLOCK].astype(np.int64) if len(t) else np.zeros(0, np.int64)
+            kk, vv = k[blk, g, t % BLOCK], v[blk, g, t % BLOCK]
+            for j in range(nq):
+                n = int(np.searchsorted(t, L - nq + j, side="right")) if verify else len(t)
+                for h in range(g * G, (g + 1) * G):
+                    out[row + j, h], zz, s = _attend(q[row + j, h], kk[:n], vv[:n], scale)
+                    if verify:
+                        dump[h, j, t[:n]] = s
+                        z[h, j] = zz
+        if verify:
+            logits.append(dump.reshape(-1))
+            lse.append(z)
+        row += nq
+    return (out, np.concatenate(logits) if logits else np.zeros(0),
+            np.stack(lse) if lse else np.zeros((0, Hq, k_tokens + 1)))

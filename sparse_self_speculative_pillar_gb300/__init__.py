@@ -40,6 +40,10 @@ Entry points (same names as the C ABI):
                   out, verify_logits, verify_lse, workspace, stream=None)   (the unified step over the 8-bit cache)
   pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
                       verify_lse, workspace, stream=None)        (the same on a plan of pillar_attn_plan)
+  pillar_kv8_read(shape, k8_pool, v8_pool, k_scale, v_scale, block_table, first, out_off, k_out, v_out,
+                  device_flags=None, stream=None)                (positions of the 8-bit cache as bf16 rows)
+  pillar_kv4_append(...), pillar_kv4_read(...), pillar_attn_kv4(...), pillar_attn_run_kv4(...)
+                                                                 (the same four over the 4-bit cache)
   pillar_prompt_attn_workspace_bytes(shape, n)
   pillar_prompt_attn(shape, q, k, v, seq_off, out, lse, workspace, stream=None)   (causal attention over packed prompts)
 """
@@ -62,12 +66,14 @@ __all__ = [
     "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
     "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
     "pillar_attn_kv8", "pillar_attn_run_kv8", "pillar_prompt_attn_workspace_bytes", "pillar_prompt_attn",
-    "FLAG_BLOCK", "FLAG_VALUE", "KV_BLOCK",
+    "pillar_kv8_read", "pillar_kv4_append", "pillar_kv4_read", "pillar_attn_kv4", "pillar_attn_run_kv4",
+    "FLAG_BLOCK", "FLAG_VALUE", "KV_BLOCK", "KV4_GROUP",
 ]
 
 FLAG_INDEX, FLAG_SLOT, FLAG_REQUEST, FLAG_COUNT, FLAG_TIMEOUT, FLAG_TOPK = 1, 2, 4, 8, 16, 32
 FLAG_BLOCK, FLAG_VALUE = 64, 128
 KV_BLOCK = 16  # PILLAR_KV_BLOCK: tokens of a cache block
+KV4_GROUP = 16  # PILLAR_KV4_GROUP: values of a row that share a scale byte in the 4-bit cache
 # values of PillarShape.schedule (PILLAR_SCHEDULE_* in the header)
 SCHEDULE_UNIFIED, SCHEDULE_DRAFT_ONLY, SCHEDULE_VERIFY_ONLY, SCHEDULE_UNIFORM_ROWS, SCHEDULE_NAIVE_JOINT = 0, 1, 2, 3, 4
 EXPORTED = ("pillar_attn_workspace_bytes", "pillar_attn_unified", "pillar_attn_unified_slotted",
@@ -79,7 +85,8 @@ EXPORTED = ("pillar_attn_workspace_bytes", "pillar_attn_unified", "pillar_attn_u
             "pillar_offload_reserve", "pillar_offload_release", "pillar_offload_evict", "pillar_offload_reload",
             "pillar_block_map_workspace_bytes", "pillar_block_map", "pillar_kv8_append",
             "pillar_attn_kv8", "pillar_attn_run_kv8",
-            "pillar_prompt_attn_workspace_bytes", "pillar_prompt_attn")
+            "pillar_prompt_attn_workspace_bytes", "pillar_prompt_attn",
+            "pillar_kv8_read", "pillar_kv4_append", "pillar_kv4_read", "pillar_attn_kv4", "pillar_attn_run_kv4")
 MAX_BUCKETS = 64  # PILLAR_MAX_BUCKETS
 OFFLOAD_QUEUE = 1024  # PILLAR_OFFLOAD_QUEUE
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024 + 256
@@ -188,6 +195,11 @@ def load():
     lib.pillar_kv8_append.argtypes = [SP, P, I64, P, I64, I32, P, P, P, I32, P, P, P, P, P, P]
     lib.pillar_attn_kv8.argtypes = [SP] + [P] * 6 + [I32] + [P] * 8 + [SZ, P]
     lib.pillar_attn_run_kv8.argtypes = [SP] + [P] * 6 + [I32] + [P] * 5 + [SZ, P]
+    for fmt in ("kv4", "kv8"):
+        getattr(lib, f"pillar_{fmt}_read").argtypes = [SP, P, P, P, P, P, I32, P, P, I32, P, I64, P, I64, P, P]
+    lib.pillar_kv4_append.argtypes = lib.pillar_kv8_append.argtypes
+    lib.pillar_attn_kv4.argtypes = lib.pillar_attn_kv8.argtypes
+    lib.pillar_attn_run_kv4.argtypes = lib.pillar_attn_run_kv8.argtypes
     lib.pillar_prompt_attn_workspace_bytes.argtypes = [SP, I32, ctypes.POINTER(SZ)]
     lib.pillar_prompt_attn.argtypes = [SP, P, I64, P, I64, P, I64, I32, P, P, P, P, SZ, P]
     lib.pillar_status_string.restype = ctypes.c_char_p
@@ -386,6 +398,7 @@ class _Types:
         self.i32, self.i64, self.f32 = (torch.int32,), (torch.int64,), (torch.float32,)
         self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 bits travel in 16-bit integers too
         self.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+        self.bytes = (torch.uint8, torch.int8)
         torch.cuda.init()
         self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         return self.__dict__[name]
@@ -489,32 +502,79 @@ def _pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev):
             _arg("k_scale", k_scale, _T.f32, blocks, dev), _arg("v_scale", v_scale, _T.f32, blocks, dev))
 
 
+def _pool4(shape, k4_pool, v4_pool, k_scale, v_scale, dev):
+    rows = (shape.num_slots // KV_BLOCK, shape.Hkv, KV_BLOCK)
+    codes, groups = rows + (shape.D // 2,), rows + (shape.D // KV4_GROUP,)
+    return (_arg("k4_pool", k4_pool, _T.bytes, codes, dev), _arg("v4_pool", v4_pool, _T.bytes, codes, dev),
+            _arg("k_scale", k_scale, _T.bytes, groups, dev), _arg("v_scale", v_scale, _T.bytes, groups, dev))
+
+
 def pillar_kv8_append(shape, k_new, v_new, req_len, new_off, block_table, k8_pool, v8_pool, k_scale, v_scale,
                       device_flags=None, stream=None):
     """The new tokens' K/V rows ([n, Hkv, D] bf16, tokens may lie apart) as e4m3 codes under the scales of their blocks;
     request b's rows new_off[b] .. new_off[b+1]-1 are its last positions."""
+    _append("pillar_kv8_append", _pool8, shape, k_new, v_new, req_len, new_off, block_table,
+            (k8_pool, v8_pool, k_scale, v_scale), device_flags, stream)
+
+
+def pillar_kv4_append(shape, k_new, v_new, req_len, new_off, block_table, k4_pool, v4_pool, k_scale, v_scale,
+                      device_flags=None, stream=None):
+    """The same into the 4-bit cache: e2m1 codes and a scale byte for every 16 values of a row."""
+    _append("pillar_kv4_append", _pool4, shape, k_new, v_new, req_len, new_off, block_table,
+            (k4_pool, v4_pool, k_scale, v_scale), device_flags, stream)
+
+
+def _append(name, pool, shape, k_new, v_new, req_len, new_off, block_table, cache, device_flags, stream):
     dev, B = _T.device(), shape.B
     n, width = _dim32("k_new", k_new, 0, 3), _dim32("block_table", block_table, 1, 2)
     kp, ks = _rows("k_new", k_new, n, shape.Hkv, shape.D, dev)
     vp, vs = _rows("v_new", v_new, n, shape.Hkv, shape.D, dev)
-    st = load().pillar_kv8_append(
+    st = getattr(load(), name)(
         ctypes.byref(shape), kp, ks, vp, vs, n, _arg("req_len", req_len, _T.i32, (B,), dev),
         _arg("new_off", new_off, _T.i32, (B + 1,), dev), _arg("block_table", block_table, _T.i32, (B, width), dev),
-        width, *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
+        width, *pool(shape, *cache, dev),
         None if device_flags is None else _arg("device_flags", device_flags, _T.i32, (1,), dev),
         _raw_stream(stream, dev))
     if st:
-        raise PillarError("pillar_kv8_append", st)
+        raise PillarError(name, st)
 
 
-def _kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev):
+def pillar_kv8_read(shape, k8_pool, v8_pool, k_scale, v_scale, block_table, first, out_off, k_out, v_out,
+                    device_flags=None, stream=None):
+    """Positions of the 8-bit cache as bf16 rows ([n, Hkv, D], tokens may lie apart): rows out_off[b] .. out_off[b+1]-1 are
+    the positions of request b from first[b] on."""
+    _read("pillar_kv8_read", _pool8, shape, (k8_pool, v8_pool, k_scale, v_scale), block_table, first, out_off, k_out, v_out,
+          device_flags, stream)
+
+
+def pillar_kv4_read(shape, k4_pool, v4_pool, k_scale, v_scale, block_table, first, out_off, k_out, v_out,
+                    device_flags=None, stream=None):
+    """The same out of the 4-bit cache."""
+    _read("pillar_kv4_read", _pool4, shape, (k4_pool, v4_pool, k_scale, v_scale), block_table, first, out_off, k_out, v_out,
+          device_flags, stream)
+
+
+def _read(name, pool, shape, cache, block_table, first, out_off, k_out, v_out, device_flags, stream):
+    dev, B = _T.device(), shape.B
+    n, width = _dim32("k_out", k_out, 0, 3), _dim32("block_table", block_table, 1, 2)
+    kp, ks = _rows("k_out", k_out, n, shape.Hkv, shape.D, dev)
+    vp, vs = _rows("v_out", v_out, n, shape.Hkv, shape.D, dev)
+    st = getattr(load(), name)(
+        ctypes.byref(shape), *pool(shape, *cache, dev), _arg("block_table", block_table, _T.i32, (B, width), dev), width,
+        _arg("first", first, _T.i32, (B,), dev), _arg("out_off", out_off, _T.i32, (B + 1,), dev), n, kp, ks, vp, vs,
+        None if device_flags is None else _arg("device_flags", device_flags, _T.i32, (1,), dev),
+        _raw_stream(stream, dev))
+    if st:
+        raise PillarError(name, st)
+
+
+def _attn_cache_args(shape, q, pool, cache, block_table, dev):
     width = _dim32("block_table", block_table, 1, 2)
-    return (_arg("q", q, _T.bf16, (_dim("q", q, 0, 3), shape.Hq, shape.D), dev),
-            *_pool8(shape, k8_pool, v8_pool, k_scale, v_scale, dev),
+    return (_arg("q", q, _T.bf16, (_dim("q", q, 0, 3), shape.Hq, shape.D), dev), *pool(shape, *cache, dev),
             _arg("block_table", block_table, _T.i32, (shape.B, width), dev), width)
 
 
-def _kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev):
+def _attn_cache_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev):
     return (_arg("out", out, _T.bf16, q.shape, dev),
             None if verify_logits is None else
             _arg("verify_logits", verify_logits, _T.f32, (_dim("verify_logits", verify_logits, 0, 1),), dev),
@@ -522,31 +582,56 @@ def _kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev):
             *_workspace(workspace, dev))
 
 
+def _attn_cache(name, pool, shape, q, cache, block_table, req_mode, req_len, sparse_idx, sparse_cnt, out, verify_logits,
+                verify_lse, workspace, stream):
+    dev, B = _T.device(), shape.B
+    st = getattr(load(), name)(
+        ctypes.byref(shape), *_attn_cache_args(shape, q, pool, cache, block_table, dev),
+        _arg("req_mode", req_mode, _T.i32, (B,), dev), _arg("req_len", req_len, _T.i32, (B,), dev),
+        _arg("sparse_idx", sparse_idx, _T.i32, (B, shape.Hkv, shape.max_sparse), dev),
+        _arg("sparse_cnt", sparse_cnt, _T.i32, (B, shape.Hkv), dev),
+        *_attn_cache_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _raw_stream(stream, dev))
+    if st:
+        raise PillarError(name, st)
+
+
+def _attn_run_cache(name, pool, shape, q, cache, block_table, sparse_idx, out, verify_logits, verify_lse, workspace, stream):
+    dev = _T.device()
+    st = getattr(load(), name)(
+        ctypes.byref(shape), *_attn_cache_args(shape, q, pool, cache, block_table, dev),
+        _arg("sparse_idx", sparse_idx, _T.i32, (shape.B, shape.Hkv, shape.max_sparse), dev),
+        *_attn_cache_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _raw_stream(stream, dev))
+    if st:
+        raise PillarError(name, st)
+
+
 def pillar_attn_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, req_mode, req_len, sparse_idx, sparse_cnt,
                     out, verify_logits, verify_lse, workspace, stream=None):
     """The unified draft/verify step over the 8-bit cache; verify_logits None: no dump.  (The sizes of q, out, the logits
     and the LSEs follow from modes and lengths that only the device knows, as in pillar_attn_unified.)"""
-    dev, B = _T.device(), shape.B
-    st = load().pillar_attn_kv8(
-        ctypes.byref(shape), *_kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev),
-        _arg("req_mode", req_mode, _T.i32, (B,), dev), _arg("req_len", req_len, _T.i32, (B,), dev),
-        _arg("sparse_idx", sparse_idx, _T.i32, (B, shape.Hkv, shape.max_sparse), dev),
-        _arg("sparse_cnt", sparse_cnt, _T.i32, (B, shape.Hkv), dev),
-        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _raw_stream(stream, dev))
-    if st:
-        raise PillarError("pillar_attn_kv8", st)
+    _attn_cache("pillar_attn_kv8", _pool8, shape, q, (k8_pool, v8_pool, k_scale, v_scale), block_table, req_mode, req_len,
+                sparse_idx, sparse_cnt, out, verify_logits, verify_lse, workspace, stream)
 
 
 def pillar_attn_run_kv8(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
                         verify_lse, workspace, stream=None):
     """pillar_attn_kv8 on the plan that pillar_attn_plan left in the workspace."""
-    dev = _T.device()
-    st = load().pillar_attn_run_kv8(
-        ctypes.byref(shape), *_kv8_args(shape, q, k8_pool, v8_pool, k_scale, v_scale, block_table, dev),
-        _arg("sparse_idx", sparse_idx, _T.i32, (shape.B, shape.Hkv, shape.max_sparse), dev),
-        *_kv8_outputs(shape, q, out, verify_logits, verify_lse, workspace, dev), _raw_stream(stream, dev))
-    if st:
-        raise PillarError("pillar_attn_run_kv8", st)
+    _attn_run_cache("pillar_attn_run_kv8", _pool8, shape, q, (k8_pool, v8_pool, k_scale, v_scale), block_table, sparse_idx,
+                    out, verify_logits, verify_lse, workspace, stream)
+
+
+def pillar_attn_kv4(shape, q, k4_pool, v4_pool, k_scale, v_scale, block_table, req_mode, req_len, sparse_idx, sparse_cnt,
+                    out, verify_logits, verify_lse, workspace, stream=None):
+    """The unified draft/verify step over the 4-bit cache; verify_logits None: no dump."""
+    _attn_cache("pillar_attn_kv4", _pool4, shape, q, (k4_pool, v4_pool, k_scale, v_scale), block_table, req_mode, req_len,
+                sparse_idx, sparse_cnt, out, verify_logits, verify_lse, workspace, stream)
+
+
+def pillar_attn_run_kv4(shape, q, k4_pool, v4_pool, k_scale, v_scale, block_table, sparse_idx, out, verify_logits,
+                        verify_lse, workspace, stream=None):
+    """pillar_attn_kv4 on the plan that pillar_attn_plan left in the workspace."""
+    _attn_run_cache("pillar_attn_run_kv4", _pool4, shape, q, (k4_pool, v4_pool, k_scale, v_scale), block_table, sparse_idx,
+                    out, verify_logits, verify_lse, workspace, stream)
 
 
 # --------------------------------------------------------------- prompts

@@ -11,6 +11,7 @@
 #include "pillar_internal.h"
 #include "pillar_kv.h"
 #include "pillar_kv8.h"
+#include "pillar_kv4.h"
 #include "pillar_lists.h"
 #include "pillar_map.h"
 #include "pillar_prompt.h"
@@ -578,6 +579,169 @@ int pillar_attn_kv8(const pillar_shape_t *shape, const uint16_t *q, const uint8_
     const int sp = pillar_attn_plan(shape, req_mode, req_len, sparse_cnt, workspace, ws_bytes, stream);
     if (sp != PILLAR_OK || shape->B == 0) return sp;
     return run_kv8(*shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, stream);
+}
+
+// Sizes that the calls over packed rows of a quantised cache go by: 32-bit counts of a token's 16-byte pieces.
+static bool packed_rows(const pillar_shape_t &s, int32_t n, int32_t max_blocks) {
+    return n >= 0 && pool_blocks(s) >= 1 && max_blocks >= 1 && (long long)s.Hkv * s.D <= (1ll << 26);
+}
+
+int pillar_kv4_append(const pillar_shape_t *shape, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
+                      int64_t v_stride, int32_t n, const int32_t *req_len, const int32_t *new_off,
+                      const int32_t *block_table, int32_t max_blocks, uint8_t *k4_pool, uint8_t *v4_pool,
+                      uint8_t *k_scale, uint8_t *v_scale, int32_t *device_flags, void *stream) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    Kv4AppendArgs a;
+    if (!packed_rows(*shape, n, max_blocks) || !row_stride(k_stride, shape->Hkv, shape->D, &a.k_stride) ||
+        !row_stride(v_stride, shape->Hkv, shape->D, &a.v_stride))
+        return PILLAR_ERR_ARG;
+    if (n == 0 || shape->B == 0) return PILLAR_OK;
+    if (!k_new || !v_new || !req_len || !new_off || !block_table || !k4_pool || !v4_pool || !k_scale || !v_scale)
+        return PILLAR_ERR_ARG;
+    for (const void *p : {(const void *)k_new, (const void *)v_new, (const void *)k4_pool, (const void *)v4_pool})
+        if (!aligned(p, 16)) return PILLAR_ERR_ARG;
+    if (!aligned(k_scale, 8) || !aligned(v_scale, 8) || !aligned(req_len, 4) || !aligned(new_off, 4) ||
+        !aligned(block_table, 4) || !aligned(device_flags, 4))
+        return PILLAR_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.req_len = req_len;
+    a.new_off = new_off;
+    a.table = block_table;
+    a.k4 = k4_pool;
+    a.v4 = v4_pool;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.flags = device_flags;
+    a.n = n;
+    a.B = shape->B;
+    a.Hkv = shape->Hkv;
+    a.D = shape->D;
+    a.max_blocks = max_blocks;
+    a.num_blocks = pool_blocks(*shape);
+    a.max_len = shape->max_len;
+    return launch_kv4_append(a, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+// Both reads: `bits` of a code, and the alignment of the scales.
+static int kv_read(const pillar_shape_t *shape, int bits, size_t scale_align, KvReadArgs a, int64_t k_stride,
+                   int64_t v_stride, void *stream) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    if (!packed_rows(*shape, a.n, a.max_blocks) || !row_stride(k_stride, shape->Hkv, shape->D, &a.k_stride) ||
+        !row_stride(v_stride, shape->Hkv, shape->D, &a.v_stride))
+        return PILLAR_ERR_ARG;
+    if (a.n == 0 || shape->B == 0) return PILLAR_OK;
+    if (!a.k || !a.v || !a.k_scale || !a.v_scale || !a.table || !a.first || !a.out_off || !a.k_out || !a.v_out)
+        return PILLAR_ERR_ARG;
+    for (const void *p : {(const void *)a.k, (const void *)a.v, (const void *)a.k_out, (const void *)a.v_out})
+        if (!aligned(p, 16)) return PILLAR_ERR_ARG;
+    if (!aligned(a.k_scale, scale_align) || !aligned(a.v_scale, scale_align) || !aligned(a.table, 4) ||
+        !aligned(a.first, 4) || !aligned(a.out_off, 4) || !aligned(a.flags, 4))
+        return PILLAR_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    a.B = shape->B;
+    a.Hkv = shape->Hkv;
+    a.D = shape->D;
+    a.num_blocks = pool_blocks(*shape);
+    a.max_len = shape->max_len;
+    a.bits = bits;
+    return launch_kv_read(a, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_pool, const uint8_t *v4_pool,
+                    const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table, int32_t max_blocks,
+                    const int32_t *first, const int32_t *out_off, int32_t n, uint16_t *k_out, int64_t k_stride,
+                    uint16_t *v_out, int64_t v_stride, int32_t *device_flags, void *stream) {
+    KvReadArgs a = {};
+    a.k = k4_pool, a.v = v4_pool, a.k_scale = k_scale, a.v_scale = v_scale, a.table = block_table;
+    a.max_blocks = max_blocks, a.first = first, a.out_off = out_off, a.n = n, a.k_out = k_out, a.v_out = v_out;
+    a.flags = device_flags;
+    return kv_read(shape, 4, 8, a, k_stride, v_stride, stream);
+}
+
+int pillar_kv8_read(const pillar_shape_t *shape, const uint8_t *k8_pool, const uint8_t *v8_pool,
+                    const float *k_scale, const float *v_scale, const int32_t *block_table, int32_t max_blocks,
+                    const int32_t *first, const int32_t *out_off, int32_t n, uint16_t *k_out, int64_t k_stride,
+                    uint16_t *v_out, int64_t v_stride, int32_t *device_flags, void *stream) {
+    KvReadArgs a = {};
+    a.k = k8_pool, a.v = v8_pool, a.k_scale = k_scale, a.v_scale = v_scale, a.table = block_table;
+    a.max_blocks = max_blocks, a.first = first, a.out_off = out_off, a.n = n, a.k_out = k_out, a.v_out = v_out;
+    a.flags = device_flags;
+    return kv_read(shape, 8, 4, a, k_stride, v_stride, stream);
+}
+
+// The host checks of an attention run over the 4-bit cache.
+static int attn_kv4_checks(const pillar_shape_t *shape, const uint16_t *q, const Kv4Cache &c, const int32_t *sparse_idx,
+                           const uint16_t *out, const float *verify_logits, const float *verify_lse,
+                           const void *workspace, size_t ws_bytes) {
+    const int st = check_shape(shape);
+    if (st != PILLAR_OK) return st;
+    const pillar_shape_t &s = *shape;
+    if (s.schedule > PILLAR_SCHEDULE_VERIFY_ONLY) return PILLAR_ERR_ARG;
+    if (s.B == 0) return PILLAR_OK;
+    if (pool_blocks(s) < 1 || c.max_blocks < 1) return PILLAR_ERR_ARG;
+    if (!q || !c.k4 || !c.v4 || !c.k_scale || !c.v_scale || !c.table || !out || !verify_lse) return PILLAR_ERR_ARG;
+    if (s.max_sparse > 0 && !sparse_idx) return PILLAR_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(c.k4, 16) || !aligned(c.v4, 16) || !aligned(out, 16) || !aligned(c.k_scale, 8) ||
+        !aligned(c.v_scale, 8) || !aligned(c.table, 4) || !aligned(sparse_idx, 4) || !aligned(verify_logits, 8) ||
+        !aligned(verify_lse, 4))
+        return PILLAR_ERR_ARG;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < attn_layout(s).total) return PILLAR_ERR_WORKSPACE;
+    return PILLAR_OK;
+}
+
+static int run_kv4(const pillar_shape_t &s, const uint16_t *q, Kv4Cache c, const int32_t *sparse_idx, uint16_t *out,
+                   float *verify_logits, float *verify_lse, void *workspace, void *stream) {
+    c.num_blocks = pool_blocks(s);
+    const int nsm = sm_count();
+    if (nsm <= 0) return PILLAR_ERR_CUDA;
+    AttnArgs aa = {};
+    aa.q = q;
+    aa.sparse_idx = sparse_idx;
+    aa.out = out;
+    aa.logits = verify_logits;
+    aa.lse = verify_lse;
+    aa.ws = static_cast<char *>(workspace);
+    aa.lay = attn_layout(s);
+    aa.num_slots = s.num_slots;
+    aa.Hq = s.Hq;
+    aa.Hkv = s.Hkv;
+    aa.D = s.D;
+    aa.k = s.k;
+    aa.max_sparse = s.max_sparse;
+    aa.schedule = s.schedule;
+    aa.scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / std::sqrt((float)s.D);
+    aa.wait_ns = s.wait_timeout_us > 0 ? (unsigned long long)s.wait_timeout_us * 1000ull : kWaitTimeoutNs;
+    return launch_attn_kv4(aa, c, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+}
+
+int pillar_attn_run_kv4(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k4_pool, const uint8_t *v4_pool,
+                        const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table, int32_t max_blocks,
+                        const int32_t *sparse_idx, uint16_t *out, float *verify_logits, float *verify_lse,
+                        void *workspace, size_t ws_bytes, void *stream) {
+    const Kv4Cache c{k4_pool, v4_pool, k_scale, v_scale, block_table, max_blocks, 0};
+    const int st = attn_kv4_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
+    if (st != PILLAR_OK || shape->B == 0) return st;
+    return run_kv4(*shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, stream);
+}
+
+int pillar_attn_kv4(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k4_pool, const uint8_t *v4_pool,
+                    const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table, int32_t max_blocks,
+                    const int32_t *req_mode, const int32_t *req_len, const int32_t *sparse_idx,
+                    const int32_t *sparse_cnt, uint16_t *out, float *verify_logits, float *verify_lse, void *workspace,
+                    size_t ws_bytes, void *stream) {
+    // the run's checks first, so that a bad call enqueues nothing
+    const Kv4Cache c{k4_pool, v4_pool, k_scale, v_scale, block_table, max_blocks, 0};
+    const int st = attn_kv4_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
+    if (st != PILLAR_OK) return st;
+    const int sp = pillar_attn_plan(shape, req_mode, req_len, sparse_cnt, workspace, ws_bytes, stream);
+    if (sp != PILLAR_OK || shape->B == 0) return sp;
+    return run_kv4(*shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, stream);
 }
 
 int pillar_prompt_attn_workspace_bytes(const pillar_shape_t *shape, int32_t n, size_t *bytes) {

@@ -177,6 +177,14 @@ struct Kv8Cache {
 };
 cudaError_t launch_attn_kv8(const AttnArgs &a, const Kv8Cache &c, int nsm, cudaStream_t st);
 
+// The 4-bit cache of an attention run.
+struct Kv4Cache {
+    const uint8_t *k4, *v4, *k_scale, *v_scale;
+    const int *table;
+    int max_blocks, num_blocks;
+};
+cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaStream_t st);
+
 struct TopkArgs {
     const float *logits, *lse;
     const int *req_len, *group_map, *K;
