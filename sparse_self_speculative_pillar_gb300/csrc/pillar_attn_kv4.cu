@@ -5,15 +5,47 @@
 // The planner, its work items, the partial records and the merge of split
 // units are those of the bf16 step; only the kernel between them differs.
 //
-// A warp has a query row of an item, a lane D / 32 of its dimensions, and
-// walks over the keys with a running maximum and sum.
+// Every cache value is an f16 value (six significant bits within 2^-18 ..
+// 61440), and so is a bf16 query row divided by a power of two (its largest
+// magnitude brought to [2^14, 2^15)), but for elements 2^-28 below that.  So
+// both products take f16 operands and the scores are sums of exact products.
+//
+// One persistent CTA an SM, 128 keys a tile, the keys on the M of tcgen05:
+//     S^T [keys x rows] = K Q^T      K from tensor memory, Q from shared memory
+//     O^T [D x rows]   += V^T P^T    V and P from shared memory
+// so that a key's row is made into an operand once, whatever the number of
+// query rows, and a few rows (N is a multiple of 16) cost little.
+//   * The resolver warp takes items from the planner's queue and turns their
+//     keys into rows of the pools, 512 at a time.
+//   * Four warps each for K and V copy the rows of the tiles ahead (16 bytes a
+//     lane), turn a key's 64 bytes of codes into f16 and write them to tensor
+//     memory (K: lane = key) or swizzled shared memory (V: keys x D, MN-major).
+//   * One warp issues all products.
+//   * Eight softmax warps, a key a thread: two groups of four that take tiles in
+//     turn where an item has at most 16 rows (each with its own O and reference
+//     maxima), and share the rows of every tile where it has more.  A reference
+//     maximum moves only when a score passes it by more than 2^8, which a vote of
+//     the group finds out.  P is rounded to f16 relative to it: weights are at
+//     most 2^14, and 2^6 or more for a row's largest.
+//   * Four warps write finished items, two stage queries.
 #include "pillar_kv4.cuh"
 
 namespace pillar {
 
 namespace {
 
-constexpr int kThreads4 = 256;
+constexpr int kTile = 128;                   // keys of a tile
+constexpr int kChunkTiles = 4;               // tiles whose rows are resolved together
+constexpr int kChunkKeys = kTile * kChunkTiles;
+constexpr int kChunks = 3;                   // chunks in flight between the resolver and their readers
+constexpr int kItems = 8;                    // items in flight
+constexpr int kStages = 4;                   // tiles of codes in shared memory
+constexpr int kWarps = 24;
+constexpr int kThreads4 = kWarps * 32;
+constexpr float kLift = 6.f;                 // log2 of the weight of a probability at its row's reference maximum
+constexpr float kGrow = 8.f + kLift;         // the reference moves once a weight passes 2^kGrow
+// tensor memory: two tiles of K, two of S^T, the O^T of two items
+constexpr uint32_t kTmemCols = 512, kTmemK = 0, kTmemS = 128, kTmemO = 256;
 
 struct Kv4Params {
     const uint16_t *q;
@@ -29,100 +61,844 @@ struct Kv4Params {
     float *part_o, *part_lse;
     int Hq, Hkv, G, k, M, max_sparse;
     float scale;
+    unsigned long long wait_ns;
 };
 
-// Dimensions [N lane, N lane + N) of a cache row.
+// A work item in shared memory.
+struct alignas(16) ItemRec {
+    int stop;               // no more items
+    int tiles, rows, verify;
+    int n, begin, L, g;     // keys; first one (verify: its position); context length; KV head
+    int q_off, vidx, nsplit, rec;
+    long long logit_off;
+    int pad[2];
+};
+
+template <int D>
+struct Smem4 {
+    static constexpr int kRow = D / 2, kScales = D / kGroup4;  // bytes of a key's codes and scales
+    alignas(1024) uint8_t v[2][kTile * D * 2];  // V operands: 64-dimension halves of [128 keys][128 bytes], 128-byte swizzle
+    alignas(1024) uint8_t p[2][kTile * 128];    // P operands: 16-row groups of [128 keys][32 bytes], 32-byte swizzle
+    alignas(1024) uint8_t q[2][kMaxRows * D * 2];  // Q operands: 64-dimension halves of [64 rows][128 bytes], 128-byte swizzle
+    alignas(128) uint8_t codes[2][kStages][kTile * kRow];    // K, V
+    alignas(16) uint8_t scales[2][kStages][kTile * kScales];
+    alignas(16) int row[kChunks][kChunkKeys];   // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
+    int chunk_tiles[kChunks];                   // 0: no more
+    ItemRec item[kItems];
+    // per query row: logit = sum * fac, in base-2 units sum * fac2; last position seen; its logits (offset of position 0, or -1)
+    alignas(16) float fac[kItems][kMaxRows], fac2[kItems][kMaxRows];
+    int lim[kItems][kMaxRows];
+    long long lb[kItems][kMaxRows];
+    // per item (in turn), group and row of the group: kLift - reference maximum (base 2); sums of weights per warp
+    alignas(16) float nref[2][2][32], sum[2][2][4][32];
+    float top[2][4][32];                        // a group's largest scores, per warp
+    uint64_t item_full[kItems], item_empty[kItems], fac_full[kItems];
+    uint64_t rows_full[kChunks], rows_empty[kChunks];
+    uint64_t q_full[2], q_empty[2], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], pv_done[2];
+    uint64_t o_full[2], o_empty[2], epi_full[2], epi_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(Smem4<128>) <= 227 * 1024, "shared memory of a CTA");
+static_assert(sizeof(Smem4<64>) > 114 * 1024, "never two CTAs on an SM: each takes all of its tensor memory");
+
+struct Bounds4 {
+    volatile int *abort;
+    int *err;
+    unsigned long long ns;
+};
+// A bounded wait by a whole warp: the first test inline, the polling out of line (a function per register count).
+template <int kRegs>
+__device__ __noinline__ bool poll4(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, unsigned long long ns) {
+    return mbar_wait_warp(bar, parity, abort, err, ns);
+}
+template <int kRegs>
+__device__ __forceinline__ bool wait4(uint64_t *bar, uint32_t parity, const Bounds4 &b) {
+    return mbar_try_wait_warp(bar, parity) || poll4<kRegs>(bar, parity, b.abort, b.err, b.ns);
+}
+constexpr int kRegsSoftmax = 104, kRegsConvert = 72, kRegsRest = 64;
+static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + 2 * kRegsRest <= kThreads4 / 128 * 80, "the registers at launch");
+
+__device__ __forceinline__ void arrive_lane0(uint64_t *bar, uint32_t count = 1) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_cnt(bar, count);
+}
+__device__ __forceinline__ bool elect_one4() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ bool test4(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+}
+
+__device__ __forceinline__ void copy16(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 template <int N>
-__device__ __forceinline__ void row_values(const uint8_t *codes, const uint8_t *scale, size_t row, int lane, float (&v)[N]) {
-    const uint8_t *src = codes + row * (N * 16) + lane * (N / 2);
-    const uint32_t w = N == 4 ? *reinterpret_cast<const uint16_t *>(src) : *src;
-    uint32_t h[4];
-    f16_of_e2m1(w, h);
-    const uint32_t s = scale_pair(scale[row * (N * 32 / kGroup4) + lane * N / kGroup4], 0);
+__device__ __forceinline__ void copy_small(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Columns of this thread's tensor-memory lane; the loads and stores are waited for together.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+// How an item's query rows are shared by the softmax groups: at most 16 rows, the groups take tiles in turn; else group 0
+// has the first `first` chunks of eight rows and group 1 the others.
+__device__ __forceinline__ bool takes_turns(int rows) { return rows <= 16; }
+__device__ __forceinline__ int first_chunks(int rows) { return ((rows + 7) / 8 + 1) / 2; }
+
+// ------------------------------------------------------------------ resolver warp
+
+template <int D>
+__device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, int lane) {
+    const int num_items = *reinterpret_cast<volatile int *>(&p.hdr->num_items);
+    int slot = 0;  // of the next chunk
+    uint32_t phase = 0;
+    for (int i = 0;; ++i) {
+        const int is = i % kItems;
+        if (!wait4<kRegsRest>(&sm.item_empty[is], (i / kItems & 1) ^ 1, bd)) return;
+        int it = 0;
+        if (lane == 0) it = atomicAdd(&p.hdr->item_counter, 1);
+        it = __shfl_sync(0xffffffffu, it, 0);
+        if (it >= num_items) {
+            if (lane == 0) sm.item[is].stop = 1;
+            arrive_lane0(&sm.item_full[is]);
+            if (!wait4<kRegsRest>(&sm.rows_empty[slot], phase ^ 1, bd)) return;
+            if (lane == 0) sm.chunk_tiles[slot] = 0;
+            arrive_lane0(&sm.rows_full[slot]);
+            return;
+        }
+        const Item itm = p.items[it];
+        const int b = itm.unit / p.Hkv, g = itm.unit - b * p.Hkv;
+        const ReqInfo ri = p.req[b];
+        const UnitInfo ui = p.unit[itm.unit];
+        const bool verify = ri.mode == 1;
+        const int n = itm.end - itm.begin, tiles = max(1, (n + kTile - 1) / kTile);
+        if (lane == 0) {
+            ItemRec r;
+            r.stop = 0;
+            r.tiles = tiles;
+            r.rows = verify ? p.M : p.G;
+            r.verify = verify;
+            r.n = n;
+            r.begin = itm.begin;
+            r.L = ri.len;
+            r.g = g;
+            r.q_off = ri.q_off;
+            r.vidx = ri.vidx;
+            r.nsplit = ui.nsplit;
+            r.rec = ui.rec_base + itm.split * ui.rec_rows;
+            r.logit_off = verify ? p.logit_off[b] : 0;
+            sm.item[is] = r;
+        }
+        arrive_lane0(&sm.item_full[is]);
+        const int *list = p.sparse_idx + ((size_t)b * p.Hkv + g) * p.max_sparse + itm.begin;
+        const int *table = p.c.table + (size_t)b * p.c.max_blocks;
+        int bad = 0;
+        for (int k0 = 0; k0 < tiles * kTile; k0 += kChunkKeys) {
+            if (!wait4<kRegsRest>(&sm.rows_empty[slot], phase ^ 1, bd)) return;
+            int *rows = sm.row[slot];
+            if (verify) {  // (items begin at multiples of 64: a lane has the sixteen keys of a block)
+                const int k = k0 + lane * PILLAR_KV_BLOCK, pos = (itm.begin + k) / PILLAR_KV_BLOCK;
+                int row = -1;
+                if (k < n) {
+                    const int blk = pos < p.c.max_blocks ? __ldg(table + pos) : -1;
+                    if (blk >= 0 && blk < p.c.num_blocks) row = (blk * p.Hkv + g) * PILLAR_KV_BLOCK;
+                    else bad |= PILLAR_FLAG_SLOT;
+                }
+                const int m = row >= 0 ? n - k : 0;
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const uint32_t x = mul_f16x2(h[i], s);
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-            : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
-            : "r"(x));
+                for (int e = 0; e < PILLAR_KV_BLOCK; e += 4)
+                    *reinterpret_cast<int4 *>(rows + lane * PILLAR_KV_BLOCK + e) =
+                        make_int4(e < m ? row + e : -1, e + 1 < m ? row + e + 1 : -1, e + 2 < m ? row + e + 2 : -1,
+                                  e + 3 < m ? row + e + 3 : -1);
+            } else {
+                int pos[kChunkKeys / 32];
+#pragma unroll
+                for (int e = 0; e < kChunkKeys / 32; ++e) {
+                    const int k = k0 + e * 32 + lane;
+                    pos[e] = -1;
+                    if (k < n) {
+                        pos[e] = __ldg(list + k);
+                        if (pos[e] < 0 || pos[e] >= ri.len) bad |= PILLAR_FLAG_INDEX, pos[e] = -1;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kChunkKeys / 32; ++e) {
+                    int blk = 0;
+                    if (pos[e] >= 0) blk = pos[e] / PILLAR_KV_BLOCK < p.c.max_blocks ? __ldg(table + pos[e] / PILLAR_KV_BLOCK) : -1;
+                    if (blk < 0 || blk >= p.c.num_blocks) bad |= PILLAR_FLAG_SLOT, pos[e] = -1;
+                    rows[e * 32 + lane] = pos[e] >= 0 ? (blk * p.Hkv + g) * PILLAR_KV_BLOCK + pos[e] % PILLAR_KV_BLOCK : -1;
+                }
+            }
+            if (lane == 0) sm.chunk_tiles[slot] = min(kChunkTiles, tiles - k0 / kTile);
+            arrive_lane0(&sm.rows_full[slot]);
+            if (++slot == kChunks) slot = 0, phase ^= 1;
+        }
+        if (bad) atomicOr(bd.err, bad);
+    }
+}
+
+// ------------------------------------------------------------------ K and V warps
+
+// Warp w of K's (or V's) four: keys 32 w .. 32 w + 31 of every tile, from the copies to the operand.
+template <int D, bool kValue>
+__device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int w, int lane) {
+    using S = Smem4<D>;
+    constexpr int RC = S::kRow / 16;                            // 16-byte pieces of a row of codes
+    const uint8_t *codes = kValue ? p.c.v4 : p.c.k4, *scales = kValue ? p.c.v_scale : p.c.k_scale;
+    const int key = 32 * w + lane;
+    // piece c of row r lies at c ^ flip(r): eight lanes that read eight rows' pieces c meet no bank twice
+    auto flip = [](int r) { return RC == 4 ? (r >> 1) & 3 : (r >> 2) & 1; };
+    int slot = 0, at = 0, tiles = 0;  // the chunk that loads go through: its slot, tile and tiles (0: the next one has to come)
+    uint32_t phase = 0, issued = 0;
+    bool more = true, ok = true;
+    auto load = [&]() {
+        if (more && at == tiles) {
+            ok = wait4<kRegsConvert>(&sm.rows_full[slot], phase, bd);
+            tiles = ok ? sm.chunk_tiles[slot] : 0;
+            at = 0;
+            more = tiles > 0;
+        }
+        if (more) {
+            const int st = issued % kStages;
+            const int *rows = sm.row[slot] + at * kTile + 32 * w;
+            uint8_t *dst = sm.codes[kValue][st] + 32 * w * S::kRow;
+            const int c = lane % RC;
+#pragma unroll
+            for (int i = 0; i < RC; ++i) {
+                const int r = i * (32 / RC) + lane / RC, row = rows[r];
+                copy16(dst + r * S::kRow + ((c ^ flip(r)) << 4), codes + (size_t)max(row, 0) * S::kRow + c * 16, row >= 0 ? 16 : 0);
+            }
+            const int row = rows[lane];
+            copy_small<S::kScales>(sm.scales[kValue][st] + key * S::kScales, scales + (size_t)max(row, 0) * S::kScales,
+                                   row >= 0 ? S::kScales : 0);
+            ++issued;
+            if (++at == tiles) {
+                arrive_lane0(&sm.rows_empty[slot]);
+                if (++slot == kChunks) slot = 0, phase ^= 1;
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) load();
+#pragma unroll 1
+    for (uint32_t x = 0; ok; ++x) {
+        load();
+        if (x == issued) break;
+        copies_wait<kStages - 1>();
+        __syncwarp();
+        const int st = x % kStages, buf = x & 1;
+        const uint8_t *src = sm.codes[kValue][st] + key * S::kRow;
+        uint32_t sc[2];
+        if (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2 *>(sm.scales[kValue][st] + key * S::kScales);
+            sc[0] = y.x, sc[1] = y.y;
+        } else {
+            sc[0] = *reinterpret_cast<const uint32_t *>(sm.scales[kValue][st] + key * S::kScales);
+            sc[1] = 0;
+        }
+        // the operand's buffer is free: the scores (the outputs) of the tile before last are done
+        ok = wait4<kRegsConvert>(kValue ? &sm.pv_done[buf] : &sm.s_full[buf], (x >> 1 & 1) ^ 1, bd);
+        if (!ok) break;
+        tc_fence_after();
+        uint8_t *dst = sm.v[buf] + key * 128;
+#pragma unroll
+        for (int i = 0; i < RC; ++i) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(src + ((i ^ flip(key)) << 4));
+            const uint32_t word[4] = {y.x, y.y, y.z, y.w};
+            uint32_t h[4][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f16_of_e2m1(word[e], h[e]);
+                const uint32_t s = scale_pair(sc[i >> 1], (2 * i + (e >> 1)) & 3);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) h[e][d] = mul_f16x2(h[e][d], s);
+            }
+            if (kValue) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<uint4 *>(dst + (i >> 1) * (kTile * 128) + ((((i & 1) * 4 + e) ^ (key & 7)) << 4)) =
+                        make_uint4(h[e][0], h[e][1], h[e][2], h[e][3]);
+            } else {
+                tmem_st16(tm + ((uint32_t)w << 21) + kTmemK + buf * 64 + i * 16, &h[0][0]);
+            }
+        }
+        if (kValue) {
+            fence_proxy_async_smem();
+        } else {
+            tmem_wait_st();
+            tc_fence_before();
+        }
+        arrive_lane0(kValue ? &sm.v_full[buf] : &sm.k_full[buf]);
+    }
+    copies_wait<0>();
+}
+
+// ------------------------------------------------------------------ MMA warp
+
+// K-step descriptors of the 32-byte-swizzled P operand: rows (N) contiguous, 16 of them 32 bytes a key; groups of 16 rows
+// 4096 bytes apart, of 8 keys 256.
+__device__ __forceinline__ uint64_t p_desc(uint32_t saddr) { return umma_sdesc(saddr, kTile * 32, 256) | ((uint64_t)6 << 61); }
+
+template <int D>
+__device__ void mma4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm) {
+    constexpr uint32_t kId = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);  // f16 operands, fp32 sums, M = 128
+    uint32_t vs = 0, vp = 0;            // tiles whose scores, whose outputs have been issued
+    int si = 0, st = 0, sT = 0, sN = 0;  // scores: item, tile of it, its tiles (0: to come), its rows
+    int oi = 0, ot = 0, oT = 0, orows = 0;
+    bool stop = false, issued = false;
+    unsigned long long idle = 0;
+    for (uint32_t spin = 0;; ++spin) {
+        bool progress = false;
+        if (!stop && vs - vp < 2) {
+            if (sT == 0 && test4(&sm.item_full[si % kItems], si / kItems & 1)) {
+                const ItemRec &r = sm.item[si % kItems];
+                if (r.stop) stop = true;
+                else sT = r.tiles, sN = (r.rows + 15) / 16 * 16, st = 0;
+            }
+            const int b = vs & 1;
+            if (sT > 0 && test4(&sm.k_full[b], vs >> 1 & 1) && test4(&sm.s_empty[b], (vs >> 1 & 1) ^ 1) &&
+                (st > 0 || test4(&sm.q_full[si & 1], si >> 1 & 1))) {
+                tc_fence_after();
+                if (elect_one4()) {
+                    const uint64_t dq = umma_sdesc_sw128(smem_u32(sm.q[si & 1]), 16, 1024);
+                    const uint32_t id = kId | ((uint32_t)sN >> 3 << 17);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_bf16_ts(tm + kTmemS + b * 64, tm + kTmemK + b * 64 + ks * 8,
+                                     dq + (uint64_t)((ks >> 2) * (kMaxRows * 128 / 16) + (ks & 3) * 2), id, ks > 0 ? 1u : 0u);
+                    umma_commit(&sm.s_full[b]);
+                    if (st + 1 == sT) umma_commit(&sm.q_empty[si & 1]);
+                }
+                __syncwarp();
+                issued = progress = true;
+                ++vs;
+                if (++st == sT) sT = 0, ++si;
+            }
+        }
+        if (vp < vs) {
+            if (oT == 0) {  // (its scores have been issued: the record is there)
+                const ItemRec &r = sm.item[oi % kItems];
+                oT = r.tiles, orows = r.rows, ot = 0;
+            }
+            const int b = vp & 1;
+            if (test4(&sm.p_full[b], vp >> 1 & 1) && test4(&sm.v_full[b], vp >> 1 & 1) &&
+                (ot > 0 || test4(&sm.o_empty[oi & 1], (oi >> 1 & 1) ^ 1))) {
+                tc_fence_after();
+                const bool turns = takes_turns(orows), add = ot >= (turns ? 2 : 1);
+                if (elect_one4()) {
+                    // V: M (dimensions) in halves of 64; for D = 64 the second half is whatever follows, and nobody reads its O
+                    const uint64_t dv = umma_sdesc_sw128(smem_u32(sm.v[b]), kTile * 128, 1024), dp = p_desc(smem_u32(sm.p[b]));
+                    const uint32_t id = kId | (1u << 15) | (1u << 16) | ((uint32_t)((orows + 15) / 16 * 16) >> 3 << 17);
+                    const uint32_t to = tm + kTmemO + (oi & 1) * 64 + (turns ? b * 16 : 0);
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        umma_bf16(to, dv + (uint64_t)(ks * 128), dp + (uint64_t)(ks * 32), id, add || ks > 0 ? 1u : 0u);
+                    umma_commit(&sm.pv_done[b]);
+                    if (ot + 1 == oT) umma_commit(&sm.o_full[oi & 1]);
+                }
+                __syncwarp();
+                progress = true;
+                ++vp;
+                if (++ot == oT) {
+                    oT = 0;
+                    arrive_lane0(&sm.item_empty[oi % kItems]);
+                    ++oi;
+                }
+            }
+        }
+        if (stop && vp == vs) break;
+        if (progress) {
+            idle = 0;
+            continue;
+        }
+        if ((spin & 63) == 0) {
+            const unsigned long long now = global_timer_ns();
+            if (idle == 0) idle = now;
+            const bool over = now - idle > bd.ns;
+            if (__any_sync(0xffffffffu, over || *bd.abort)) {
+                if (over) atomicOr(bd.err, PILLAR_FLAG_TIMEOUT);
+                *bd.abort = 1;
+                break;
+            }
+        }
+    }
+    if (issued && elect_one4()) {  // every product has completed before the tensor memory is freed
+        umma_commit(&sm.drain);
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait(&sm.drain, 0))
+            if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax warps
+
+// True when it is for any thread of the group (which all reach it).
+__device__ __forceinline__ bool group_any(int grp, bool x) {
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y)
+                 : "r"(grp + 1), "r"((uint32_t)x)
+                 : "memory");
+    return y != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {  // (a NaN is passed over)
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D>
+__device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int grp, int w, int lane) {
+    const int key = 32 * w + lane;
+    const uint32_t quad = tm + ((uint32_t)w << 21);
+    uint32_t x = 0;  // tile
+    int slot = 0;    // of the chunk
+    uint32_t phase = 0;
+    bool dead = false;  // a wait has given up: the group leaves together, at its next vote
+    for (int i = 0;; ++i) {
+        const int is = i % kItems, sl = i & 1;
+        dead |= !wait4<kRegsSoftmax>(&sm.item_full[is], i / kItems & 1, bd);
+        if (group_any(grp, dead)) return;
+        const ItemRec &rec = sm.item[is];
+        if (rec.stop) return;
+        const int tiles = rec.tiles, rows = rec.rows, n = rec.n, begin = rec.begin;
+        const bool verify = rec.verify, turns = takes_turns(rows), dump = verify && p.logits;
+        const int sure = verify ? rec.L - (p.k + 1) : 0x7fffffff;  // every row sees up to here
+        const int c0 = !turns && grp ? 8 * first_chunks(rows) : 0;
+        const int mine = !turns && !grp ? min(rows, 8 * first_chunks(rows)) : rows - c0, nch = (mine + 7) / 8;
+        dead |= !wait4<kRegsSoftmax>(&sm.fac_full[is], i / kItems & 1, bd);
+        dead |= !wait4<kRegsSoftmax>(&sm.epi_empty[sl], (i >> 1 & 1) ^ 1, bd);
+        // Where both groups use both buffers, the other one is done with the item before: its tiles' phases are over, and a
+        // wait for the next phase of a buffer that this group has not watched is one for the right one.
+        if (!turns && i > 0) dead |= !wait4<kRegsSoftmax>(&sm.epi_full[sl ^ 1], (i - 1) >> 1 & 1, bd);
+        const float *fac2 = sm.fac2[is] + c0;
+        float *nref = sm.nref[sl][grp];
+        if (w == 0) nref[lane] = kLift;
+        float l[4][8], m = neg_inf();  // m: the reference maximum of row `lane` of the group, in every warp
+        bool fresh = true, first = true;  // some row has none yet; nothing has been added to O
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l[ch][e] = 0.f;
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t, ++x) {
+            if (t % kChunkTiles == 0) dead |= !wait4<kRegsSoftmax>(&sm.rows_full[slot], phase, bd);
+            const bool there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
+            if (t % kChunkTiles == kChunkTiles - 1 || t == tiles - 1) {
+                arrive_lane0(&sm.rows_empty[slot]);
+                if (++slot == kChunks) slot = 0, phase ^= 1;
+            }
+            const int b = x & 1;
+            if (turns && b != grp) continue;
+            const uint32_t ph = x >> 1 & 1;
+            dead |= !wait4<kRegsSoftmax>(&sm.s_full[b], ph, bd);
+            tc_fence_after();
+            float s[4][8];
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                if (ch < nch) tmem_ld8(quad + kTmemS + b * 64 + c0 + ch * 8, s[ch]);
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive_lane0(&sm.s_empty[b], turns ? 2 : 1);
+            const int pos = begin + t * kTile + key;
+            if (!there || (verify && pos > sure)) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (ch < nch)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!there || pos > sm.lim[is][c0 + ch * 8 + e]) s[ch][e] = neg_inf();
+            }
+            float most = neg_inf();
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                if (ch < nch)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaf(s[ch][e], fac2[ch * 8 + e], nref[ch * 8 + e]));
+            if (group_any(grp, most > kGrow || fresh || dead)) {  // rare: new reference maxima
+                if (group_any(grp, dead)) return;
+                float mx = neg_inf();
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (ch < nch)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float y = warp_max(s[ch][e] * fac2[ch * 8 + e]);
+                            if (lane == ch * 8 + e) mx = y;
+                        }
+                sm.top[grp][w][lane] = mx;
+                if (!first) {  // what has been added to O so far is done: its rows are scaled below
+                    const uint32_t y = turns ? x - 2 : x - 1;
+                    dead |= !wait4<kRegsSoftmax>(&sm.pv_done[y & 1], y >> 1 & 1, bd);
+                    tc_fence_after();
+                }
+                group_any(grp, false);
+                mx = fmaxf(fmaxf(sm.top[grp][0][lane], sm.top[grp][1][lane]), fmaxf(sm.top[grp][2][lane], sm.top[grp][3][lane]));
+                // (a row's reference goes by its own scores alone: one whose scores stayed within the bound keeps its)
+                const float to_m = m == neg_inf() || mx > m + (kGrow - kLift) ? fmaxf(mx, m) : m;
+                const float f = m == neg_inf() || to_m == m ? 1.f : ex2_approx(m - to_m);
+                m = to_m;
+                if (w == 0) nref[lane] = kLift - (m == neg_inf() ? 0.f : m);
+                fresh = __any_sync(0xffffffffu, lane < mine && m == neg_inf());
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (ch < nch) {
+                        float o[8];
+                        const uint32_t to = quad + kTmemO + sl * 64 + (turns ? grp * 16 : c0) + ch * 8;
+                        if (!first) {
+                            tmem_ld8(to, o);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float fe = __shfl_sync(0xffffffffu, f, ch * 8 + e);
+                            l[ch][e] *= fe;
+                            o[e] *= fe;
+                        }
+                        if (!first) tmem_st8(to, o);
+                    }
+                if (!first) tmem_wait_st();
+                group_any(grp, false);
+            }
+            first = false;
+            dead |= !wait4<kRegsSoftmax>(&sm.pv_done[b], ph ^ 1, bd);  // the P of the tile before last has been read
+            uint8_t *dst = sm.p[b] + key * 32;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                if (ch < nch) {
+                    float e8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        e8[e] = ex2_approx(fmaf(s[ch][e], fac2[ch * 8 + e], nref[ch * 8 + e]));
+                        l[ch][e] += e8[e];
+                    }
+                    const int cc = c0 / 8 + ch;
+                    *reinterpret_cast<uint4 *>(dst + (cc >> 1) * (kTile * 32) + (((cc & 1) ^ ((key >> 2) & 1)) << 4)) =
+                        make_uint4(pack_f16x2(e8[0], e8[1]), pack_f16x2(e8[2], e8[3]), pack_f16x2(e8[4], e8[5]),
+                                   pack_f16x2(e8[6], e8[7]));
+                }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            arrive_lane0(&sm.p_full[b], turns ? 2 : 1);
+            if (dump && t * kTile + key < n) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (ch < nch)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const long long lb = sm.lb[is][c0 + ch * 8 + e];
+                            if (lb >= 0) p.logits[lb + pos] = s[ch][e] * sm.fac[is][c0 + ch * 8 + e];
+                        }
+            }
+        }
+        // the sums of weights over the warp's keys: of eight rows at a time, each lane ends up with one
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+            if (ch < nch) {
+                float a[4], c[2], z;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float keep = lane & 16 ? l[ch][4 + e] : l[ch][e], give = lane & 16 ? l[ch][e] : l[ch][4 + e];
+                    a[e] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float keep = lane & 8 ? a[2 + e] : a[e], give = lane & 8 ? a[e] : a[2 + e];
+                    c[e] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+                }
+                {
+                    const float keep = lane & 4 ? c[1] : c[0], give = lane & 4 ? c[0] : c[1];
+                    z = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+                }
+                z += __shfl_xor_sync(0xffffffffu, z, 2);
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                if ((lane & 3) == 0) sm.sum[sl][grp][w][ch * 8 + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = z;
+            }
+        arrive_lane0(&sm.epi_full[sl]);
+        arrive_lane0(&sm.item_empty[is]);
+    }
+}
+
+// ------------------------------------------------------------------ query warps
+
+// The f16 query operands of an item (two warps, eight rows at a time each) and what the softmax warps know about its rows.
+template <int D>
+__device__ void queries4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, int w, int lane) {
+    constexpr int W = D / 64;  // words of a lane
+    for (int i = 0;; ++i) {
+        const int is = i % kItems;
+        if (!wait4<kRegsRest>(&sm.item_full[is], i / kItems & 1, bd)) return;
+        const ItemRec rec = sm.item[is];
+        if (rec.stop) return;
+        if (!wait4<kRegsRest>(&sm.q_empty[i & 1], (i >> 1 & 1) ^ 1, bd)) return;
+        for (int r0 = 8 * w; r0 < rec.rows; r0 += 16) {
+            uint32_t x[8][W];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = r0 + e, j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
+#pragma unroll
+                for (int a = 0; a < W; ++a) x[e][a] = 0;
+                if (r < rec.rows) {
+                    const uint16_t *src = p.q + ((size_t)(rec.q_off + j) * p.Hq + (size_t)rec.g * p.G + gi) * D + lane * 2 * W;
+                    if (W == 2) {
+                        const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src));
+                        x[e][0] = y.x, x[e][W - 1] = y.y;
+                    } else {
+                        x[e][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = r0 + e;
+                uint32_t mx = x[e][0] & 0x7fff7fffu;
+                if (W == 2) mx = __vmaxu2(mx, x[e][W - 1] & 0x7fff7fffu);
+                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+                const int ex = max((int)(mx >> 7), 15);            // biased exponent, such that 2^(141 - ex) is finite
+                const float up = __int_as_float((268 - ex) << 23); // 2^(141 - ex): the largest comes to [2^14, 2^15)
+                const float down = __int_as_float((ex - 14) << 23);
+                uint8_t *dst = sm.q[i & 1] + (lane * W / 32) * (kMaxRows * 128) + r * 128 +
+                               (((lane * W % 32 / 4) ^ (r & 7)) << 4) + lane * W % 4 * 4;
+                if (W == 2)
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up),
+                                                                 pack_f16x2(bf16lo(x[e][W - 1]) * up, bf16hi(x[e][W - 1]) * up));
+                else
+                    *reinterpret_cast<uint32_t *>(dst) = pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up);
+                if (lane == e) {
+                    const int j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
+                    const float fac = fmaxf(down * p.scale, __int_as_float(1));  // (above 0: a masked score stays -inf)
+                    sm.fac[is][r] = fac;
+                    sm.fac2[is][r] = fmaxf(fac * kLog2e, __int_as_float(1));
+                    sm.lim[is][r] = rec.verify && r < rec.rows ? rec.L - (p.k + 1) + j : 0x7fffffff;
+                    sm.lb[is][r] = r < rec.rows && rec.verify && p.logits
+                                       ? rec.logit_off + ((long long)(rec.g * p.G + gi) * (p.k + 1) + j) * rec.L : -1;
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        arrive_lane0(&sm.q_full[i & 1]);
+        arrive_lane0(&sm.fac_full[is]);
+        arrive_lane0(&sm.item_empty[is]);
+    }
+}
+
+// ------------------------------------------------------------------ epilogue warps
+
+template <int D>
+__device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int w, int lane) {
+    const int d = 32 * w + lane;
+    for (int i = 0;; ++i) {
+        const int is = i % kItems, sl = i & 1;
+        if (!wait4<kRegsRest>(&sm.item_full[is], i / kItems & 1, bd)) return;
+        const ItemRec rec = sm.item[is];
+        if (rec.stop) return;
+        if (!wait4<kRegsRest>(&sm.epi_full[sl], i >> 1 & 1, bd) || !wait4<kRegsRest>(&sm.o_full[sl], i >> 1 & 1, bd)) return;
+        tc_fence_after();
+        const bool turns = takes_turns(rec.rows);
+        const int split = 8 * first_chunks(rec.rows);
+        // rows lane and lane + 32: what the (two) accumulators are multiplied by
+        float f0[2] = {0.f, 0.f}, f1[2] = {0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = lane + 32 * h;
+            if (r >= rec.rows) continue;
+            const int grp = !turns && r >= split, c = r - (grp ? split : 0);
+            const float *s0 = &sm.sum[sl][grp][0][c];
+            float l = s0[0] + s0[32] + s0[64] + s0[96], ref = -sm.nref[sl][grp][c];
+            f0[h] = 1.f;
+            if (turns) {
+                const float *s1 = &sm.sum[sl][1][0][c];
+                const float l1 = s1[0] + s1[32] + s1[64] + s1[96], ref1 = -sm.nref[sl][1][c];
+                // (a sum of 0 has no reference)
+                const float top = l == 0.f ? ref1 : l1 == 0.f ? ref : fmaxf(ref, ref1);
+                f0[h] = l == 0.f ? 0.f : ex2_approx(ref - top);
+                f1[h] = l1 == 0.f ? 0.f : ex2_approx(ref1 - top);
+                l = __fadd_rn(__fmul_rn(l, f0[h]), __fmul_rn(l1, f1[h]));  // (the same whichever group began)
+                ref = top;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // (what is 0 stays it under a NaN sum: an accumulator that nobody wrote is not read)
+            if (f0[h] != 0.f) f0[h] *= inv;
+            if (f1[h] != 0.f) f1[h] *= inv;
+            if (w == 0) {
+                const float z = l > 0.f ? ref * 0.69314718f + logf(l) : (l == 0.f ? neg_inf() : l);  // (a NaN sum stays one)
+                const int j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
+                if (rec.nsplit > 1) p.part_lse[(size_t)rec.rec + r] = z;
+                else if (rec.verify) p.lse[((size_t)rec.vidx * p.Hq + (size_t)rec.g * p.G + gi) * (p.k + 1) + j] = z;
+            }
+        }
+        // (in turns, an item of one tile has one accumulator: a group that met no tile has sums of 0)
+        const bool any0 = !turns || __any_sync(0xffffffffu, f0[0] != 0.f), any1 = turns && __any_sync(0xffffffffu, f1[0] != 0.f);
+        int j = 0, gi = 0;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rec.rows; r0 += 8) {
+            float o[8], o1[8];
+            tmem_ld8(tm + ((uint32_t)w << 21) + kTmemO + sl * 64 + r0, o);
+            if (any1) tmem_ld8(tm + ((uint32_t)w << 21) + kTmemO + sl * 64 + 16 + r0, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = r0 + e;
+                const float a0 = __shfl_sync(0xffffffffu, r0 < 32 ? f0[0] : f0[1], r & 31);
+                const float a1 = __shfl_sync(0xffffffffu, f1[0], r & 31);
+                const float y = __fadd_rn(any0 ? __fmul_rn(o[e], a0) : 0.f, any1 ? __fmul_rn(o1[e], a1) : 0.f);
+                if (r < rec.rows && d < D) {
+                    if (rec.nsplit > 1) p.part_o[((size_t)rec.rec + r) * D + d] = y;
+                    else
+                        p.out[((size_t)(rec.q_off + j) * p.Hq + (size_t)rec.g * p.G + gi) * D + d] =
+                            (uint16_t)pack_bf16x2(y, 0.f);
+                }
+                if (++gi == p.G && rec.verify) gi = 0, ++j;
+            }
+        }
+        tc_fence_before();
+        arrive_lane0(&sm.o_empty[sl]);
+        arrive_lane0(&sm.epi_empty[sl]);
+        arrive_lane0(&sm.item_empty[is]);
+    }
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads4, 1) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
+    extern __shared__ __align__(1024) char smem[];
+    Smem4<D> &sm = *reinterpret_cast<Smem4<D> *>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp & 3;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], 8 + 4 + 2 + 1);  // softmax, epilogue and query warps, the products' warp
+            mbar_init(&sm.fac_full[i], 2);
+        }
+        for (int i = 0; i < kChunks; ++i) {
+            mbar_init(&sm.rows_full[i], 1);
+            mbar_init(&sm.rows_empty[i], 16);  // K, V and softmax warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 2);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.k_full[i], 4);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_empty[i], 8);
+            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.o_empty[i], 4);
+            mbar_init(&sm.epi_full[i], 8);
+            mbar_init(&sm.epi_empty[i], 4);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;
+    pdl_wait_prerequisites();  // the plan's output is read only from here on
+    pdl_launch_dependents();   // (the merge waits for this kernel's completion itself)
+    const Bounds4 bd{&sm.abort, &p.hdr->err, p.wait_ns};
+    // the registers go to the softmax warps: 80 a thread at launch
+    switch (warp >> 2) {
+        case 0:
+        case 1:
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+            softmax4<D>(p, sm, bd, tm, warp >> 2, w, lane);
+            break;
+        case 2:
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+            convert4<D, false>(p, sm, bd, tm, w, lane);
+            break;
+        case 3:
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+            convert4<D, true>(p, sm, bd, tm, w, lane);
+            break;
+        case 4:
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+            if (w == 0) resolver4<D>(p, sm, bd, lane);
+            else if (w == 1) mma4<D>(p, sm, bd, tm);
+            else queries4<D>(p, sm, bd, w - 2, lane);
+            break;
+        default:
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+            epilogue4<D>(p, sm, bd, tm, w, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tm, kTmemCols);
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads4) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
-    constexpr int N = D / 32;
-    __shared__ int s_item;
-    pdl_wait_prerequisites();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int num_items = *reinterpret_cast<volatile int *>(&p.hdr->num_items);
-    int bad = 0;
-    for (;;) {
-        __syncthreads();
-        if (threadIdx.x == 0) s_item = atomicAdd(&p.hdr->item_counter, 1);
-        __syncthreads();
-        if (s_item >= num_items) break;
-        const Item it = p.items[s_item];
-        const int b = it.unit / p.Hkv, g = it.unit - b * p.Hkv;
-        const ReqInfo req = p.req[b];
-        const UnitInfo unit = p.unit[it.unit];
-        const bool verify = req.mode == 1;
-        const int rows = verify ? p.M : p.G, rec = unit.rec_base + it.split * unit.rec_rows;
-        for (int r = warp; r < rows; r += kThreads4 / 32) {
-            const int j = verify ? r / p.G : 0, gi = r - j * p.G;
-            const size_t orow = (size_t)(req.q_off + j) * p.Hq + (size_t)g * p.G + gi;
-            const long long lb = verify && p.logits
-                                     ? p.logit_off[b] + ((long long)(g * p.G + gi) * (p.k + 1) + j) * req.len : -1;
-            const int lim = verify ? req.len - (p.k + 1) + j : 0x7fffffff;
-            float q[N], o[N] = {}, m = neg_inf(), l = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) q[i] = bf16lo(p.q[orow * D + lane * N + i]);
-            for (int t = it.begin; t < it.end; ++t) {
-                int pos = t;
-                if (!verify) pos = p.sparse_idx[((size_t)b * p.Hkv + g) * p.max_sparse + t];
-                float s = neg_inf();
-                size_t row = 0;
-                if (pos < 0 || pos >= req.len) {
-                    bad |= PILLAR_FLAG_INDEX;
-                } else {
-                    const int blk = pos / PILLAR_KV_BLOCK < p.c.max_blocks
-                                        ? p.c.table[(size_t)b * p.c.max_blocks + pos / PILLAR_KV_BLOCK] : -1;
-                    if (blk < 0 || blk >= p.c.num_blocks) {
-                        bad |= PILLAR_FLAG_SLOT;
-                    } else if (pos <= lim) {
-                        row = ((size_t)blk * p.Hkv + g) * PILLAR_KV_BLOCK + pos % PILLAR_KV_BLOCK;
-                        float k[N];
-                        row_values<N>(p.c.k4, p.c.k_scale, row, lane, k);
-                        s = 0.f;
-#pragma unroll
-                        for (int i = 0; i < N; ++i) s += q[i] * k[i];
-#pragma unroll
-                        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                        s *= p.scale;
-                    }
-                }
-                if (lb >= 0 && lane == 0) p.logits[lb + pos] = s;
-                if (s == neg_inf()) continue;
-                const float mn = fmaxf(m, s), f = m == neg_inf() ? 0.f : expf(m - mn), e = expf(s - mn);
-                float v[N];
-                row_values<N>(p.c.v4, p.c.v_scale, row, lane, v);
-                l = l * f + e;
-#pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = o[i] * f + e * v[i];
-                m = mn;
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l, z = l > 0.f ? m + logf(l) : (l == 0.f ? neg_inf() : l);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (unit.nsplit > 1) p.part_o[((size_t)rec + r) * D + lane * N + i] = o[i] * inv;
-                else p.out[orow * D + lane * N + i] = (uint16_t)pack_bf16x2(o[i] * inv, 0.f);
-            }
-            if (lane == 0) {
-                if (unit.nsplit > 1) p.part_lse[(size_t)rec + r] = z;
-                else if (verify) p.lse[((size_t)req.vidx * p.Hq + (size_t)g * p.G + gi) * (p.k + 1) + j] = z;
-            }
-        }
+cudaError_t launch_t(const Kv4Params &p, int nsm, cudaStream_t st) {
+    constexpr int kSmem = (int)sizeof(Smem4<D>);
+    static unsigned long long configured[kMaxDevices] = {};
+    int dev = 0;
+    unsigned long long ctx = 0;
+    cudaError_t e = current_device_context(&dev, &ctx);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (ctx == 0 || __atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE) != ctx) {
+        e = cudaFuncSetAttribute(attn_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kv4_kernel<D>, kThreads4, kSmem);
+        if (e != cudaSuccess) return e;
+        if (n != 1) return cudaErrorInvalidConfiguration;  // a CTA takes all of its SM's tensor memory
+        e = current_device_context(&dev, &ctx);  // (the calls above made a context current)
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&configured[dev], ctx, __ATOMIC_RELEASE);
     }
-    if (bad) atomicOr(&p.hdr->err, bad);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nsm);
+    cfg.blockDim = dim3(kThreads4);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D>, p);
 }
 
 }  // namespace
@@ -149,16 +925,8 @@ cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaS
     p.M = (a.k + 1) * p.G;
     p.max_sparse = a.max_sparse;
     p.scale = a.scale;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4 * nsm);
-    cfg.blockDim = dim3(kThreads4);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = a.D == 128 ? cudaLaunchKernelEx(&cfg, attn_kv4_kernel<128>, p) : cudaLaunchKernelEx(&cfg, attn_kv4_kernel<64>, p);
+    p.wait_ns = a.wait_ns;
+    const cudaError_t e = a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
     return e == cudaSuccess ? launch_merge(a, nsm, st) : e;
 }
 
