@@ -44,8 +44,8 @@ constexpr int kWarps = 24;
 constexpr int kThreads4 = kWarps * 32;
 constexpr float kLift = 6.f;                 // log2 of the weight of a probability at its row's reference maximum
 constexpr float kGrow = 8.f + kLift;         // the reference moves once a weight passes 2^kGrow
-// tensor memory: two tiles of K, two of S^T, the O^T of two items
-constexpr uint32_t kTmemCols = 512, kTmemK = 0, kTmemS = 128, kTmemO = 256;
+// tensor memory: two tiles of K, two of S^T, the O^T of two items, sums of weights (a key's lane, a column per row)
+constexpr uint32_t kTmemCols = 512, kTmemK = 0, kTmemS = 128, kTmemO = 256, kTmemL = 384;
 
 struct Kv4Params {
     const uint16_t *q;
@@ -85,10 +85,10 @@ struct Smem4 {
     alignas(16) int row[kChunks][kChunkKeys];   // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
     int chunk_tiles[kChunks];                   // 0: no more
     ItemRec item[kItems];
-    // per query row: logit = sum * fac, in base-2 units sum * fac2; last position seen; its logits (offset of position 0, or -1)
+    // per query row: logit = sum * fac, in base-2 units sum * fac2; last position seen; its logits, or null
     alignas(16) float fac[kItems][kMaxRows], fac2[kItems][kMaxRows];
     int lim[kItems][kMaxRows];
-    long long lb[kItems][kMaxRows];
+    float *lb[kItems][kMaxRows];
     // per item (in turn), group and row of the group: kLift - reference maximum (base 2); sums of weights per warp
     alignas(16) float nref[2][2][32], sum[2][2][4][32];
     float top[2][4][32];                        // a group's largest scores, per warp
@@ -132,12 +132,12 @@ __device__ __forceinline__ bool test4(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
 }
 
-__device__ __forceinline__ void copy16(void *dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 template <int N>
-__device__ __forceinline__ void copy_small(void *dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "n"(N) : "memory");
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -271,7 +271,8 @@ __device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, i
 
 // ------------------------------------------------------------------ K and V warps
 
-// Warp w of K's (or V's) four: keys 32 w .. 32 w + 31 of every tile, from the copies to the operand.
+// Warp w of K's (or V's) four: keys 32 w .. 32 w + 31 of every tile, from the copies to the operand.  (Code is kept small here
+// and below, rolled where it can be: the roles run at once and share the instruction cache.)
 template <int D, bool kValue>
 __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int w, int lane) {
     using S = Smem4<D>;
@@ -281,9 +282,12 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
     // piece c of row r lies at c ^ flip(r): eight lanes that read eight rows' pieces c meet no bank twice
     auto flip = [](int r) { return RC == 4 ? (r >> 1) & 3 : (r >> 2) & 1; };
     int slot = 0, at = 0, tiles = 0;  // the chunk that loads go through: its slot, tile and tiles (0: the next one has to come)
-    uint32_t phase = 0, issued = 0;
+    uint32_t phase = 0;
+    int issued = 0;
     bool more = true, ok = true;
-    auto load = [&]() {
+#pragma unroll 1
+    for (int x = 1 - kStages; ok; ++x) {
+        // the loads of tile x + kStages - 1
         if (more && at == tiles) {
             ok = wait4<kRegsConvert>(&sm.rows_full[slot], phase, bd);
             tiles = ok ? sm.chunk_tiles[slot] : 0;
@@ -293,7 +297,7 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
         if (more) {
             const int st = issued % kStages;
             const int *rows = sm.row[slot] + at * kTile + 32 * w;
-            uint8_t *dst = sm.codes[kValue][st] + 32 * w * S::kRow;
+            const uint32_t dst = smem_u32(sm.codes[kValue][st] + 32 * w * S::kRow);
             const int c = lane % RC;
 #pragma unroll
             for (int i = 0; i < RC; ++i) {
@@ -301,7 +305,7 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
                 copy16(dst + r * S::kRow + ((c ^ flip(r)) << 4), codes + (size_t)max(row, 0) * S::kRow + c * 16, row >= 0 ? 16 : 0);
             }
             const int row = rows[lane];
-            copy_small<S::kScales>(sm.scales[kValue][st] + key * S::kScales, scales + (size_t)max(row, 0) * S::kScales,
+            copy_small<S::kScales>(smem_u32(sm.scales[kValue][st] + key * S::kScales), scales + (size_t)max(row, 0) * S::kScales,
                                    row >= 0 ? S::kScales : 0);
             ++issued;
             if (++at == tiles) {
@@ -310,46 +314,36 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
             }
         }
         copies_commit();
-    };
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) load();
-#pragma unroll 1
-    for (uint32_t x = 0; ok; ++x) {
-        load();
+        if (x < 0) continue;
         if (x == issued) break;
         copies_wait<kStages - 1>();
         __syncwarp();
         const int st = x % kStages, buf = x & 1;
-        const uint8_t *src = sm.codes[kValue][st] + key * S::kRow;
-        uint32_t sc[2];
-        if (D == 128) {
-            const uint2 y = *reinterpret_cast<const uint2 *>(sm.scales[kValue][st] + key * S::kScales);
-            sc[0] = y.x, sc[1] = y.y;
-        } else {
-            sc[0] = *reinterpret_cast<const uint32_t *>(sm.scales[kValue][st] + key * S::kScales);
-            sc[1] = 0;
-        }
         // the operand's buffer is free: the scores (the outputs) of the tile before last are done
         ok = wait4<kRegsConvert>(kValue ? &sm.pv_done[buf] : &sm.s_full[buf], (x >> 1 & 1) ^ 1, bd);
         if (!ok) break;
         tc_fence_after();
+        const uint8_t *src = sm.codes[kValue][st] + key * S::kRow;
+        const uint8_t *sc = sm.scales[kValue][st] + key * S::kScales;
         uint8_t *dst = sm.v[buf] + key * 128;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < RC; ++i) {
             const uint4 y = *reinterpret_cast<const uint4 *>(src + ((i ^ flip(key)) << 4));
+            const uint32_t two = *reinterpret_cast<const uint16_t *>(sc + 2 * i);
+            const uint32_t s0 = scale_pair(two, 0), s1 = scale_pair(two, 1);
             const uint32_t word[4] = {y.x, y.y, y.z, y.w};
             uint32_t h[4][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 f16_of_e2m1(word[e], h[e]);
-                const uint32_t s = scale_pair(sc[i >> 1], (2 * i + (e >> 1)) & 3);
 #pragma unroll
-                for (int d = 0; d < 4; ++d) h[e][d] = mul_f16x2(h[e][d], s);
+                for (int d = 0; d < 4; ++d) h[e][d] = mul_f16x2(h[e][d], e < 2 ? s0 : s1);
             }
             if (kValue) {
+                uint8_t *half = dst + (i >> 1) * (kTile * 128);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<uint4 *>(dst + (i >> 1) * (kTile * 128) + ((((i & 1) * 4 + e) ^ (key & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(half + ((((i & 1) * 4 + e) ^ (key & 7)) << 4)) =
                         make_uint4(h[e][0], h[e][1], h[e][2], h[e][3]);
             } else {
                 tmem_st16(tm + ((uint32_t)w << 21) + kTmemK + buf * 64 + i * 16, &h[0][0]);
@@ -481,6 +475,26 @@ __device__ __forceinline__ float warp_max(float x) {  // (a NaN is passed over)
     return y;
 }
 
+// Eight rows' scores of a thread's key, with those that do not count at -inf.
+struct Key4 {
+    bool there, part;  // there is such a key; some row does not see it
+    int pos;
+    const int *lim;
+};
+__device__ __forceinline__ void scores8(uint32_t taddr, const Key4 &k, int ch, float (&s)[8]) {
+    tmem_ld8(taddr + ch * 8, s);
+    tmem_wait_ld();
+    if (k.part) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (!k.there || k.pos > k.lim[ch * 8 + e]) s[e] = neg_inf();
+    }
+}
+__device__ __forceinline__ void load8(const float *src, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
 template <int D>
 __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int grp, int w, int lane) {
     const int key = 32 * w + lane;
@@ -489,13 +503,14 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
     int slot = 0;    // of the chunk
     uint32_t phase = 0;
     bool dead = false;  // a wait has given up: the group leaves together, at its next vote
+#pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems, sl = i & 1;
         dead |= !wait4<kRegsSoftmax>(&sm.item_full[is], i / kItems & 1, bd);
         if (group_any(grp, dead)) return;
         const ItemRec &rec = sm.item[is];
         if (rec.stop) return;
-        const int tiles = rec.tiles, rows = rec.rows, n = rec.n, begin = rec.begin;
+        const int tiles = rec.tiles, rows = rec.rows, n = rec.n;
         const bool verify = rec.verify, turns = takes_turns(rows), dump = verify && p.logits;
         const int sure = verify ? rec.L - (p.k + 1) : 0x7fffffff;  // every row sees up to here
         const int c0 = !turns && grp ? 8 * first_chunks(rows) : 0;
@@ -508,58 +523,50 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
         const float *fac2 = sm.fac2[is] + c0;
         float *nref = sm.nref[sl][grp];
         if (w == 0) nref[lane] = kLift;
-        float l[4][8], m = neg_inf();  // m: the reference maximum of row `lane` of the group, in every warp
+        const uint32_t tl = quad + kTmemL + grp * 32, to = quad + kTmemO + sl * 64 + (turns ? grp * 16 : c0);
+        float m = neg_inf();  // the reference maximum of row `lane` of the group, in every warp
         bool fresh = true, first = true;  // some row has none yet; nothing has been added to O
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) l[ch][e] = 0.f;
+        Key4 kk;
+        kk.pos = rec.begin + key;
+        kk.lim = sm.lim[is] + c0;
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t, ++x) {
+        for (int t = 0; t < tiles; ++t, ++x, kk.pos += kTile) {
             if (t % kChunkTiles == 0) dead |= !wait4<kRegsSoftmax>(&sm.rows_full[slot], phase, bd);
-            const bool there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
+            kk.there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
             if (t % kChunkTiles == kChunkTiles - 1 || t == tiles - 1) {
                 arrive_lane0(&sm.rows_empty[slot]);
                 if (++slot == kChunks) slot = 0, phase ^= 1;
             }
             const int b = x & 1;
             if (turns && b != grp) continue;
-            const uint32_t ph = x >> 1 & 1;
+            const uint32_t ph = x >> 1 & 1, ts = quad + kTmemS + b * 64 + c0;
+            kk.part = !kk.there || (verify && kk.pos > sure);
             dead |= !wait4<kRegsSoftmax>(&sm.s_full[b], ph, bd);
             tc_fence_after();
-            float s[4][8];
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                if (ch < nch) tmem_ld8(quad + kTmemS + b * 64 + c0 + ch * 8, s[ch]);
-            tmem_wait_ld();
-            tc_fence_before();
-            arrive_lane0(&sm.s_empty[b], turns ? 2 : 1);
-            const int pos = begin + t * kTile + key;
-            if (!there || (verify && pos > sure)) {
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    if (ch < nch)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (!there || pos > sm.lim[is][c0 + ch * 8 + e]) s[ch][e] = neg_inf();
-            }
             float most = neg_inf();
+#pragma unroll 1
+            for (int ch = 0; ch < nch; ++ch) {
+                float s[8], f[8], r[8];
+                load8(fac2 + ch * 8, f);
+                load8(nref + ch * 8, r);
+                scores8(ts, kk, ch, s);
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                if (ch < nch)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaf(s[ch][e], fac2[ch * 8 + e], nref[ch * 8 + e]));
+                for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaf(s[e], f[e], r[e]));
+            }
             if (group_any(grp, most > kGrow || fresh || dead)) {  // rare: new reference maxima
                 if (group_any(grp, dead)) return;
                 float mx = neg_inf();
+#pragma unroll 1
+                for (int ch = 0; ch < nch; ++ch) {
+                    float s[8], f[8];
+                    load8(fac2 + ch * 8, f);
+                    scores8(ts, kk, ch, s);
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    if (ch < nch)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float y = warp_max(s[ch][e] * fac2[ch * 8 + e]);
-                            if (lane == ch * 8 + e) mx = y;
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = warp_max(s[e] * f[e]);
+                        if (lane == ch * 8 + e) mx = y;
+                    }
+                }
                 sm.top[grp][w][lane] = mx;
                 if (!first) {  // what has been added to O so far is done: its rows are scaled below
                     const uint32_t y = turns ? x - 2 : x - 1;
@@ -574,80 +581,84 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
                 m = to_m;
                 if (w == 0) nref[lane] = kLift - (m == neg_inf() ? 0.f : m);
                 fresh = __any_sync(0xffffffffu, lane < mine && m == neg_inf());
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    if (ch < nch) {
-                        float o[8];
-                        const uint32_t to = quad + kTmemO + sl * 64 + (turns ? grp * 16 : c0) + ch * 8;
-                        if (!first) {
-                            tmem_ld8(to, o);
-                            tmem_wait_ld();
-                        }
+                if (!first) {
+#pragma unroll 1
+                    for (int ch = 0; ch < nch; ++ch) {
+                        float o[8], l[8];
+                        tmem_ld8(to + ch * 8, o);
+                        tmem_ld8(tl + ch * 8, l);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float fe = __shfl_sync(0xffffffffu, f, ch * 8 + e);
-                            l[ch][e] *= fe;
+                            l[e] *= fe;
                             o[e] *= fe;
                         }
-                        if (!first) tmem_st8(to, o);
+                        tmem_st8(to + ch * 8, o);
+                        tmem_st8(tl + ch * 8, l);
                     }
-                if (!first) tmem_wait_st();
+                    tmem_wait_st();
+                }
                 group_any(grp, false);
             }
-            first = false;
             dead |= !wait4<kRegsSoftmax>(&sm.pv_done[b], ph ^ 1, bd);  // the P of the tile before last has been read
             uint8_t *dst = sm.p[b] + key * 32;
+            const bool write = dump && t * kTile + key < n;
+#pragma unroll 1
+            for (int ch = 0; ch < nch; ++ch) {
+                float s[8], f[8], r[8], l[8];
+                load8(fac2 + ch * 8, f);
+                load8(nref + ch * 8, r);
+                tmem_ld8(tl + ch * 8, l);
+                scores8(ts, kk, ch, s);
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                if (ch < nch) {
-                    float e8[8];
+                for (int e = 0; e < 8; ++e) {
+                    r[e] = ex2_approx(fmaf(s[e], f[e], r[e]));
+                    l[e] = r[e] + (first ? 0.f : l[e]);
+                }
+                tmem_st8(tl + ch * 8, l);
+                const int cc = c0 / 8 + ch;
+                *reinterpret_cast<uint4 *>(dst + (cc >> 1) * (kTile * 32) + (((cc & 1) ^ ((key >> 2) & 1)) << 4)) =
+                    make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
+                if (write) {
+                    load8(sm.fac[is] + c0 + ch * 8, f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        e8[e] = ex2_approx(fmaf(s[ch][e], fac2[ch * 8 + e], nref[ch * 8 + e]));
-                        l[ch][e] += e8[e];
+                        float *row = sm.lb[is][c0 + ch * 8 + e];
+                        if (row) row[kk.pos] = s[e] * f[e];
                     }
-                    const int cc = c0 / 8 + ch;
-                    *reinterpret_cast<uint4 *>(dst + (cc >> 1) * (kTile * 32) + (((cc & 1) ^ ((key >> 2) & 1)) << 4)) =
-                        make_uint4(pack_f16x2(e8[0], e8[1]), pack_f16x2(e8[2], e8[3]), pack_f16x2(e8[4], e8[5]),
-                                   pack_f16x2(e8[6], e8[7]));
                 }
+            }
+            first = false;
+            tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
-            arrive_lane0(&sm.p_full[b], turns ? 2 : 1);
-            if (dump && t * kTile + key < n) {
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    if (ch < nch)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const long long lb = sm.lb[is][c0 + ch * 8 + e];
-                            if (lb >= 0) p.logits[lb + pos] = s[ch][e] * sm.fac[is][c0 + ch * 8 + e];
-                        }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_cnt(&sm.p_full[b], turns ? 2 : 1);
+                mbar_arrive_cnt(&sm.s_empty[b], turns ? 2 : 1);
             }
+            __syncwarp();
         }
         // the sums of weights over the warp's keys: of eight rows at a time, each lane ends up with one
+#pragma unroll 1
+        for (int ch = 0; ch < nch; ++ch) {
+            float l[8], z;
+            tmem_ld8(tl + ch * 8, l);
+            tmem_wait_ld();
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-            if (ch < nch) {
-                float a[4], c[2], z;
+            for (int h = 16, k = 4; k; h >>= 1, k >>= 1)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float keep = lane & 16 ? l[ch][4 + e] : l[ch][e], give = lane & 16 ? l[ch][e] : l[ch][4 + e];
-                    a[e] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+                for (int e = 0; e < k; ++e) {
+                    const bool up = lane & h;
+                    const float keep = up ? l[k + e] : l[e], give = up ? l[e] : l[k + e];
+                    l[e] = keep + __shfl_xor_sync(0xffffffffu, give, h);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float keep = lane & 8 ? a[2 + e] : a[e], give = lane & 8 ? a[e] : a[2 + e];
-                    c[e] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
-                }
-                {
-                    const float keep = lane & 4 ? c[1] : c[0], give = lane & 4 ? c[0] : c[1];
-                    z = keep + __shfl_xor_sync(0xffffffffu, give, 4);
-                }
-                z += __shfl_xor_sync(0xffffffffu, z, 2);
-                z += __shfl_xor_sync(0xffffffffu, z, 1);
-                if ((lane & 3) == 0) sm.sum[sl][grp][w][ch * 8 + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = z;
-            }
+            z = first ? 0.f : l[0];
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            if ((lane & 3) == 0) sm.sum[sl][grp][w][ch * 8 + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = z;
+        }
         arrive_lane0(&sm.epi_full[sl]);
         arrive_lane0(&sm.item_empty[is]);
     }
@@ -659,54 +670,58 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
 template <int D>
 __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, int w, int lane) {
     constexpr int W = D / 64;  // words of a lane
+#pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems;
         if (!wait4<kRegsRest>(&sm.item_full[is], i / kItems & 1, bd)) return;
         const ItemRec rec = sm.item[is];
         if (rec.stop) return;
         if (!wait4<kRegsRest>(&sm.q_empty[i & 1], (i >> 1 & 1) ^ 1, bd)) return;
+#pragma unroll 1
         for (int r0 = 8 * w; r0 < rec.rows; r0 += 16) {
-            uint32_t x[8][W];
+            // (lane l looks after row r0 + l % 8)
+            const int my = r0 + (lane & 7), j = rec.verify ? my / p.G : 0, gi = my - j * p.G;
+            const int at = my < rec.rows ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : -1;
+            uint32_t x[8][W], mine = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int r = r0 + e, j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
+                const int row = __shfl_sync(0xffffffffu, at, e);
 #pragma unroll
                 for (int a = 0; a < W; ++a) x[e][a] = 0;
-                if (r < rec.rows) {
-                    const uint16_t *src = p.q + ((size_t)(rec.q_off + j) * p.Hq + (size_t)rec.g * p.G + gi) * D + lane * 2 * W;
+                if (row >= 0) {
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (size_t)row * D) + lane * W;
                     if (W == 2) {
                         const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src));
                         x[e][0] = y.x, x[e][W - 1] = y.y;
                     } else {
-                        x[e][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+                        x[e][0] = __ldg(src);
                     }
                 }
             }
+            uint8_t *dst = sm.q[i & 1] + (lane * W / 32) * (kMaxRows * 128) + r0 * 128 + lane * W % 4 * 4;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int r = r0 + e;
                 uint32_t mx = x[e][0] & 0x7fff7fffu;
                 if (W == 2) mx = __vmaxu2(mx, x[e][W - 1] & 0x7fff7fffu);
-                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-                const int ex = max((int)(mx >> 7), 15);            // biased exponent, such that 2^(141 - ex) is finite
-                const float up = __int_as_float((268 - ex) << 23); // 2^(141 - ex): the largest comes to [2^14, 2^15)
-                const float down = __int_as_float((ex - 14) << 23);
-                uint8_t *dst = sm.q[i & 1] + (lane * W / 32) * (kMaxRows * 128) + r * 128 +
-                               (((lane * W % 32 / 4) ^ (r & 7)) << 4) + lane * W % 4 * 4;
+                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16)) >> 7;
+                mx = max(mx, 15u);                                     // biased exponent, such that 2^(141 - mx) is finite
+                if ((lane & 7) == e) mine = mx;
+                const float up = __uint_as_float((268u - mx) << 23);   // 2^(141 - mx): the largest comes to [2^14, 2^15)
+                uint8_t *to = dst + e * 128 + (((lane * W % 32 / 4) ^ e) << 4);  // (r0 is a multiple of 8)
                 if (W == 2)
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up),
-                                                                 pack_f16x2(bf16lo(x[e][W - 1]) * up, bf16hi(x[e][W - 1]) * up));
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up),
+                                                                pack_f16x2(bf16lo(x[e][W - 1]) * up, bf16hi(x[e][W - 1]) * up));
                 else
-                    *reinterpret_cast<uint32_t *>(dst) = pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up);
-                if (lane == e) {
-                    const int j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
-                    const float fac = fmaxf(down * p.scale, __int_as_float(1));  // (above 0: a masked score stays -inf)
-                    sm.fac[is][r] = fac;
-                    sm.fac2[is][r] = fmaxf(fac * kLog2e, __int_as_float(1));
-                    sm.lim[is][r] = rec.verify && r < rec.rows ? rec.L - (p.k + 1) + j : 0x7fffffff;
-                    sm.lb[is][r] = r < rec.rows && rec.verify && p.logits
-                                       ? rec.logit_off + ((long long)(rec.g * p.G + gi) * (p.k + 1) + j) * rec.L : -1;
-                }
+                    *reinterpret_cast<uint32_t *>(to) = pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up);
+            }
+            if (lane < 8) {
+                const float down = __uint_as_float((mine - 14u) << 23);
+                const float fac = fmaxf(down * p.scale, __int_as_float(1));  // (above 0: a masked score stays -inf)
+                sm.fac[is][my] = fac;
+                sm.fac2[is][my] = fmaxf(fac * kLog2e, __int_as_float(1));
+                sm.lim[is][my] = rec.verify && my < rec.rows ? rec.L - (p.k + 1) + j : 0x7fffffff;
+                sm.lb[is][my] = my < rec.rows && rec.verify && p.logits
+                                    ? p.logits + (rec.logit_off + ((long long)(rec.g * p.G + gi) * (p.k + 1) + j) * rec.L) : nullptr;
             }
         }
         fence_proxy_async_smem();
@@ -721,6 +736,7 @@ __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, in
 template <int D>
 __device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int w, int lane) {
     const int d = 32 * w + lane;
+#pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems, sl = i & 1;
         if (!wait4<kRegsRest>(&sm.item_full[is], i / kItems & 1, bd)) return;
