@@ -97,24 +97,25 @@ struct Smem4 {
     uint64_t q_full[2], q_empty[2], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], pv_done[2];
     uint64_t o_full[2], o_empty[2], epi_full[2], epi_empty[2], drain;
     uint32_t tmem;
-    int abort;
+    int abort;  // a wait has given up
 };
 static_assert(sizeof(Smem4<128>) <= 227 * 1024, "shared memory of a CTA");
 static_assert(sizeof(Smem4<64>) > 114 * 1024, "never two CTAs on an SM: each takes all of its tensor memory");
 
-struct Bounds4 {
-    volatile int *abort;
-    int *err;
-    unsigned long long ns;
-};
-// A bounded wait by a whole warp: the first test inline, the polling out of line (a function per register count).
-template <int kRegs>
-__device__ __noinline__ bool poll4(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, unsigned long long ns) {
-    return mbar_wait_warp(bar, parity, abort, err, ns);
-}
-template <int kRegs>
-__device__ __forceinline__ bool wait4(uint64_t *bar, uint32_t parity, const Bounds4 &b) {
-    return mbar_try_wait_warp(bar, parity) || poll4<kRegs>(bar, parity, b.abort, b.err, b.ns);
+// A wait by a whole warp, a few instructions long (every wait that is inlined costs the roles' shared instruction cache; with
+// the clock in each, plain decoding took 227 us where this took XXX).  The products' warp watches the clock for all: nothing
+// moves in a CTA for long without it, and when it has had nothing to do for the bound it raises the abort flag.  A count of polls
+// bounds the waits that outlive it.
+constexpr int kMostPolls = 1 << 22;
+template <int D>
+__device__ __forceinline__ bool wait4(uint64_t *bar, uint32_t parity, Smem4<D> &sm) {
+#pragma unroll 1
+    for (int n = 0; !mbar_try_wait_warp(bar, parity); ++n)
+        if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort) | (n > kMostPolls))) {
+            sm.abort = 1;
+            return false;
+        }
+    return true;
 }
 constexpr int kRegsSoftmax = 104, kRegsConvert = 72, kRegsRest = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + 2 * kRegsRest <= kThreads4 / 128 * 80, "the registers at launch");
@@ -180,20 +181,21 @@ __device__ __forceinline__ int first_chunks(int rows) { return ((rows + 7) / 8 +
 // ------------------------------------------------------------------ resolver warp
 
 template <int D>
-__device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, int lane) {
+__device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, int lane) {
     const int num_items = *reinterpret_cast<volatile int *>(&p.hdr->num_items);
     int slot = 0;  // of the next chunk
     uint32_t phase = 0;
+#pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems;
-        if (!wait4<kRegsRest>(&sm.item_empty[is], (i / kItems & 1) ^ 1, bd)) return;
+        if (!wait4(&sm.item_empty[is], (i / kItems & 1) ^ 1, sm)) return;
         int it = 0;
         if (lane == 0) it = atomicAdd(&p.hdr->item_counter, 1);
         it = __shfl_sync(0xffffffffu, it, 0);
         if (it >= num_items) {
             if (lane == 0) sm.item[is].stop = 1;
             arrive_lane0(&sm.item_full[is]);
-            if (!wait4<kRegsRest>(&sm.rows_empty[slot], phase ^ 1, bd)) return;
+            if (!wait4(&sm.rows_empty[slot], phase ^ 1, sm)) return;
             if (lane == 0) sm.chunk_tiles[slot] = 0;
             arrive_lane0(&sm.rows_full[slot]);
             return;
@@ -225,8 +227,9 @@ __device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, i
         const int *list = p.sparse_idx + ((size_t)b * p.Hkv + g) * p.max_sparse + itm.begin;
         const int *table = p.c.table + (size_t)b * p.c.max_blocks;
         int bad = 0;
+#pragma unroll 1
         for (int k0 = 0; k0 < tiles * kTile; k0 += kChunkKeys) {
-            if (!wait4<kRegsRest>(&sm.rows_empty[slot], phase ^ 1, bd)) return;
+            if (!wait4(&sm.rows_empty[slot], phase ^ 1, sm)) return;
             int *rows = sm.row[slot];
             if (verify) {  // (items begin at multiples of 64: a lane has the sixteen keys of a block)
                 const int k = k0 + lane * PILLAR_KV_BLOCK, pos = (itm.begin + k) / PILLAR_KV_BLOCK;
@@ -243,29 +246,34 @@ __device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, i
                         make_int4(e < m ? row + e : -1, e + 1 < m ? row + e + 1 : -1, e + 2 < m ? row + e + 2 : -1,
                                   e + 3 < m ? row + e + 3 : -1);
             } else {
-                int pos[kChunkKeys / 32];
+                // (the loads without conditions, eight in flight: past the end, and for bad positions, of a key that there is)
+#pragma unroll 1
+              for (int k1 = 0; k1 < kChunkKeys && k0 + k1 < tiles * kTile; k1 += 256) {
+                int pos[8], blk[8];
 #pragma unroll
-                for (int e = 0; e < kChunkKeys / 32; ++e) {
-                    const int k = k0 + e * 32 + lane;
-                    pos[e] = -1;
-                    if (k < n) {
-                        pos[e] = __ldg(list + k);
-                        if (pos[e] < 0 || pos[e] >= ri.len) bad |= PILLAR_FLAG_INDEX, pos[e] = -1;
+                for (int e = 0; e < 8; ++e) pos[e] = n > 0 ? __ldg(list + min(k0 + k1 + e * 32 + lane, n - 1)) : -1;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if ((unsigned)pos[e] >= (unsigned)ri.len) bad |= PILLAR_FLAG_INDEX * (n > 0), pos[e] = -1;
+                    blk[e] = __ldg(table + min((unsigned)max(pos[e], 0) / PILLAR_KV_BLOCK, (unsigned)p.c.max_blocks - 1));
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    int row = -1;
+                    if (pos[e] >= 0) {
+                        if ((unsigned)blk[e] < (unsigned)p.c.num_blocks && pos[e] / PILLAR_KV_BLOCK < p.c.max_blocks)
+                            row = (blk[e] * p.Hkv + g) * PILLAR_KV_BLOCK + pos[e] % PILLAR_KV_BLOCK;
+                        else bad |= PILLAR_FLAG_SLOT;
                     }
+                    rows[k1 + e * 32 + lane] = k0 + k1 + e * 32 + lane < n ? row : -1;
                 }
-#pragma unroll
-                for (int e = 0; e < kChunkKeys / 32; ++e) {
-                    int blk = 0;
-                    if (pos[e] >= 0) blk = pos[e] / PILLAR_KV_BLOCK < p.c.max_blocks ? __ldg(table + pos[e] / PILLAR_KV_BLOCK) : -1;
-                    if (blk < 0 || blk >= p.c.num_blocks) bad |= PILLAR_FLAG_SLOT, pos[e] = -1;
-                    rows[e * 32 + lane] = pos[e] >= 0 ? (blk * p.Hkv + g) * PILLAR_KV_BLOCK + pos[e] % PILLAR_KV_BLOCK : -1;
-                }
+              }
             }
             if (lane == 0) sm.chunk_tiles[slot] = min(kChunkTiles, tiles - k0 / kTile);
             arrive_lane0(&sm.rows_full[slot]);
             if (++slot == kChunks) slot = 0, phase ^= 1;
         }
-        if (bad) atomicOr(bd.err, bad);
+        if (bad) atomicOr(&p.hdr->err, bad);
     }
 }
 
@@ -274,7 +282,7 @@ __device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, i
 // Warp w of K's (or V's) four: keys 32 w .. 32 w + 31 of every tile, from the copies to the operand.  (Code is kept small here
 // and below, rolled where it can be: the roles run at once and share the instruction cache.)
 template <int D, bool kValue>
-__device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int w, int lane) {
+__device__ void convert4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, int lane) {
     using S = Smem4<D>;
     constexpr int RC = S::kRow / 16;                            // 16-byte pieces of a row of codes
     const uint8_t *codes = kValue ? p.c.v4 : p.c.k4, *scales = kValue ? p.c.v_scale : p.c.k_scale;
@@ -289,7 +297,7 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
     for (int x = 1 - kStages; ok; ++x) {
         // the loads of tile x + kStages - 1
         if (more && at == tiles) {
-            ok = wait4<kRegsConvert>(&sm.rows_full[slot], phase, bd);
+            ok = wait4(&sm.rows_full[slot], phase, sm);
             tiles = ok ? sm.chunk_tiles[slot] : 0;
             at = 0;
             more = tiles > 0;
@@ -320,7 +328,7 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
         __syncwarp();
         const int st = x % kStages, buf = x & 1;
         // the operand's buffer is free: the scores (the outputs) of the tile before last are done
-        ok = wait4<kRegsConvert>(kValue ? &sm.pv_done[buf] : &sm.s_full[buf], (x >> 1 & 1) ^ 1, bd);
+        ok = wait4(kValue ? &sm.pv_done[buf] : &sm.s_full[buf], (x >> 1 & 1) ^ 1, sm);
         if (!ok) break;
         tc_fence_after();
         const uint8_t *src = sm.codes[kValue][st] + key * S::kRow;
@@ -367,13 +375,14 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
 __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) { return umma_sdesc(saddr, kTile * 32, 256) | ((uint64_t)6 << 61); }
 
 template <int D>
-__device__ void mma4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm) {
+__device__ void mma4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
     constexpr uint32_t kId = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);  // f16 operands, fp32 sums, M = 128
     uint32_t vs = 0, vp = 0;            // tiles whose scores, whose outputs have been issued
     int si = 0, st = 0, sT = 0, sN = 0;  // scores: item, tile of it, its tiles (0: to come), its rows
     int oi = 0, ot = 0, oT = 0, orows = 0;
     bool stop = false, issued = false;
     unsigned long long idle = 0;
+#pragma unroll 1
     for (uint32_t spin = 0;; ++spin) {
         bool progress = false;
         if (!stop && vs - vp < 2) {
@@ -441,10 +450,8 @@ __device__ void mma4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32
         if ((spin & 63) == 0) {
             const unsigned long long now = global_timer_ns();
             if (idle == 0) idle = now;
-            const bool over = now - idle > bd.ns;
-            if (__any_sync(0xffffffffu, over || *bd.abort)) {
-                if (over) atomicOr(bd.err, PILLAR_FLAG_TIMEOUT);
-                *bd.abort = 1;
+            if (__any_sync(0xffffffffu, now - idle > p.wait_ns || *static_cast<volatile int *>(&sm.abort))) {
+                *static_cast<volatile int *>(&sm.abort) = 1;
                 break;
             }
         }
@@ -496,7 +503,7 @@ __device__ __forceinline__ void load8(const float *src, float (&v)[8]) {
 }
 
 template <int D>
-__device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int grp, int w, int lane) {
+__device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp, int w, int lane) {
     const int key = 32 * w + lane;
     const uint32_t quad = tm + ((uint32_t)w << 21);
     uint32_t x = 0;  // tile
@@ -506,7 +513,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems, sl = i & 1;
-        dead |= !wait4<kRegsSoftmax>(&sm.item_full[is], i / kItems & 1, bd);
+        dead |= !wait4(&sm.item_full[is], i / kItems & 1, sm);
         if (group_any(grp, dead)) return;
         const ItemRec &rec = sm.item[is];
         if (rec.stop) return;
@@ -515,11 +522,11 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
         const int sure = verify ? rec.L - (p.k + 1) : 0x7fffffff;  // every row sees up to here
         const int c0 = !turns && grp ? 8 * first_chunks(rows) : 0;
         const int mine = !turns && !grp ? min(rows, 8 * first_chunks(rows)) : rows - c0, nch = (mine + 7) / 8;
-        dead |= !wait4<kRegsSoftmax>(&sm.fac_full[is], i / kItems & 1, bd);
-        dead |= !wait4<kRegsSoftmax>(&sm.epi_empty[sl], (i >> 1 & 1) ^ 1, bd);
+        dead |= !wait4(&sm.fac_full[is], i / kItems & 1, sm);
+        dead |= !wait4(&sm.epi_empty[sl], (i >> 1 & 1) ^ 1, sm);
         // Where both groups use both buffers, the other one is done with the item before: its tiles' phases are over, and a
         // wait for the next phase of a buffer that this group has not watched is one for the right one.
-        if (!turns && i > 0) dead |= !wait4<kRegsSoftmax>(&sm.epi_full[sl ^ 1], (i - 1) >> 1 & 1, bd);
+        if (!turns && i > 0) dead |= !wait4(&sm.epi_full[sl ^ 1], (i - 1) >> 1 & 1, sm);
         const float *fac2 = sm.fac2[is] + c0;
         float *nref = sm.nref[sl][grp];
         if (w == 0) nref[lane] = kLift;
@@ -531,7 +538,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
         kk.lim = sm.lim[is] + c0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t, ++x, kk.pos += kTile) {
-            if (t % kChunkTiles == 0) dead |= !wait4<kRegsSoftmax>(&sm.rows_full[slot], phase, bd);
+            if (t % kChunkTiles == 0) dead |= !wait4(&sm.rows_full[slot], phase, sm);
             kk.there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
             if (t % kChunkTiles == kChunkTiles - 1 || t == tiles - 1) {
                 arrive_lane0(&sm.rows_empty[slot]);
@@ -541,7 +548,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
             if (turns && b != grp) continue;
             const uint32_t ph = x >> 1 & 1, ts = quad + kTmemS + b * 64 + c0;
             kk.part = !kk.there || (verify && kk.pos > sure);
-            dead |= !wait4<kRegsSoftmax>(&sm.s_full[b], ph, bd);
+            dead |= !wait4(&sm.s_full[b], ph, sm);
             tc_fence_after();
             float most = neg_inf();
 #pragma unroll 1
@@ -570,7 +577,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
                 sm.top[grp][w][lane] = mx;
                 if (!first) {  // what has been added to O so far is done: its rows are scaled below
                     const uint32_t y = turns ? x - 2 : x - 1;
-                    dead |= !wait4<kRegsSoftmax>(&sm.pv_done[y & 1], y >> 1 & 1, bd);
+                    dead |= !wait4(&sm.pv_done[y & 1], y >> 1 & 1, sm);
                     tc_fence_after();
                 }
                 group_any(grp, false);
@@ -601,7 +608,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
                 }
                 group_any(grp, false);
             }
-            dead |= !wait4<kRegsSoftmax>(&sm.pv_done[b], ph ^ 1, bd);  // the P of the tile before last has been read
+            dead |= !wait4(&sm.pv_done[b], ph ^ 1, sm);  // the P of the tile before last has been read
             uint8_t *dst = sm.p[b] + key * 32;
             const bool write = dump && t * kTile + key < n;
 #pragma unroll 1
@@ -666,25 +673,25 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, ui
 
 // ------------------------------------------------------------------ query warps
 
-// The f16 query operands of an item (two warps, eight rows at a time each) and what the softmax warps know about its rows.
+// The f16 query operands of an item (two warps, four rows at a time each) and what the softmax warps know about its rows.
 template <int D>
-__device__ void queries4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, int w, int lane) {
+__device__ void queries4(const Kv4Params &p, Smem4<D> &sm, int w, int lane) {
     constexpr int W = D / 64;  // words of a lane
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems;
-        if (!wait4<kRegsRest>(&sm.item_full[is], i / kItems & 1, bd)) return;
+        if (!wait4(&sm.item_full[is], i / kItems & 1, sm)) return;
         const ItemRec rec = sm.item[is];
         if (rec.stop) return;
-        if (!wait4<kRegsRest>(&sm.q_empty[i & 1], (i >> 1 & 1) ^ 1, bd)) return;
+        if (!wait4(&sm.q_empty[i & 1], (i >> 1 & 1) ^ 1, sm)) return;
 #pragma unroll 1
-        for (int r0 = 8 * w; r0 < rec.rows; r0 += 16) {
-            // (lane l looks after row r0 + l % 8)
-            const int my = r0 + (lane & 7), j = rec.verify ? my / p.G : 0, gi = my - j * p.G;
+        for (int r0 = 4 * w; r0 < (rec.rows + 7) / 8 * 8; r0 += 8) {
+            // (lane l looks after row r0 + l % 4)
+            const int my = r0 + (lane & 3), j = rec.verify ? my / p.G : 0, gi = my - j * p.G;
             const int at = my < rec.rows ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : -1;
-            uint32_t x[8][W], mine = 0;
+            uint32_t x[4][W], mine = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 const int row = __shfl_sync(0xffffffffu, at, e);
 #pragma unroll
                 for (int a = 0; a < W; ++a) x[e][a] = 0;
@@ -700,21 +707,21 @@ __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, in
             }
             uint8_t *dst = sm.q[i & 1] + (lane * W / 32) * (kMaxRows * 128) + r0 * 128 + lane * W % 4 * 4;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 uint32_t mx = x[e][0] & 0x7fff7fffu;
                 if (W == 2) mx = __vmaxu2(mx, x[e][W - 1] & 0x7fff7fffu);
                 mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16)) >> 7;
                 mx = max(mx, 15u);                                     // biased exponent, such that 2^(141 - mx) is finite
-                if ((lane & 7) == e) mine = mx;
+                if ((lane & 3) == e) mine = mx;
                 const float up = __uint_as_float((268u - mx) << 23);   // 2^(141 - mx): the largest comes to [2^14, 2^15)
-                uint8_t *to = dst + e * 128 + (((lane * W % 32 / 4) ^ e) << 4);  // (r0 is a multiple of 8)
+                uint8_t *to = dst + e * 128 + (((lane * W % 32 / 4) ^ ((r0 + e) & 7)) << 4);
                 if (W == 2)
                     *reinterpret_cast<uint2 *>(to) = make_uint2(pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up),
                                                                 pack_f16x2(bf16lo(x[e][W - 1]) * up, bf16hi(x[e][W - 1]) * up));
                 else
                     *reinterpret_cast<uint32_t *>(to) = pack_f16x2(bf16lo(x[e][0]) * up, bf16hi(x[e][0]) * up);
             }
-            if (lane < 8) {
+            if (lane < 4) {
                 const float down = __uint_as_float((mine - 14u) << 23);
                 const float fac = fmaxf(down * p.scale, __int_as_float(1));  // (above 0: a masked score stays -inf)
                 sm.fac[is][my] = fac;
@@ -734,71 +741,70 @@ __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, in
 // ------------------------------------------------------------------ epilogue warps
 
 template <int D>
-__device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, const Bounds4 &bd, uint32_t tm, int w, int lane) {
+__device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, int lane) {
     const int d = 32 * w + lane;
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems, sl = i & 1;
-        if (!wait4<kRegsRest>(&sm.item_full[is], i / kItems & 1, bd)) return;
+        if (!wait4(&sm.item_full[is], i / kItems & 1, sm)) return;
         const ItemRec rec = sm.item[is];
         if (rec.stop) return;
-        if (!wait4<kRegsRest>(&sm.epi_full[sl], i >> 1 & 1, bd) || !wait4<kRegsRest>(&sm.o_full[sl], i >> 1 & 1, bd)) return;
+        if (!wait4(&sm.epi_full[sl], i >> 1 & 1, sm) || !wait4(&sm.o_full[sl], i >> 1 & 1, sm)) return;
         tc_fence_after();
-        const bool turns = takes_turns(rec.rows);
+        const bool turns = takes_turns(rec.rows), whole = rec.nsplit == 1;
         const int split = 8 * first_chunks(rec.rows);
-        // rows lane and lane + 32: what the (two) accumulators are multiplied by
-        float f0[2] = {0.f, 0.f}, f1[2] = {0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = lane + 32 * h;
-            if (r >= rec.rows) continue;
-            const int grp = !turns && r >= split, c = r - (grp ? split : 0);
-            const float *s0 = &sm.sum[sl][grp][0][c];
-            float l = s0[0] + s0[32] + s0[64] + s0[96], ref = -sm.nref[sl][grp][c];
-            f0[h] = 1.f;
-            if (turns) {
-                const float *s1 = &sm.sum[sl][1][0][c];
-                const float l1 = s1[0] + s1[32] + s1[64] + s1[96], ref1 = -sm.nref[sl][1][c];
-                // (a sum of 0 has no reference)
-                const float top = l == 0.f ? ref1 : l1 == 0.f ? ref : fmaxf(ref, ref1);
-                f0[h] = l == 0.f ? 0.f : ex2_approx(ref - top);
-                f1[h] = l1 == 0.f ? 0.f : ex2_approx(ref1 - top);
-                l = __fadd_rn(__fmul_rn(l, f0[h]), __fmul_rn(l1, f1[h]));  // (the same whichever group began)
-                ref = top;
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            // (what is 0 stays it under a NaN sum: an accumulator that nobody wrote is not read)
-            if (f0[h] != 0.f) f0[h] *= inv;
-            if (f1[h] != 0.f) f1[h] *= inv;
-            if (w == 0) {
-                const float z = l > 0.f ? ref * 0.69314718f + logf(l) : (l == 0.f ? neg_inf() : l);  // (a NaN sum stays one)
-                const int j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
-                if (rec.nsplit > 1) p.part_lse[(size_t)rec.rec + r] = z;
-                else if (rec.verify) p.lse[((size_t)rec.vidx * p.Hq + (size_t)rec.g * p.G + gi) * (p.k + 1) + j] = z;
-            }
-        }
-        // (in turns, an item of one tile has one accumulator: a group that met no tile has sums of 0)
-        const bool any0 = !turns || __any_sync(0xffffffffu, f0[0] != 0.f), any1 = turns && __any_sync(0xffffffffu, f1[0] != 0.f);
-        int j = 0, gi = 0;
 #pragma unroll 1
-        for (int r0 = 0; r0 < rec.rows; r0 += 8) {
-            float o[8], o1[8];
-            tmem_ld8(tm + ((uint32_t)w << 21) + kTmemO + sl * 64 + r0, o);
-            if (any1) tmem_ld8(tm + ((uint32_t)w << 21) + kTmemO + sl * 64 + 16 + r0, o1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int r = r0 + e;
-                const float a0 = __shfl_sync(0xffffffffu, r0 < 32 ? f0[0] : f0[1], r & 31);
-                const float a1 = __shfl_sync(0xffffffffu, f1[0], r & 31);
-                const float y = __fadd_rn(any0 ? __fmul_rn(o[e], a0) : 0.f, any1 ? __fmul_rn(o1[e], a1) : 0.f);
-                if (r < rec.rows && d < D) {
-                    if (rec.nsplit > 1) p.part_o[((size_t)rec.rec + r) * D + d] = y;
-                    else
-                        p.out[((size_t)(rec.q_off + j) * p.Hq + (size_t)rec.g * p.G + gi) * D + d] =
-                            (uint16_t)pack_bf16x2(y, 0.f);
+        for (int h = 0; h < rec.rows; h += 32) {
+            // row h + lane: where it goes (-1: there is none), and what the (two) accumulators are multiplied by
+            const int r = h + lane, j = rec.verify ? r / p.G : 0, gi = r - j * p.G;
+            int at = -1;
+            float f0 = 0.f, f1 = 0.f;
+            if (r < rec.rows) {
+                at = whole ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : rec.rec + r;
+                const int grp = !turns && r >= split, c = r - (grp ? split : 0);
+                const float *s0 = &sm.sum[sl][grp][0][c];
+                float l = s0[0] + s0[32] + s0[64] + s0[96], ref = -sm.nref[sl][grp][c];
+                f0 = 1.f;
+                if (turns) {
+                    const float *s1 = &sm.sum[sl][1][0][c];
+                    const float l1 = s1[0] + s1[32] + s1[64] + s1[96], ref1 = -sm.nref[sl][1][c];
+                    // (a sum of 0 has no reference)
+                    const float top = l == 0.f ? ref1 : l1 == 0.f ? ref : fmaxf(ref, ref1);
+                    f0 = l == 0.f ? 0.f : ex2_approx(ref - top);
+                    f1 = l1 == 0.f ? 0.f : ex2_approx(ref1 - top);
+                    l = __fadd_rn(__fmul_rn(l, f0), __fmul_rn(l1, f1));  // (the same whichever group began)
+                    ref = top;
                 }
-                if (++gi == p.G && rec.verify) gi = 0, ++j;
+                const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+                // (what is 0 stays it under a NaN sum: an accumulator that nobody wrote is not read)
+                if (f0 != 0.f) f0 *= inv;
+                if (f1 != 0.f) f1 *= inv;
+                if (w == 0) {
+                    const float z = l > 0.f ? ref * 0.69314718f + logf(l) : (l == 0.f ? neg_inf() : l);  // (a NaN sum stays one)
+                    if (!whole) p.part_lse[at] = z;
+                    else if (rec.verify) p.lse[((size_t)rec.vidx * p.Hq + (size_t)rec.g * p.G + gi) * (p.k + 1) + j] = z;
+                }
+            }
+            // (in turns, an item of one tile has one accumulator: a group that met no tile has sums of 0)
+            const bool any0 = !turns || __any_sync(0xffffffffu, f0 != 0.f), any1 = __any_sync(0xffffffffu, f1 != 0.f);
+#pragma unroll 1
+            for (int r0 = 0; r0 < min(32, rec.rows - h); r0 += 8) {
+                float o[8], o1[8];
+                const uint32_t from = tm + ((uint32_t)w << 21) + kTmemO + sl * 64 + h + r0;
+                tmem_ld8(from, o);
+                tmem_ld8(from + (turns ? 16 : 0), o1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a0 = __shfl_sync(0xffffffffu, f0, r0 + e), a1 = __shfl_sync(0xffffffffu, f1, r0 + e);
+                    const int row = __shfl_sync(0xffffffffu, at, r0 + e);
+                    const float y = __fadd_rn(any0 ? __fmul_rn(o[e], a0) : 0.f, any1 ? __fmul_rn(o1[e], a1) : 0.f);
+                    if (row >= 0 && d < D) {
+                        const size_t to = (size_t)row * D + d;
+                        if (whole) p.out[to] = (uint16_t)pack_bf16x2(y, 0.f);
+                        else p.part_o[to] = y;
+                    }
+                }
             }
         }
         tc_fence_before();
@@ -850,34 +856,34 @@ __global__ void __launch_bounds__(kThreads4, 1) attn_kv4_kernel(const __grid_con
     const uint32_t tm = sm.tmem;
     pdl_wait_prerequisites();  // the plan's output is read only from here on
     pdl_launch_dependents();   // (the merge waits for this kernel's completion itself)
-    const Bounds4 bd{&sm.abort, &p.hdr->err, p.wait_ns};
     // the registers go to the softmax warps: 80 a thread at launch
     switch (warp >> 2) {
         case 0:
         case 1:
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-            softmax4<D>(p, sm, bd, tm, warp >> 2, w, lane);
+            softmax4<D>(p, sm, tm, warp >> 2, w, lane);
             break;
         case 2:
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-            convert4<D, false>(p, sm, bd, tm, w, lane);
+            convert4<D, false>(p, sm, tm, w, lane);
             break;
         case 3:
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-            convert4<D, true>(p, sm, bd, tm, w, lane);
+            convert4<D, true>(p, sm, tm, w, lane);
             break;
         case 4:
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-            if (w == 0) resolver4<D>(p, sm, bd, lane);
-            else if (w == 1) mma4<D>(p, sm, bd, tm);
-            else queries4<D>(p, sm, bd, w - 2, lane);
+            if (w == 0) resolver4<D>(p, sm, lane);
+            else if (w == 1) mma4<D>(p, sm, tm);
+            else queries4<D>(p, sm, w - 2, lane);
             break;
         default:
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-            epilogue4<D>(p, sm, bd, tm, w, lane);
+            epilogue4<D>(p, sm, tm, w, lane);
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sm.abort) atomicOr(&p.hdr->err, PILLAR_FLAG_TIMEOUT);
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tm, kTmemCols);
