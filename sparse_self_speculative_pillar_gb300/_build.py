@@ -15,7 +15,8 @@ LIB = os.path.join(OUT_DIR, "libpillar_gb300.so")
 SOURCES = ["pillar_plan.cu", "pillar_attn.cu", "pillar_topk.cu", "pillar_api.cu", "pillar_topk_noalloc.cu",
            "pillar_sched.cu", "pillar_kv.cu", "pillar_lists.cu", "pillar_map.cu",
            "pillar_kv8.cu", "pillar_attn_kv8.cu", "pillar_prompt.cu",
-           "pillar_kv4.cu", "pillar_kv_read.cu", "pillar_attn_kv4.cu"]
+           "pillar_kv4.cu", "pillar_kv_read.cu", "pillar_attn_kv4.cu",
+           "pillar_attn_kv4_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

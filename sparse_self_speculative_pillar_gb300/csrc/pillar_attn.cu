@@ -1122,8 +1122,8 @@ constexpr int kMergeCtasPerSm = 1;  // one large CTA per SM: the whole grid is r
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads, kMergeCtasPerSm) merge_kernel(const AttnParams p) {
     pdl_wait_prerequisites();  // the partials come from the attention kernel
-    // the attention kernel is complete: its work queue is reset for the next run on the same plan
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->item_counter = 0;
+    // the attention kernel is complete: its work queues are reset for the next run on the same plan
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->item_counter = 0, p.hdr->draft_counter = 0;
     constexpr int C4 = D / 4;
     const int vslot = p.M * C4, dslot = p.G * C4;  // thread slots of a verify unit, of a draft unit
     const int nv = p.hdr->num_merge, nd = p.hdr->num_merge_draft, U = p.hdr->num_units;

@@ -28,7 +28,7 @@
 //     the group finds out.  P is rounded to f16 relative to it: weights are at
 //     most 2^14, and 2^6 or more for a row's largest.
 //   * Four warps write finished items, two stage queries.
-#include "pillar_kv4.cuh"
+#include "pillar_attn_kv4.cuh"
 
 namespace pillar {
 
@@ -42,27 +42,8 @@ constexpr int kItems = 8;                    // items in flight
 constexpr int kStages = 4;                   // tiles of codes in shared memory
 constexpr int kWarps = 24;
 constexpr int kThreads4 = kWarps * 32;
-constexpr float kLift = 6.f;                 // log2 of the weight of a probability at its row's reference maximum
-constexpr float kGrow = 8.f + kLift;         // the reference moves once a weight passes 2^kGrow
 // tensor memory: two tiles of K, two of S^T, the O^T of two items, sums of weights (a key's lane, a column per row)
 constexpr uint32_t kTmemCols = 512, kTmemK = 0, kTmemS = 128, kTmemO = 256, kTmemL = 384;
-
-struct Kv4Params {
-    const uint16_t *q;
-    Kv4Cache c;
-    const int *sparse_idx;
-    uint16_t *out;
-    float *logits, *lse;  // logits may be null
-    WsHeader *hdr;
-    const ReqInfo *req;
-    const long long *logit_off;
-    const UnitInfo *unit;
-    const Item *items;
-    float *part_o, *part_lse;
-    int Hq, Hkv, G, k, M, max_sparse;
-    float scale;
-    unsigned long long wait_ns;
-};
 
 // A work item in shared memory.
 struct alignas(16) ItemRec {
@@ -167,12 +148,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
-    return h;
-}
-
 // How an item's query rows are shared by the softmax groups: at most 16 rows, the groups take tiles in turn; else group 0
 // has the first `first` chunks of eight rows and group 1 the others.
 __device__ __forceinline__ bool takes_turns(int rows) { return rows <= 16; }
@@ -182,7 +157,7 @@ __device__ __forceinline__ int first_chunks(int rows) { return ((rows + 7) / 8 +
 
 template <int D>
 __device__ void resolver4(const Kv4Params &p, Smem4<D> &sm, int lane) {
-    const int num_items = *reinterpret_cast<volatile int *>(&p.hdr->num_items);
+    const int num_items = *reinterpret_cast<volatile int *>(&p.hdr->num_verify_items);
     int slot = 0;  // of the next chunk
     uint32_t phase = 0;
 #pragma unroll 1
@@ -948,7 +923,12 @@ cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaS
     p.max_sparse = a.max_sparse;
     p.scale = a.scale;
     p.wait_ns = a.wait_ns;
-    const cudaError_t e = a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
+    // Verify items of more than eight rows and then the others, whose CTAs take the place of the first ones as these end.
+    const bool many = p.M > kFewRows && a.schedule != PILLAR_SCHEDULE_DRAFT_ONLY;
+    cudaError_t e = cudaSuccess;
+    if (many) e = a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
+    if (e == cudaSuccess && (!many || a.schedule != PILLAR_SCHEDULE_VERIFY_ONLY))
+        e = launch_attn_kv4_few(p, a.D, many, nsm, st);
     return e == cudaSuccess ? launch_merge(a, nsm, st) : e;
 }
 

@@ -1,0 +1,49 @@
+// pillar_attn_kv4.cuh -- what the two kernels of the 4-bit attention share: items of at most eight query rows
+// (pillar_attn_kv4_few.cu) and the others (pillar_attn_kv4.cu).
+#pragma once
+
+#include "pillar_kv4.cuh"
+
+namespace pillar {
+
+constexpr int kFewRows = 8;
+
+struct Kv4Params {
+    const uint16_t *q;
+    Kv4Cache c;
+    const int *sparse_idx;
+    uint16_t *out;
+    float *logits, *lse;  // logits may be null
+    WsHeader *hdr;
+    const ReqInfo *req;
+    const long long *logit_off;
+    const UnitInfo *unit;
+    const Item *items;
+    float *part_o, *part_lse;
+    int Hq, Hkv, G, k, M, max_sparse;
+    float scale;
+    unsigned long long wait_ns;
+};
+
+// A weight is 2^(s - m + kLift) for a score s and its row's reference maximum m (base 2); the reference moves once a weight
+// passes 2^kGrow.  So f16 weights are at most 2^14, and 2^6 or more for a row's largest.
+constexpr float kLift = 6.f, kGrow = 8.f + kLift;
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+// The power of two that brings a query row, whose largest magnitude has the bf16 bits mx, to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ void query_scale(uint32_t mx, float *up, float *down) {
+    const uint32_t e = max(mx >> 7, 15u);          // biased exponent, such that 2^(141 - e) is finite
+    *up = __uint_as_float((268u - e) << 23);       // 2^(141 - e)
+    *down = __uint_as_float((e - 14u) << 23);
+}
+
+// The items of at most kFewRows rows.  after: another kernel on this stream has the verify items, and is the one waited for
+// at the end.
+cudaError_t launch_attn_kv4_few(const Kv4Params &p, int D, bool after, int nsm, cudaStream_t st);
+
+}  // namespace pillar

@@ -69,7 +69,9 @@ struct WsHeader {
     int num_units;
     int num_merge;        // verify units whose partials the merge kernel combines (merge_units[0, num_merge))
     int num_merge_draft;  // draft units it combines (merge_units[num_units - num_merge_draft, num_units))
-    int pad[58];          // keeps the arrays 256-byte aligned
+    int num_verify_items; // items[0, num_verify_items) are those of verify requests
+    int draft_counter;    // a second queue, of the items behind them
+    int pad[56];          // keeps the arrays 256-byte aligned
 };
 
 // Byte offsets of the attention workspace sections.

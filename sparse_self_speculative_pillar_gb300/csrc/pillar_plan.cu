@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
     if (tid == 0) {
         p.hdr->err = 0;
         p.hdr->item_counter = 0;
+        p.hdr->draft_counter = 0;
     }
     int bad = 0;
     // When at most kRegChunks chunks cover every unit, each thread keeps its
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
     __syncthreads();
     if (tid == 0) {
         p.hdr->num_items = (int)(carry[4] + carry[5]);
+        p.hdr->num_verify_items = (int)carry[4];
         p.hdr->num_units = U;
         p.hdr->num_merge = (int)carry[7];
         p.hdr->num_merge_draft = s_mdraft;
