@@ -61,6 +61,31 @@ template <int N>
 __device__ __forceinline__ void copy_scales(uint32_t dst, const void *src, int bytes) {  // (zeros behind `bytes`)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
 }
+// Shared-memory loads at an address and a constant.
+template <int kOff>
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "n"(kOff));
+    return v;
+}
+template <int kOff>
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2+%3];" : "=r"(v.x), "=r"(v.y) : "r"(at), "n"(kOff));
+    return v;
+}
+template <int kOff>
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(at), "n"(kOff));
+    return v;
+}
+template <int kOff>
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1+%2];" : "=r"(v) : "r"(at), "n"(kOff));
+    return v;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -97,59 +122,95 @@ struct StateF {
     bool fresh;                        // a row has no reference yet
 };
 
+// Where a lane's parts of a piece lie, from the piece's first byte on.
+template <int D>
+struct PlaceF {
+    uint32_t k, ks, v, vs;
+    __device__ __forceinline__ PlaceF(int g, int c) {
+        using Pc = PieceF<D>;
+        k = D == 128 ? k_at<D>(2 * g, c) : k_at<D>(2 * g, c >> 1) + (c & 1) * 8;  // (row 2g + 1: ^ Pc::kRow)
+        v = 16 * Pc::kRow + (D == 128 ? v_at<D>(4 * c, g >> 1) + (g & 1) * 8 : v_at<D>(4 * c, g >> 2) + (g & 3) * 4);
+        ks = 32 * Pc::kRow + 2 * g * Pc::kScales + c * Pc::kScales / 4;
+        vs = 32 * Pc::kRow + 16 * Pc::kScales + 4 * c * Pc::kScales + g * Pc::kScales / 8;
+    }
+};
+
 // 16 keys: those of `vis`; all: every row sees them all; pos0: position of the first (verify); left: keys of the item from
 // it on; logits: where the logits of rows 2c and 2c + 1 at position 0 go, or null.
 template <int D>
-__device__ __forceinline__ void keys16(const PieceF<D> &pc, unsigned vis, bool all, int pos0, int left, float *const (&logits)[2],
-                                       StateF<D> &a) {
+__device__ __forceinline__ void keys16(uint32_t pc, const PlaceF<D> &at, unsigned vis, bool all, int pos0, int left,
+                                       float *const (&logits)[2], StateF<D> &a) {
     using Pc = PieceF<D>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     float s[4] = {0.f, 0.f, 0.f, 0.f};  // keys 2g (rows 2c, 2c + 1) and 2g + 1
     {
         constexpr int W = D / 32;  // words of a lane's part of a row
-        uint32_t x[2][W], sc[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint8_t *src = pc.k + (D == 128 ? k_at<D>(2 * g + e, c) : k_at<D>(2 * g + e, c >> 1) + (c & 1) * 8);
-            if (D == 128) {
-                const uint4 y = *reinterpret_cast<const uint4 *>(src);
-                x[e][0] = y.x, x[e][1] = y.y, x[e][W - 2] = y.z, x[e][W - 1] = y.w;
-                sc[e] = *reinterpret_cast<const uint16_t *>(pc.ks + (2 * g + e) * Pc::kScales + 2 * c);
-            } else {
-                const uint2 y = *reinterpret_cast<const uint2 *>(src);
-                x[e][0] = y.x, x[e][1] = y.y;
-                sc[e] = pc.ks[(2 * g + e) * Pc::kScales + c];
-            }
+        constexpr uint32_t kBoth = 0x00800080u;  // (a scale byte in bits 7 to 14 is its f16 value)
+        uint32_t x[2][W];
+        const uint32_t k0 = pc + at.k, k1 = pc + (at.k ^ Pc::kRow), ks = pc + at.ks;
+        if (D == 128) {
+            const uint4 y0 = lds128<0>(k0), y1 = lds128<0>(k1);
+            x[0][0] = y0.x, x[0][1] = y0.y, x[0][W - 2] = y0.z, x[0][W - 1] = y0.w;
+            x[1][0] = y1.x, x[1][1] = y1.y, x[1][W - 2] = y1.z, x[1][W - 1] = y1.w;
+        } else {
+            const uint2 y0 = lds64<0>(k0), y1 = lds64<0>(k1);
+            x[0][0] = y0.x, x[0][1] = y0.y, x[1][0] = y1.x, x[1][1] = y1.y;
+        }
+        uint32_t sc[2][2];
+        sc[0][0] = lds8<0>(ks) * kBoth;
+        sc[1][0] = lds8<Pc::kScales>(ks) * kBoth;
+        if (D == 128) {
+            sc[0][1] = lds8<1>(ks) * kBoth;
+            sc[1][1] = lds8<Pc::kScales + 1>(ks) * kBoth;
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             uint32_t h0[4], h1[4];
             f16_of_e2m1(x[0][i], h0);
             f16_of_e2m1(x[1][i], h1);
-            const uint32_t s0 = scale_pair(sc[0], i >> 1), s1 = scale_pair(sc[1], i >> 1);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h0[e] = mul_f16x2(h0[e], s0), h1[e] = mul_f16x2(h1[e], s1);
+            for (int e = 0; e < 4; ++e) h0[e] = mul_f16x2(h0[e], sc[0][i >> 1]), h1[e] = mul_f16x2(h1[e], sc[1][i >> 1]);
             mma16816(s, h0[0], h1[0], h0[1], h1[1], a.q[2 * i][0], a.q[2 * i][1]);
             mma16816(s, h0[2], h1[2], h0[3], h1[3], a.q[2 * i + 1][0], a.q[2 * i + 1][1]);
         }
     }
+    // V: this lane's D / 8 dimensions of keys 4c .. 4c + 3 (k = 2c, 2c + 8, 2c + 1, 2c + 9)
+    constexpr int W = D / 64;  // words per key
+    uint32_t x[4][W], s02, s13;
+    {
+        const uint32_t v0 = pc + at.v, vs = pc + at.vs;
+        if (D == 128) {
+            const uint32_t v1 = pc + (at.v ^ 64);
+            const uint2 y0 = lds64<0>(v0), y1 = lds64<0>(v1), y2 = lds64<128>(v0), y3 = lds64<128>(v1);
+            x[0][0] = y0.x, x[0][W - 1] = y0.y, x[1][0] = y1.x, x[1][W - 1] = y1.y;
+            x[2][0] = y2.x, x[2][W - 1] = y2.y, x[3][0] = y3.x, x[3][W - 1] = y3.y;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u][0] = lds32<0>(pc + (at.v ^ (32 * u)));
+        }
+        s02 = lds8<0>(vs) * 0x80u + lds8<2 * Pc::kScales>(vs) * 0x800000u;
+        s13 = lds8<Pc::kScales>(vs) * 0x80u + lds8<3 * Pc::kScales>(vs) * 0x800000u;
+    }
     if (!all) {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int key = 2 * g + (e >> 1);
             if (!((vis >> key) & 1) || pos0 + key > a.lim[e & 1]) s[e] = neg_inf();
         }
     }
+    if (logits[0] || logits[1]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (!logits[e]) continue;
-        float *dst = logits[e] + pos0 + 2 * g;  // eight lanes write 64 bytes of a row
-        const float y0 = s[e] * a.fac[e], y1 = s[e + 2] * a.fac[e];
-        if (2 * g + 2 <= left && !(reinterpret_cast<uintptr_t>(dst) & 7)) {
-            *reinterpret_cast<float2 *>(dst) = make_float2(y0, y1);
-        } else {
-            if (2 * g < left) dst[0] = y0;
-            if (2 * g + 1 < left) dst[1] = y1;
+        for (int e = 0; e < 2; ++e) {
+            if (!logits[e]) continue;
+            float *dst = logits[e] + pos0 + 2 * g;  // eight lanes write 64 bytes of a row
+            const float y0 = s[e] * a.fac[e], y1 = s[e + 2] * a.fac[e];
+            if (2 * g + 2 <= left && !(reinterpret_cast<uintptr_t>(dst) & 7)) {
+                *reinterpret_cast<float2 *>(dst) = make_float2(y0, y1);
+            } else {
+                if (2 * g < left) dst[0] = y0;
+                if (2 * g + 1 < left) dst[1] = y1;
+            }
         }
     }
     float w[4];
@@ -181,23 +242,6 @@ __device__ __forceinline__ void keys16(const PieceF<D> &pc, unsigned vis, bool a
     a.l[0] += w[0] + w[2];
     a.l[1] += w[1] + w[3];
     const uint32_t b0 = transpose8x8(pack_f16x2(w[0], w[1])), b1 = transpose8x8(pack_f16x2(w[2], w[3]));
-    // V: this lane's D / 8 dimensions of keys 4c .. 4c + 3 (k = 2c, 2c + 8, 2c + 1, 2c + 9)
-    constexpr int W = D / 64;  // words per key
-    uint32_t x[4][W], sc[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const uint8_t *src = pc.v + (D == 128 ? v_at<D>(4 * c + u, g >> 1) + (g & 1) * 8 : v_at<D>(4 * c + u, g >> 2) + (g & 3) * 4);
-        if (D == 128) {
-            const uint2 y = *reinterpret_cast<const uint2 *>(src);
-            x[u][0] = y.x, x[u][W - 1] = y.y;
-            sc[u] = pc.vs[(4 * c + u) * Pc::kScales + g];
-        } else {
-            x[u][0] = *reinterpret_cast<const uint32_t *>(src);
-            sc[u] = pc.vs[(4 * c + u) * Pc::kScales + (g >> 1)];
-        }
-    }
-    // (a scale byte in bits 7 to 14 is its f16 value)
-    const uint32_t s02 = sc[0] * 0x80u + sc[2] * 0x800000u, s13 = sc[1] * 0x80u + sc[3] * 0x800000u;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         constexpr uint32_t kLow = 0x0f0f0f0fu;
@@ -269,6 +313,7 @@ __global__ void __launch_bounds__(kThreadsF, kCtasF) attn_kv4_few_kernel(const _
     int base = 0;
     unsigned vis = 0;
     StateF<D> a;
+    const PlaceF<D> at(g, c);
     uint4 qx[D / 64][2];  // the next item's queries, on their way
     int qrow = -1;
     auto look_up = [&](const WorkF &w) {  // an item's rows and queries: loads only as far as they depend on none of the others
@@ -329,29 +374,39 @@ __global__ void __launch_bounds__(kThreadsF, kCtasF) attn_kv4_few_kernel(const _
         const bool verify = w.verify;
         const int n = w.n, rows = verify ? p.M : p.G;
         const int pieces = (n - warp * 16 + kWarpsF * 16 - 1) / (kWarpsF * 16);  // (0 or less: none)
+        constexpr uint32_t kBytes = sizeof(Pc);
         const uint32_t slots = smem_u32(sm.piece[warp]);
-        auto fetch = [&](int j) {
+        auto fetch = [&](int j, uint32_t dst) {
             if (j >= pieces) return;
-            const uint32_t dst = slots + (j % kSlotsF) * (uint32_t)sizeof(Pc);
-            const int first_row = __shfl_sync(0xffffffffu, base, j);
-            const unsigned there = __shfl_sync(0xffffffffu, vis, j);
             constexpr int RC = Pc::kRow / 16, RP = 32 / RC;  // 16-byte pieces of a row, rows of a pass
-            const int ch = lane % RC;
+            const unsigned there = __shfl_sync(0xffffffffu, vis, j);
+            const int r = lane / RC, ch = lane % RC, sr = lane & 15;
+            const uint32_t to_s = dst + 32 * Pc::kRow + lane * Pc::kScales, bytes = (there >> sr) & 1 ? Pc::kScales : 0;
+            const uint8_t *scales = lane < 16 ? p.c.k_scale : p.c.v_scale;
+            // (the codes of a key that is not there: any, its scales are 0)
+            if (verify) {
+                const int row = max(__shfl_sync(0xffffffffu, base, j), 0);
+                const size_t src = (size_t)(unsigned)row * Pc::kRow + lane * 16;
 #pragma unroll
-            for (int i = 0; i < 16 / RP; ++i) {
-                const int r = i * RP + lane / RC, row = max(verify ? first_row + r : sm.row[warp][j * 16 + r], 0);
-                const size_t src = (size_t)row * Pc::kRow + ch * 16;  // (of a key that is not there: any, its scales are 0)
-                copy16(dst + k_at<D>(r, ch), p.c.k4 + src);
-                copy16(dst + 16 * Pc::kRow + v_at<D>(r, ch), p.c.v4 + src);
+                for (int i = 0; i < 16 / RP; ++i) {
+                    copy16(dst + k_at<D>(i * RP + r, ch), p.c.k4 + src + i * 512);
+                    copy16(dst + 16 * Pc::kRow + v_at<D>(i * RP + r, ch), p.c.v4 + src + i * 512);
+                }
+                copy_scales<Pc::kScales>(to_s, scales + (size_t)(unsigned)(row + sr) * Pc::kScales, bytes);
+            } else {
+                const int *rows = sm.row[warp] + j * 16;
+#pragma unroll
+                for (int i = 0; i < 16 / RP; ++i) {
+                    const size_t src = (size_t)(unsigned)max(rows[i * RP + r], 0) * Pc::kRow + ch * 16;
+                    copy16(dst + k_at<D>(i * RP + r, ch), p.c.k4 + src);
+                    copy16(dst + 16 * Pc::kRow + v_at<D>(i * RP + r, ch), p.c.v4 + src);
+                }
+                copy_scales<Pc::kScales>(to_s, scales + (size_t)(unsigned)max(rows[sr], 0) * Pc::kScales, bytes);
             }
-            const int r = lane & 15, row = max(verify ? first_row + r : sm.row[warp][j * 16 + r], 0);
-            copy_scales<Pc::kScales>(dst + 32 * Pc::kRow + lane * Pc::kScales,
-                                     (lane < 16 ? p.c.k_scale : p.c.v_scale) + (size_t)row * Pc::kScales,
-                                     (there >> r) & 1 ? Pc::kScales : 0);
         };
 #pragma unroll
         for (int j = 0; j < kSlotsF - 1; ++j) {
-            fetch(j);
+            fetch(j, slots + j * kBytes);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         // the queries' operands
@@ -400,17 +455,20 @@ __global__ void __launch_bounds__(kThreadsF, kCtasF) attn_kv4_few_kernel(const _
             if (verify && p.logits && r < rows)
                 logits[e] = p.logits + w.logit_off + ((long long)(w.g * p.G + gi) * (p.k + 1) + j) * w.L;
         }
+        uint32_t here = slots, there_to = slots + (kSlotsF - 1) * kBytes;  // the slots of piece j, of the one fetched
 #pragma unroll 1
         for (int j = 0; j < pieces; ++j) {
             if (tid == 0 && j + 4 >= pieces && step < 3) advance();  // (not before it is needed: no item waits behind a long one)
-            fetch(j + kSlotsF - 1);
+            fetch(j + kSlotsF - 1, there_to);
             asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kSlotsF - 1) : "memory");
             __syncwarp();
             const int k0 = (warp + j * kWarpsF) * 16;
             const unsigned there = __shfl_sync(0xffffffffu, vis, j);
             const int pos0 = verify ? w.begin + k0 : 0;
-            keys16<D>(sm.piece[warp][j % kSlotsF], there, there == 0xffffu && (!verify || pos0 + 15 <= sure), pos0, n - k0, logits, a);
+            keys16<D>(here, at, there, there == 0xffffu && (!verify || pos0 + 15 <= sure), pos0, n - k0, logits, a);
             __syncwarp();
+            there_to = here;
+            here = here == slots + (kSlotsF - 1) * kBytes ? slots : here + kBytes;
         }
         // --- the item's rows: the warps' parts
         __syncthreads();  // (those of the item before have been read)
