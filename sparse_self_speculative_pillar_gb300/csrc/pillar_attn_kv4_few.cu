@@ -44,6 +44,12 @@ struct SmemF {
     PieceF<D> piece[kWarpsF][kSlotsF];
     float o[kWarpsF][8][D + 4], m[kWarpsF][8], l[kWarpsF][8];  // the warps' parts of an item's rows
     int row[kWarpsF][kPieces * 16];                            // lists: rows of the pools, or -1
+    struct alignas(16) {
+        Item item;
+        ReqInfo req;
+        UnitInfo unit;
+    } ahead;     // the next item's records
+    float *lb[8];  // where the logits of the item's rows at position 0 go, or null
     WorkF w[2];  // this item and the next, in turn
     int item;
 };
@@ -136,10 +142,10 @@ struct PlaceF {
 };
 
 // 16 keys: those of `vis`; all: every row sees them all; pos0: position of the first (verify); left: keys of the item from
-// it on; logits: where the logits of rows 2c and 2c + 1 at position 0 go, or null.
+// it on; logits: where the logits of rows 2c and 2c + 1 at position 0 go (each null for no such row), or null.
 template <int D>
 __device__ __forceinline__ void keys16(uint32_t pc, const PlaceF<D> &at, unsigned vis, bool all, int pos0, int left,
-                                       float *const (&logits)[2], StateF<D> &a) {
+                                       float *const *logits, StateF<D> &a) {
     using Pc = PieceF<D>;
     float s[4] = {0.f, 0.f, 0.f, 0.f};  // keys 2g (rows 2c, 2c + 1) and 2g + 1
     {
@@ -198,13 +204,14 @@ __device__ __forceinline__ void keys16(uint32_t pc, const PlaceF<D> &at, unsigne
             if (!((vis >> key) & 1) || pos0 + key > a.lim[e & 1]) s[e] = neg_inf();
         }
     }
-    if (logits[0] || logits[1]) {
+    if (logits) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            if (!logits[e]) continue;
-            float *dst = logits[e] + pos0 + 2 * g;  // eight lanes write 64 bytes of a row
-            const float y0 = s[e] * a.fac[e], y1 = s[e + 2] * a.fac[e];
+            float *dst = logits[e];
+            if (!dst) continue;
+            dst += pos0 + 2 * g;  // eight lanes write 64 bytes of a row
+            const float fac = e ? a.fac[1] : a.fac[0], y0 = (e ? s[1] : s[0]) * fac, y1 = (e ? s[3] : s[2]) * fac;
             if (2 * g + 2 <= left && !(reinterpret_cast<uintptr_t>(dst) & 7)) {
                 *reinterpret_cast<float2 *>(dst) = make_float2(y0, y1);
             } else {
@@ -273,38 +280,46 @@ __global__ void __launch_bounds__(kThreadsF, kCtasF) attn_kv4_few_kernel(const _
     int bad = 0;
     // thread 0 takes the next item one step at a time: its index, its record, the records that names
     int step = 0, next = 0;
-    int4 itm = make_int4(0, 0, 0, 0), rq = itm, un = itm;
     auto advance = [&]() {
         if (step == 0) {
             next = first + atomicAdd(fp.counter, 1);
         } else if (next < num_items) {
             if (step == 1) {
-                itm = __ldcg(reinterpret_cast<const int4 *>(p.items + next));
-            } else if (step == 2) {
-                rq = __ldcg(reinterpret_cast<const int4 *>(p.req + itm.x / p.Hkv));
-                un = __ldcg(reinterpret_cast<const int4 *>(p.unit + itm.x));
+                copy16(smem_u32(&sm.ahead.item), p.items + next);
+            } else if (step == 4) {  // (copies of this step come with the pieces of two steps on)
+                const int unit = sm.ahead.item.unit;
+                copy16(smem_u32(&sm.ahead.req), p.req + unit / p.Hkv);
+                copy16(smem_u32(&sm.ahead.unit), p.unit + unit);
             }
         }
         ++step;
     };
     static_assert(sizeof(Item) == 16 && sizeof(ReqInfo) == 16 && sizeof(UnitInfo) == 16, "records of 16 bytes");
+    static_assert(kSlotsF == 3, "a copy is there two steps later");
     auto open = [&](WorkF &w) {  // the next item's record, by thread 0
 #pragma unroll 1
-        while (step < 3) advance();
+        while (step < 5) {
+            if (step == 4) asm volatile("cp.async.wait_all;" ::: "memory");
+            advance();
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         step = 0;
         sm.item = next;
         if (next >= num_items) return;
-        w.b = itm.x / p.Hkv;
-        w.g = itm.x - w.b * p.Hkv;
-        w.begin = itm.y;
-        w.n = itm.z - itm.y;
-        w.q_off = rq.x;
-        w.vidx = rq.y;
-        w.L = rq.z;
-        w.verify = rq.w == 1;
-        w.nsplit = un.x;
-        w.rec = un.z + itm.w * un.w;
-        w.logit_off = w.verify ? __ldcg(p.logit_off + w.b) : 0;
+        const Item itm = sm.ahead.item;
+        const ReqInfo rq = sm.ahead.req;
+        const UnitInfo un = sm.ahead.unit;
+        w.b = itm.unit / p.Hkv;
+        w.g = itm.unit - w.b * p.Hkv;
+        w.begin = itm.begin;
+        w.n = itm.end - itm.begin;
+        w.q_off = rq.q_off;
+        w.vidx = rq.vidx;
+        w.L = rq.len;
+        w.verify = rq.mode == 1;
+        w.nsplit = un.nsplit;
+        w.rec = un.rec_base + itm.split * un.rec_rows;
+        w.logit_off = w.verify && p.logits ? __ldcg(p.logit_off + w.b) : 0;
     };
     if (tid == 0) open(sm.w[0]);
     __syncthreads();
@@ -447,25 +462,30 @@ __global__ void __launch_bounds__(kThreadsF, kCtasF) attn_kv4_few_kernel(const _
             a.fresh = true;
         }
         const int sure = verify ? w.L - (p.k + 1) : 0x7fffffff;  // every row sees up to here
-        float *logits[2] = {nullptr, nullptr};
+        const bool dump = verify && p.logits;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 2 * c + e, j = r / p.G, gi = r - j * p.G;
-            a.lim[e] = verify && r < rows ? sure + j : 0x7fffffff;
-            if (verify && p.logits && r < rows)
-                logits[e] = p.logits + w.logit_off + ((long long)(w.g * p.G + gi) * (p.k + 1) + j) * w.L;
+            const int r = 2 * c + e;
+            a.lim[e] = verify && r < rows ? sure + r / p.G : 0x7fffffff;
+        }
+        if (dump) {
+            if (tid < 8) {
+                const int j = tid / p.G, gi = tid - j * p.G;
+                sm.lb[tid] = tid < rows ? p.logits + w.logit_off + ((long long)(w.g * p.G + gi) * (p.k + 1) + j) * w.L : nullptr;
+            }
+            __syncthreads();
         }
         uint32_t here = slots, there_to = slots + (kSlotsF - 1) * kBytes;  // the slots of piece j, of the one fetched
 #pragma unroll 1
         for (int j = 0; j < pieces; ++j) {
-            if (tid == 0 && j + 4 >= pieces && step < 3) advance();  // (not before it is needed: no item waits behind a long one)
+            if (tid == 0 && j + 6 >= pieces && step < 5) advance();  // (not before it is needed: no item waits behind a long one)
             fetch(j + kSlotsF - 1, there_to);
             asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kSlotsF - 1) : "memory");
             __syncwarp();
             const int k0 = (warp + j * kWarpsF) * 16;
             const unsigned there = __shfl_sync(0xffffffffu, vis, j);
             const int pos0 = verify ? w.begin + k0 : 0;
-            keys16<D>(here, at, there, there == 0xffffu && (!verify || pos0 + 15 <= sure), pos0, n - k0, logits, a);
+            keys16<D>(here, at, there, there == 0xffffu && (!verify || pos0 + 15 <= sure), pos0, n - k0, dump ? sm.lb + 2 * c : nullptr, a);
             __syncwarp();
             there_to = here;
             here = here == slots + (kSlotsF - 1) * kBytes ? slots : here + kBytes;
