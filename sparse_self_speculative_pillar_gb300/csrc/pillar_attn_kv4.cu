@@ -70,7 +70,7 @@ struct Smem4 {
     // per query row: logit = sum * fac, in base-2 units sum * fac2; last position seen; its logits, or null
     alignas(16) float fac[kItems][kMaxRows], fac2[kItems][kMaxRows];
     int lim[kItems][kMaxRows];
-    float *lb[kItems][kMaxRows];
+    alignas(16) float *lb[kItems][kMaxRows];
     // per item (in turn) and row: kLift - reference maximum (base 2); sums of weights, by the keys' warp of a tile
     alignas(16) float nref[2][kMaxRows], sum[2][4][kMaxRows];
     float top[kGroups][4][16];                  // a group's largest scores, per warp
@@ -454,6 +454,8 @@ __device__ __forceinline__ float warp_max(float x) {  // (a NaN is passed over)
     return y;
 }
 
+// (Without a clobber of memory: the loads of the next row's place need not wait for it.)
+__device__ __forceinline__ void store_global(float *dst, float v) { asm volatile("st.global.f32 [%0], %1;" ::"l"(dst), "f"(v)); }
 __device__ __forceinline__ void load8(const float *src, float *v) {
     const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -608,7 +610,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp,
                         load8(sm.fac[is] + r0, f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (r0 + e < rows) sm.lb[is][r0 + e][pos] = s[ch][e] * f[e];
+                            if (r0 + e < rows) store_global(sm.lb[is][r0 + e] + pos, s[ch][e] * f[e]);
                     }
             }
         }
