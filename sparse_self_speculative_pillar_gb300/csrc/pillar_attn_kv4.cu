@@ -22,7 +22,7 @@
 //   * Four warps each for K and V copy the rows of the tiles ahead (16 bytes a
 //     lane), turn a key's codes into f16 and write them to tensor memory (K: lane
 //     = key) or swizzled shared memory (V: keys x D, MN-major).
-//   * One thread issues the products of S^T, another one those of O^T.
+//   * One warp issues the products of S^T, another one those of O^T.
 //   * Sixteen softmax warps, a key a thread, in four groups that share an item's
 //     rows, eight at a time.  A reference maximum moves only when a score passes it
 //     by more than 2^8, which a vote of the group finds out.
@@ -99,28 +99,25 @@ __device__ __forceinline__ bool wait4(uint64_t *bar, uint32_t parity, Smem4<D> &
         }
     return true;
 }
-// The same by one thread, of those that watch the clock.
+// The same for two barriers, by the warps that watch the clock.  (By the whole warp, too: one thread's tests of a barrier come back
+// at once, 40 cycles apart, and took a third of its scheduler's issue slots.)
 template <int D>
-__device__ __forceinline__ bool poll4(uint64_t *bar, uint32_t parity, Smem4<D> *sm, unsigned long long ns) {
-    const unsigned long long t0 = global_timer_ns();
+__device__ __forceinline__ bool watch4(uint64_t *bar, uint32_t parity, uint64_t *bar2, uint32_t parity2, Smem4<D> &sm,
+                                       unsigned long long ns) {
+    unsigned long long t0 = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (*static_cast<volatile int *>(&sm->abort) || global_timer_ns() - t0 > ns) {
-            *static_cast<volatile int *>(&sm->abort) = 1;
+    for (;;) {
+        const bool one = mbar_try_wait(bar, parity), two = mbar_try_wait(bar2, parity2);  // (the tests' latencies overlap)
+        if (__all_sync(0xffffffffu, one && two)) return true;
+        const unsigned long long now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort) | (now - t0 > ns))) {
+            sm.abort = 1;
             return false;
         }
-    return true;
+    }
 }
-template <int D>
-__device__ __forceinline__ bool watch4(uint64_t *bar, uint32_t parity, Smem4<D> &sm, unsigned long long ns) {
-    return poll4(bar, parity, &sm, ns);
-}
-template <int D>
-__device__ __forceinline__ bool watch4_two(uint64_t *bar, uint32_t parity, uint64_t *bar2, uint32_t parity2, Smem4<D> &sm,
-                                           unsigned long long ns) {
-    const bool one = mbar_try_wait(bar, parity), two = mbar_try_wait(bar2, parity2);  // (the tests' latencies overlap)
-    return (one && two) || (poll4(bar, parity, &sm, ns) && poll4(bar2, parity2, &sm, ns));
-}
+
 __device__ __forceinline__ void arrive_lane0(uint64_t *bar, uint32_t count = 1) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive_cnt(bar, count);
@@ -366,8 +363,8 @@ __device__ __forceinline__ void drain4(Smem4<D> &sm, int which) {
         if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
 }
 
-// S^T of every tile, by one thread.  (The products of a tile take 250 and 440 cycles, O^T's waiting for its operands in shared
-// memory; one thread for both, with the tests of its waits between them, took 1900 a tile.)
+// S^T of every tile.  (The products of a tile take 250 and 440 cycles, O^T's waiting for its operands in shared memory; one warp
+// for both, with the tests of its waits between them, took 1900 a tile.)
 template <int D>
 __device__ void scores4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
     const uint32_t id = kId4 | ((uint32_t)(p.M + 15) / 16 << 18);
@@ -375,12 +372,12 @@ __device__ void scores4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems;
-        if (!watch4(&sm.item_full[is], i / kItems & 1, sm, p.wait_ns)) break;
-        const ItemRec &rec = sm.item[is];
-        const int tiles = rec.tiles;
-        if (rec.stop) break;
-        mbar_arrive(&sm.item_empty[is]);
-        if (!watch4(&sm.q_full[i & 1], i >> 1 & 1, sm, p.wait_ns)) break;
+        if (!watch4(&sm.item_full[is], i / kItems & 1, &sm.item_full[is], i / kItems & 1, sm, p.wait_ns)) break;
+        // (a reduction leaves its result in a uniform register, as the products' operands have to be)
+        const int tiles = __reduce_or_sync(0xffffffffu, (unsigned)(sm.item[is].stop ? 0 : sm.item[is].tiles));
+        if (tiles == 0) break;
+        arrive_lane0(&sm.item_empty[is]);
+        if (!watch4(&sm.q_full[i & 1], i >> 1 & 1, &sm.q_full[i & 1], i >> 1 & 1, sm, p.wait_ns)) break;
         const uint64_t dq = umma_sdesc_sw128(smem_u32(sm.q[i & 1]), 16, 1024);
         int t = 0;
 #pragma unroll 1
@@ -388,21 +385,25 @@ __device__ void scores4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
             const int b = x & 1;
             const uint32_t ph = x >> 1 & 1;
             // (the scores of the tile before last have been read: its P is there)
-            if (!watch4_two(&sm.k_full[b], ph, &sm.p_full[b], ph ^ 1, sm, p.wait_ns)) break;
+            if (!watch4(&sm.k_full[b], ph, &sm.p_full[b], ph ^ 1, sm, p.wait_ns)) break;
             tc_fence_after();
+            if (elect_one4()) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                umma_bf16_ts(tm + kTmemS + b * 64, tm + kTmemK + b * 64 + ks * 8,
-                             dq + (uint64_t)((ks >> 2) * (kMaxRows * 128 / 16) + (ks & 3) * 2), id, ks > 0 ? 1u : 0u);
-            umma_commit(&sm.s_full[b]);
+                for (int ks = 0; ks < D / 16; ++ks)
+                    umma_bf16_ts(tm + kTmemS + b * 64, tm + kTmemK + b * 64 + ks * 8,
+                                 dq + (uint64_t)((ks >> 2) * (kMaxRows * 128 / 16) + (ks & 3) * 2), id, ks > 0 ? 1u : 0u);
+                umma_commit(&sm.s_full[b]);
+                if (t + 1 == tiles) umma_commit(&sm.q_empty[i & 1]);
+            }
+            __syncwarp();
         }
         if (t < tiles) break;
-        umma_commit(&sm.q_empty[i & 1]);
     }
-    if (x > 0) drain4(sm, 0);
+    if (x > 0 && elect_one4()) drain4(sm, 0);
+    __syncwarp();
 }
 
-// O^T of every tile, by one thread.
+// O^T of every tile.
 template <int D>
 __device__ void outputs4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
     const uint32_t id = kId4 | (1u << 15) | (1u << 16) | ((uint32_t)(p.M + 15) / 16 << 18);
@@ -410,31 +411,34 @@ __device__ void outputs4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int is = i % kItems;
-        if (!watch4(&sm.item_full[is], i / kItems & 1, sm, p.wait_ns)) break;
-        const ItemRec &rec = sm.item[is];
-        const int tiles = rec.tiles;
-        if (rec.stop) break;
-        mbar_arrive(&sm.item_empty[is]);
-        if (!watch4(&sm.o_empty[i & 1], (i >> 1 & 1) ^ 1, sm, p.wait_ns)) break;
+        if (!watch4(&sm.item_full[is], i / kItems & 1, &sm.item_full[is], i / kItems & 1, sm, p.wait_ns)) break;
+        const int tiles = __reduce_or_sync(0xffffffffu, (unsigned)(sm.item[is].stop ? 0 : sm.item[is].tiles));
+        if (tiles == 0) break;
+        arrive_lane0(&sm.item_empty[is]);
+        if (!watch4(&sm.o_empty[i & 1], (i >> 1 & 1) ^ 1, &sm.o_empty[i & 1], (i >> 1 & 1) ^ 1, sm, p.wait_ns)) break;
         int t = 0;
 #pragma unroll 1
         for (; t < tiles; ++t, ++x) {
             const int b = x & 1;
             const uint32_t ph = x >> 1 & 1;
-            if (!watch4_two(&sm.v_full[b], ph, &sm.p_full[b], ph, sm, p.wait_ns)) break;
+            if (!watch4(&sm.v_full[b], ph, &sm.p_full[b], ph, sm, p.wait_ns)) break;
             tc_fence_after();
-            // V: M (dimensions) in halves of 64; for D = 64 the second half is whatever follows, and nobody reads its O
-            const uint64_t dv = umma_sdesc_sw128(smem_u32(sm.v[b]), kTile * 128, 1024), dp = p_desc(smem_u32(sm.p[b]));
-            const uint32_t to = tm + kTmemO + (i & 1) * 64, add = t > 0;
+            if (elect_one4()) {
+                // V: M (dimensions) in halves of 64; for D = 64 the second half is whatever follows, and nobody reads its O
+                const uint64_t dv = umma_sdesc_sw128(smem_u32(sm.v[b]), kTile * 128, 1024), dp = p_desc(smem_u32(sm.p[b]));
+                const uint32_t to = tm + kTmemO + (i & 1) * 64, add = t > 0;
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-                umma_bf16(to, dv + (uint64_t)(ks * 128), dp + (uint64_t)(ks * 32), id, ks > 0 ? 1u : add);
-            umma_commit(&sm.pv_done[b]);
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    umma_bf16(to, dv + (uint64_t)(ks * 128), dp + (uint64_t)(ks * 32), id, ks > 0 ? 1u : add);
+                umma_commit(&sm.pv_done[b]);
+                if (t + 1 == tiles) umma_commit(&sm.o_full[i & 1]);
+            }
+            __syncwarp();
         }
         if (t < tiles) break;
-        umma_commit(&sm.o_full[i & 1]);
     }
-    if (x > 0) drain4(sm, 1);
+    if (x > 0 && elect_one4()) drain4(sm, 1);
+    __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax warps
@@ -771,7 +775,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attn_kv4_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sm.item_full[i], 1);
-            mbar_init(&sm.item_empty[i], 4 * kGroups + 4 + 1 + 2);  // softmax, epilogue and query warps, the products' threads
+            mbar_init(&sm.item_empty[i], 4 * kGroups + 4 + 1 + 2);  // softmax, epilogue and query warps, the products' warps
             mbar_init(&sm.fac_full[i], 1);
         }
         for (int i = 0; i < kChunks; ++i) {
@@ -812,11 +816,8 @@ __global__ void __launch_bounds__(kThreads4, 1) attn_kv4_kernel(const __grid_con
     } else if (wg == kGroups + 2) {
         if (w == 0) resolver4<D>(p, sm, lane);
         else if (w == 3) queries4<D>(p, sm, lane);
-        else if (elect_one4()) {
-            if (w == 1) scores4<D>(p, sm, tm);
-            else outputs4<D>(p, sm, tm);
-        }
-        __syncwarp();
+        else if (w == 1) scores4<D>(p, sm, tm);
+        else outputs4<D>(p, sm, tm);
     } else {
         epilogue4<D>(p, sm, tm, w, lane);
     }
