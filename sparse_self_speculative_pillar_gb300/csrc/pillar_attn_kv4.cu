@@ -10,7 +10,7 @@
 // magnitude brought to [2^14, 2^15)), but for elements 2^-28 below that.  So
 // both products take f16 operands and the scores are sums of exact products.
 //
-// Here are the verify items of more than eight rows; pillar_attn_kv4_few.cu has
+// Here are the verify items of more than sixteen rows; pillar_attn_kv4_few.cu has
 // the others.  One persistent CTA an SM, 128 keys a tile, the keys on the M of
 // tcgen05:
 //     S^T [keys x rows] = K Q^T      K from tensor memory, Q from shared memory
@@ -888,12 +888,16 @@ cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaS
     p.max_sparse = a.max_sparse;
     p.scale = a.scale;
     p.wait_ns = a.wait_ns;
-    // Verify items of more than eight rows and then the others, whose CTAs take the place of the first ones as these end.
-    const bool many = p.M > kFewRows && a.schedule != PILLAR_SCHEDULE_DRAFT_ONLY;
+    // All items have at most eight rows, or those of verify requests go first, in a kernel whose CTAs the others take the place
+    // of as these end.
     cudaError_t e = cudaSuccess;
-    if (many) e = a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
-    if (e == cudaSuccess && (!many || a.schedule != PILLAR_SCHEDULE_VERIFY_ONLY))
-        e = launch_attn_kv4_few(p, a.D, many, nsm, st);
+    if (p.M <= 8 || a.schedule == PILLAR_SCHEDULE_DRAFT_ONLY) {
+        e = launch_attn_kv4_few(p, a.D, 8, 0, false, nsm, st);
+    } else {
+        e = p.M <= kFewRows ? launch_attn_kv4_few(p, a.D, p.M, 1, false, nsm, st)
+                            : a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
+        if (e == cudaSuccess && a.schedule != PILLAR_SCHEDULE_VERIFY_ONLY) e = launch_attn_kv4_few(p, a.D, 8, 2, true, nsm, st);
+    }
     return e == cudaSuccess ? launch_merge(a, nsm, st) : e;
 }
 

@@ -1,4 +1,4 @@
-// pillar_attn_kv4.cuh -- what the two kernels of the 4-bit attention share: items of at most eight query rows
+// pillar_attn_kv4.cuh -- what the two kernels of the 4-bit attention share: items of at most sixteen query rows
 // (pillar_attn_kv4_few.cu) and the others (pillar_attn_kv4.cu).
 #pragma once
 
@@ -6,7 +6,7 @@
 
 namespace pillar {
 
-constexpr int kFewRows = 8;
+constexpr int kFewRows = 16;
 
 struct Kv4Params {
     const uint16_t *q;
@@ -42,8 +42,8 @@ __device__ __forceinline__ void query_scale(uint32_t mx, float *up, float *down)
     *down = __uint_as_float((e - 14u) << 23);
 }
 
-// The items of at most kFewRows rows.  after: another kernel on this stream has the verify items, and is the one waited for
-// at the end.
-cudaError_t launch_attn_kv4_few(const Kv4Params &p, int D, bool after, int nsm, cudaStream_t st);
+// The items of part 0 (all), 1 (of verify requests) or 2 (the others), of `rows` <= kFewRows rows at most.  after: another
+// kernel on this stream has the verify items, and is the one waited for at the end.
+cudaError_t launch_attn_kv4_few(const Kv4Params &p, int D, int rows, int part, bool after, int nsm, cudaStream_t st);
 
 }  // namespace pillar
