@@ -21,11 +21,11 @@ namespace pillar {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kCtas = 2;   // CTAs of an SM
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kCtas = 4;   // CTAs of an SM
 constexpr int kSlots = 3;  // 16-key pieces of a warp: one being read, two on their way
 constexpr int kPieces = kMaxChunk / 16 / kWarps;  // of a warp in an item, at most
-static_assert(kPieces <= 16, "a lane keeps what it knows of a piece, lists fill 16");
+static_assert(kPieces <= 32, "a lane keeps what it knows of a piece");
 
 template <int D>
 struct Piece4 {
@@ -45,11 +45,11 @@ struct Smem4 {
     static constexpr int kRows = 8 * NT;
     Piece4<D> piece[kWarps][kSlots];
     float o[kWarps][8][D + 4], m[kWarps][8], l[kWarps][8];  // the warps' parts of a row tile
-    uint2 q[NT][D / 16][32];                                // query operands: row tile, step, lane (two row tiles)
+    uint2 q[NT][NT == 1 ? 1 : D / 16][32];                  // two row tiles: query operands by row tile, step, lane
     alignas(8) float fac[kRows], fac2[kRows];               // per row: logit = sum * fac, fac2 in base 2
     int lim[kRows];                                         // last position seen
     float *lb[kRows];                                       // where its logits at position 0 go, or null
-    int row[kWarps][kPieces * 16];                          // lists: rows of the pools, or -1
+    int row[kWarps][NT == 1 ? kPieces * 16 : 1];            // lists (of one row tile): rows of the pools, or -1
     struct alignas(16) {
         Item item;
         ReqInfo req;
@@ -183,7 +183,7 @@ __device__ __forceinline__ void keys16(const Smem4<D, NT> &sm, uint32_t pc, cons
             sc[0][1] = lds8<1>(ks) * kBoth;
             sc[1][1] = lds8<Pc::kScales + 1>(ks) * kBoth;
         }
-        const uint2 *q = &sm.q[0][0][lane];
+        const uint2 *q = &sm.q[0][0][lane];  // (two row tiles)
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             uint32_t h0[4], h1[4];
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
         }
         const int *table = p.c.table + (size_t)w.b * p.c.max_blocks;
         vis = 0;
-        if (w.verify) {  // (items begin at multiples of 64: a piece is a block)
+        if (NT > 1 || w.verify) {  // (items begin at multiples of 64: a piece is a block)
             const int k = (warp + lane * kWarps) * 16, pos = (w.begin + k) / PILLAR_KV_BLOCK;
             base = -1;
             if (lane < kPieces && k < w.n) {
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
         const uint32_t to_s = dst + 32 * Pc::kRow + lane * Pc::kScales, bytes = (there >> sr) & 1 ? Pc::kScales : 0;
         const uint8_t *scales = lane < 16 ? p.c.k_scale : p.c.v_scale;
         // (the codes of a key that is not there: any, its scales are 0)
-        if (verify) {
+        if (NT > 1 || verify) {
             const int row = max(__shfl_sync(0xffffffffu, base, j), 0);
             const size_t src = (size_t)(unsigned)row * Pc::kRow + lane * 16;
 #pragma unroll
