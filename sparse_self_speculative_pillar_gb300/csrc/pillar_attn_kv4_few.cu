@@ -372,8 +372,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
     __syncthreads();
     // Of its pieces of the item (warp, warp + 8, ..) a lane keeps the first row of piece `lane` (contexts) and which of its keys
     // there are; lists have their rows in shared memory.
-    int base = 0;
-    unsigned vis = 0;
+    unsigned base = 0, vis = 0;
     State4<D, NT> a;
     const Place4<D> at(g, c);
     uint4 qx[D / 64][2];  // the next item's queries, on their way: row tile `warp` (row tile 0, one only)
@@ -391,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
         vis = 0;
         if (NT > 1 || w.verify) {  // (items begin at multiples of 64: a piece is a block)
             const int k = (warp + lane * kWarps) * 16, pos = (w.begin + k) / PILLAR_KV_BLOCK;
-            base = -1;
+            base = 0;
             if (lane < kPieces && k < w.n) {
                 const int blk = pos < p.c.max_blocks ? __ldg(table + pos) : -1;
                 if (blk >= 0 && blk < p.c.num_blocks) {
@@ -432,32 +431,34 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
     };
     constexpr uint32_t kBytes = sizeof(Pc);
     const uint32_t slots = smem_u32(sm.piece[warp]);
+    // A lane copies 16 bytes of rows r and r + RP .. of a piece, K's and V's, and the scales of one key of either.
+    constexpr int RC = Pc::kRow / 16, RP = 32 / RC;  // 16-byte pieces of a row, rows of a pass
+    const int cr = lane / RC, ch = lane % RC, sr = lane & 15;
+    const uint8_t *const k_from = p.c.k4 + lane * 16, *const v_from = p.c.v4 + lane * 16;
+    const uint8_t *const s_from = (lane < 16 ? p.c.k_scale : p.c.v_scale) + sr * Pc::kScales;
+    const uint32_t s_to = 32 * Pc::kRow + lane * Pc::kScales;
     auto fetch = [&](int j, int pieces, bool verify, uint32_t dst) {
         if (j >= pieces) return;
-        constexpr int RC = Pc::kRow / 16, RP = 32 / RC;  // 16-byte pieces of a row, rows of a pass
-        const unsigned there = __shfl_sync(0xffffffffu, vis, j);
-        const int r = lane / RC, ch = lane % RC, sr = lane & 15;
-        const uint32_t to_s = dst + 32 * Pc::kRow + lane * Pc::kScales, bytes = (there >> sr) & 1 ? Pc::kScales : 0;
-        const uint8_t *scales = lane < 16 ? p.c.k_scale : p.c.v_scale;
+        const uint32_t bytes = (__shfl_sync(0xffffffffu, vis, j) >> sr & 1) * Pc::kScales;
         // (the codes of a key that is not there: any, its scales are 0)
         if (NT > 1 || verify) {
-            const int row = max(__shfl_sync(0xffffffffu, base, j), 0);
-            const size_t src = (size_t)(unsigned)row * Pc::kRow + lane * 16;
+            const uint32_t row = __shfl_sync(0xffffffffu, base, j);
+            const uint8_t *k = k_from + (size_t)row * Pc::kRow, *v = v_from + (size_t)row * Pc::kRow;
 #pragma unroll
             for (int i = 0; i < 16 / RP; ++i) {
-                copy16(dst + k_at<D>(i * RP + r, ch), p.c.k4 + src + i * 512);
-                copy16(dst + 16 * Pc::kRow + v_at<D>(i * RP + r, ch), p.c.v4 + src + i * 512);
+                copy16(dst + k_at<D>(i * RP + cr, ch), k + i * 512);
+                copy16(dst + 16 * Pc::kRow + v_at<D>(i * RP + cr, ch), v + i * 512);
             }
-            copy_scales<Pc::kScales>(to_s, scales + (size_t)(unsigned)(row + sr) * Pc::kScales, bytes);
+            copy_scales<Pc::kScales>(dst + s_to, s_from + (size_t)row * Pc::kScales, bytes);
         } else {
             const int *rows = sm.row[warp] + j * 16;
 #pragma unroll
             for (int i = 0; i < 16 / RP; ++i) {
-                const size_t src = (size_t)(unsigned)max(rows[i * RP + r], 0) * Pc::kRow + ch * 16;
-                copy16(dst + k_at<D>(i * RP + r, ch), p.c.k4 + src);
-                copy16(dst + 16 * Pc::kRow + v_at<D>(i * RP + r, ch), p.c.v4 + src);
+                const size_t src = (size_t)(unsigned)max(rows[i * RP + cr], 0) * Pc::kRow + ch * 16;
+                copy16(dst + k_at<D>(i * RP + cr, ch), p.c.k4 + src);
+                copy16(dst + 16 * Pc::kRow + v_at<D>(i * RP + cr, ch), p.c.v4 + src);
             }
-            copy_scales<Pc::kScales>(to_s, scales + (size_t)(unsigned)max(rows[sr], 0) * Pc::kScales, bytes);
+            copy_scales<Pc::kScales>(dst + s_to, (lane < 16 ? p.c.k_scale : p.c.v_scale) + (size_t)(unsigned)max(rows[sr], 0) * Pc::kScales, bytes);
         }
     };
     auto pieces_of = [&](const Work4 &w) { return (w.n - warp * 16 + kWarps * 16 - 1) / (kWarps * 16); };  // (0 or less: none)
