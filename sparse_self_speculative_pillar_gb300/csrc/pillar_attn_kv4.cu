@@ -23,9 +23,10 @@
 //     lane), turn a key's codes into f16 and write them to tensor memory (K: lane
 //     = key) or swizzled shared memory (V: keys x D, MN-major).
 //   * One warp issues the products of S^T, another one those of O^T.
-//   * Sixteen softmax warps, a key a thread, in four groups that share an item's
-//     rows, eight at a time.  A reference maximum moves only when a score passes it
-//     by more than 2^8, which a vote of the group finds out.
+//   * Sixteen softmax warps, a key a thread: two sets that take tiles in turn, each
+//     with an O and reference maxima of its own, of two groups that share the rows,
+//     eight at a time.  A reference maximum moves only when a score passes it by
+//     more than 2^8, which a vote of the group finds out.
 //   * Four warps write finished items, one stages queries.
 #include "pillar_attn_kv4.cuh"
 
@@ -40,11 +41,11 @@ constexpr int kChunkKeys = kTile * kChunkTiles;
 // tile x.  With items of one tile, each a chunk, those are free once the softmax warps have come to tile x + 4 - kChunks, and
 // to tile x they come without these: kChunks >= 4.
 constexpr int kChunks = 5;
-constexpr int kItems = 8;                    // items in flight
+constexpr int kItems = 6;                    // items in flight (tile x + 4 may belong to item i + 4: as for kChunks, at least 5)
 constexpr int kStages = 4;                   // tiles of codes in shared memory
 constexpr int kWarps = 32, kGroups = 4;       // groups of softmax warps
 constexpr int kThreads4 = kWarps * 32;
-// tensor memory: two tiles of K, two of S^T, the O^T of two items, sums of weights (a key's lane, a column per row)
+// tensor memory: two tiles of K, two of S^T, the O^T of each set, sums of weights (a key's lane, a column per row) of each set
 constexpr uint32_t kTmemCols = 512, kTmemK = 0, kTmemS = 128, kTmemO = 256, kTmemL = 384;
 
 // A work item in shared memory.
@@ -71,9 +72,9 @@ struct Smem4 {
     alignas(16) float fac[kItems][kMaxRows], fac2[kItems][kMaxRows];
     int lim[kItems][kMaxRows];
     alignas(16) float *lb[kItems][kMaxRows];
-    // per item (in turn) and row: kLift - reference maximum (base 2); sums of weights, by the keys' warp of a tile
-    alignas(16) float nref[2][kMaxRows], sum[2][4][kMaxRows];
-    float top[kGroups][4][16];                  // a group's largest scores, per warp
+    // per item (in turn), set and row: kLift - reference maximum (base 2); sums of weights, by the keys' warp of a tile
+    alignas(16) float nref[2][2][kMaxRows], sum[2][2][4][kMaxRows];
+    float top[kGroups][4][32];                  // a group's largest scores, per warp
     uint64_t item_full[kItems], item_empty[kItems], fac_full[kItems];
     uint64_t rows_full[kChunks], rows_empty[kChunks];
     uint64_t q_full[2], q_empty[2], k_full[2], s_full[2], p_full[2], v_full[2], pv_done[2];
@@ -161,8 +162,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The chunks of eight rows are dealt out to the softmax groups: group g has chunks g and g + kGroups.
-static_assert(kMaxRows == 16 * kGroups, "two chunks of eight rows a group, at most");
+// The rows' chunks of eight are dealt out to the two groups of a softmax set: group h has chunks h, h + 2, ..
+static_assert(kMaxRows == 64 && kGroups == 4, "four chunks of eight rows a group, at most: a lane a row");
 
 // ------------------------------------------------------------------ resolver warp
 
@@ -415,7 +416,8 @@ __device__ void outputs4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
         const int tiles = __reduce_or_sync(0xffffffffu, (unsigned)(sm.item[is].stop ? 0 : sm.item[is].tiles));
         if (tiles == 0) break;
         arrive_lane0(&sm.item_empty[is]);
-        if (!watch4(&sm.o_empty[i & 1], (i >> 1 & 1) ^ 1, &sm.o_empty[i & 1], (i >> 1 & 1) ^ 1, sm, p.wait_ns)) break;
+        // (the item before has been written: O is not kept twice)
+        if (i > 0 && !watch4(&sm.o_empty[(i & 1) ^ 1], (i - 1) >> 1 & 1, &sm.o_empty[(i & 1) ^ 1], (i - 1) >> 1 & 1, sm, p.wait_ns)) break;
         int t = 0;
 #pragma unroll 1
         for (; t < tiles; ++t, ++x) {
@@ -426,7 +428,7 @@ __device__ void outputs4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm) {
             if (elect_one4()) {
                 // V: M (dimensions) in halves of 64; for D = 64 the second half is whatever follows, and nobody reads its O
                 const uint64_t dv = umma_sdesc_sw128(smem_u32(sm.v[b]), kTile * 128, 1024), dp = p_desc(smem_u32(sm.p[b]));
-                const uint32_t to = tm + kTmemO + (i & 1) * 64, add = t > 0;
+                const uint32_t to = tm + kTmemO + b * 64, add = t > 1;
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks)
                     umma_bf16(to, dv + (uint64_t)(ks * 128), dp + (uint64_t)(ks * 32), id, ks > 0 ? 1u : add);
@@ -465,15 +467,28 @@ __device__ __forceinline__ void load8(const float *src, float *v) {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// A group's rows are those of chunks grp and grp + kGroups; what the roles share is indexed by row.
+// Eight rows' scores of a thread's key, with those that do not count at -inf.
+struct Key4 {
+    bool there, part;  // there is such a key; some row does not see it
+    int pos;
+};
+__device__ __forceinline__ void scores8(uint32_t taddr, const Key4 &k, const int *lim, float (&s)[8]) {
+    tmem_ld8(taddr, s);
+    tmem_wait_ld();
+    if (k.part) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (!k.there || k.pos > lim[e]) s[e] = neg_inf();
+    }
+}
+
+// Group `half` of set `set`; its chunk ch is rows [8 half + 16 ch, + 8).
 template <int D>
 __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp, int w, int lane) {
-    const int key = 32 * w + lane;
-    const uint32_t quad = tm + ((uint32_t)w << 21);
-    const int rows = p.M, nch = ((rows + 7) / 8 - grp + kGroups - 1) / kGroups;  // (0: this group only keeps step)
-    // `lane` (below 16) looks after row 8 (grp + kGroups * (lane / 8)) + lane % 8
-    const int mine = 8 * (grp + kGroups * (lane >> 3)) + (lane & 7);
-    const uint32_t tl = quad + kTmemL + 8 * grp;  // (sums of weights; the second chunk 32 columns on)
+    const int key = 32 * w + lane, set = grp >> 1, half = grp & 1;
+    const uint32_t quad = tm + ((uint32_t)w << 21) + set * 64 + half * 8;
+    const int rows = p.M, nch = ((rows + 7) / 8 - half + 1) / 2;
+    const int mine = 8 * half + 16 * (lane >> 3) + (lane & 7);  // the row that this lane looks after
     uint32_t x = 0;  // tile
     int slot = 0;    // of the chunk
     uint32_t phase = 0;
@@ -489,85 +504,76 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp,
         const int sure = rec.L - (p.k + 1);               // every row sees up to here
         dead |= !wait4(&sm.fac_full[is], i / kItems & 1, sm);
         dead |= !wait4(&sm.epi_empty[sl], (i >> 1 & 1) ^ 1, sm);
-        const float *fac2 = sm.fac2[is] + 8 * grp;
-        float *nref = sm.nref[sl] + 8 * grp;
-        const uint32_t to = quad + kTmemO + sl * 64 + 8 * grp;
+        const float *fac2 = sm.fac2[is] + 8 * half;
+        const int *lim = sm.lim[is] + 8 * half;
+        float *nref = sm.nref[sl][set] + 8 * half;
         float m = neg_inf();  // the reference maximum of row `mine`, in every warp
-        bool fresh = nch > 0, first = true;  // some row has none yet; nothing has been added to O
+        bool fresh = true, first = true;  // some row has none yet; nothing has been added to O
         {
             const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            tmem_st8(tl, zero);
-            tmem_st8(tl + 32, zero);
-            tmem_wait_st();
-        }
-        int pos = rec.begin + key;
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t, ++x, pos += kTile) {
+            for (int ch = 0; ch < nch; ++ch) tmem_st8(quad + kTmemL + 16 * ch, zero);
+            tmem_wait_st();
+            if (w == 0 && mine < kMaxRows) sm.nref[sl][set][mine] = kLift;
+        }
+        Key4 kk;
+        kk.pos = rec.begin + key;
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t, ++x, kk.pos += kTile) {
             if (t % kChunkTiles == 0) dead |= !wait4(&sm.rows_full[slot], phase, sm);
-            const bool there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
+            kk.there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
             if (t % kChunkTiles == kChunkTiles - 1 || t == tiles - 1) {
                 arrive_lane0(&sm.rows_empty[slot]);
                 if (++slot == kChunks) slot = 0, phase ^= 1;
             }
-            const int b = x & 1;
-            const uint32_t ph = x >> 1 & 1, ts = quad + kTmemS + b * 64 + 8 * grp;
-            dead |= !wait4(&sm.s_full[b], ph, sm);
+            if ((x & 1) != set) continue;
+            const uint32_t ph = x >> 1 & 1;
+            kk.part = !kk.there || kk.pos > sure;
+            dead |= !wait4(&sm.s_full[set], ph, sm);
             tc_fence_after();
-            float s[2][8];
-            if (nch > 0) tmem_ld8(ts, s[0]);
-            if (nch > 1) tmem_ld8(ts + 32, s[1]);
-            tmem_wait_ld();
-            if (!there || pos > sure) {
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!there || pos > sm.lim[is][8 * (grp + kGroups * ch) + e]) s[ch][e] = neg_inf();
-            }
             float most = neg_inf();
+#pragma unroll 1
+            for (int ch = 0; ch < nch; ++ch) {
+                float s[8], f[8], r[8];
+                load8(fac2 + 16 * ch, f);
+                load8(nref + 16 * ch, r);
+                scores8(quad + kTmemS + 16 * ch, kk, lim + 16 * ch, s);
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-                if (ch < nch) {
-                    float f[8], r[8];
-                    load8(fac2 + ch * 32, f);
-                    load8(nref + ch * 32, r);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaf(s[ch][e], f[e], r[e]));
-                }
+                for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaf(s[e], f[e], r[e]));
+            }
             if (group_any(grp, most > kGrow || fresh || dead)) {  // rare: new reference maxima
                 if (group_any(grp, dead)) return;
                 float mx = neg_inf();
+#pragma unroll 1
+                for (int ch = 0; ch < nch; ++ch) {
+                    float s[8], f[8];
+                    load8(fac2 + 16 * ch, f);
+                    scores8(quad + kTmemS + 16 * ch, kk, lim + 16 * ch, s);
 #pragma unroll
-                for (int ch = 0; ch < 2; ++ch)
-                    if (ch < nch) {
-                        float f[8];
-                        load8(fac2 + ch * 32, f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float y = warp_max(s[ch][e] * f[e]);
-                            if (lane == ch * 8 + e) mx = y;
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = warp_max(s[e] * f[e]);
+                        if (lane == ch * 8 + e) mx = y;
                     }
-                if (lane < 16) sm.top[grp][w][lane] = mx;
+                }
+                sm.top[grp][w][lane] = mx;
                 if (!first) {  // what has been added to O so far is done: its rows are scaled below
-                    dead |= !wait4(&sm.pv_done[b ^ 1], (x - 1) >> 1 & 1, sm);
+                    dead |= !wait4(&sm.pv_done[set], ph ^ 1, sm);
                     tc_fence_after();
                 }
                 group_any(grp, false);
-                const int col = lane & 15;
-                mx = fmaxf(fmaxf(sm.top[grp][0][col], sm.top[grp][1][col]), fmaxf(sm.top[grp][2][col], sm.top[grp][3][col]));
+                mx = fmaxf(fmaxf(sm.top[grp][0][lane], sm.top[grp][1][lane]), fmaxf(sm.top[grp][2][lane], sm.top[grp][3][lane]));
                 // (a row's reference goes by its own scores alone: one whose scores stayed within the bound keeps its)
                 const float to_m = m == neg_inf() || mx > m + (kGrow - kLift) ? fmaxf(mx, m) : m;
                 const float f = m == neg_inf() || to_m == m ? 1.f : ex2_approx(m - to_m);
                 m = to_m;
-                if (w == 0 && lane < 8 * nch) nref[(lane >> 3) * 32 + (lane & 7)] = kLift - (m == neg_inf() ? 0.f : m);
+                if (w == 0 && lane < 8 * nch) sm.nref[sl][set][mine] = kLift - (m == neg_inf() ? 0.f : m);
                 fresh = __any_sync(0xffffffffu, lane < 8 * nch && mine < rows && m == neg_inf());
                 if (!first) {
 #pragma unroll 1
                     for (int ch = 0; ch < nch; ++ch) {
                         float o[8], l[8];
-                        tmem_ld8(to + ch * 32, o);
-                        tmem_ld8(tl + ch * 32, l);
+                        tmem_ld8(quad + kTmemO + 16 * ch, o);
+                        tmem_ld8(quad + kTmemL + 16 * ch, l);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -575,54 +581,50 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp,
                             l[e] *= fe;
                             o[e] *= fe;
                         }
-                        tmem_st8(to + ch * 32, o);
-                        tmem_st8(tl + ch * 32, l);
+                        tmem_st8(quad + kTmemO + 16 * ch, o);
+                        tmem_st8(quad + kTmemL + 16 * ch, l);
                     }
                     tmem_wait_st();
                 }
                 group_any(grp, false);
             }
             first = false;
-            dead |= !wait4(&sm.pv_done[b], ph ^ 1, sm);  // the P of the tile before last has been read
-            uint8_t *dst = sm.p[b] + (grp >> 1) * (kTile * 32) + key * 32 + (((grp & 1) ^ ((key >> 2) & 1)) << 4);
+            dead |= !wait4(&sm.pv_done[set], ph ^ 1, sm);  // the P of this set's tile before has been read
+            uint8_t *dst = sm.p[set] + key * 32 + ((half ^ ((key >> 2) & 1)) << 4);
+            const bool dump = p.logits && t * kTile < last;
+#pragma unroll 1
+            for (int ch = 0; ch < nch; ++ch) {
+                float s[8], f[8], r[8], l[8];
+                load8(fac2 + 16 * ch, f);
+                load8(nref + 16 * ch, r);
+                tmem_ld8(quad + kTmemL + 16 * ch, l);
+                scores8(quad + kTmemS + 16 * ch, kk, lim + 16 * ch, s);
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-                if (ch < nch) {
-                    float f[8], r[8], l[8];
-                    tmem_ld8(tl + ch * 32, l);
-                    load8(fac2 + ch * 32, f);
-                    load8(nref + ch * 32, r);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = ex2_approx(fmaf(s[ch][e], f[e], r[e]));
-                    *reinterpret_cast<uint4 *>(dst + ch * (2 * kTile * 32)) =
-                        make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) l[e] += r[e];
-                    tmem_st8(tl + ch * 32, l);
+                for (int e = 0; e < 8; ++e) {
+                    r[e] = ex2_approx(fmaf(s[e], f[e], r[e]));
+                    l[e] += r[e];
                 }
+                tmem_st8(quad + kTmemL + 16 * ch, l);
+                *reinterpret_cast<uint4 *>(dst + ch * (kTile * 32)) =
+                    make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
+                if (dump) {
+                    const int r0 = 8 * half + 16 * ch;
+                    load8(sm.fac[is] + r0, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (r0 + e < rows) store_global(sm.lb[is][r0 + e] + kk.pos, s[e] * f[e]);
+                }
+            }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
-            arrive_lane0(&sm.p_full[b]);
-            if (p.logits && t * kTile < last) {
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch)
-                    if (ch < nch) {
-                        const int r0 = 8 * (grp + kGroups * ch);
-                        float f[8];
-                        load8(sm.fac[is] + r0, f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (r0 + e < rows) store_global(sm.lb[is][r0 + e] + pos, s[ch][e] * f[e]);
-                    }
-            }
+            arrive_lane0(&sm.p_full[set]);
         }
         // the sums of weights over the warp's keys: of eight rows at a time, each lane ends up with one
 #pragma unroll 1
         for (int ch = 0; ch < nch; ++ch) {
             float l[8], z;
-            tmem_ld8(tl + ch * 32, l);
+            tmem_ld8(quad + kTmemL + 16 * ch, l);
             tmem_wait_ld();
 #pragma unroll
             for (int h = 16, k = 4; k; h >>= 1, k >>= 1)
@@ -636,7 +638,7 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp,
             z += __shfl_xor_sync(0xffffffffu, z, 2);
             z += __shfl_xor_sync(0xffffffffu, z, 1);
             if ((lane & 3) == 0)
-                sm.sum[sl][w][8 * (grp + kGroups * ch) + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = z;
+                sm.sum[sl][set][w][8 * half + 16 * ch + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = z;
         }
         arrive_lane0(&sm.epi_full[sl]);
         arrive_lane0(&sm.item_empty[is]);
@@ -727,29 +729,44 @@ __device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, 
         const bool whole = rec.nsplit == 1;
 #pragma unroll 1
         for (int h = 0; h < p.M; h += 32) {
-            // row h + lane: where it goes (-1: there is none), and what its O is multiplied by
+            // row h + lane: where it goes (-1: there is none), and what the sets' O are multiplied by
             const int r = h + lane, j = r / p.G, gi = r - j * p.G;
             int at = -1;
-            float f = 0.f;
+            float f0 = 0.f, f1 = 0.f;
             if (r < p.M) {
                 at = whole ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : rec.rec + r;
-                const float l = sm.sum[sl][0][r] + sm.sum[sl][1][r] + sm.sum[sl][2][r] + sm.sum[sl][3][r];
-                f = l == 0.f ? 0.f : __frcp_rn(l);
+                const float *s0 = &sm.sum[sl][0][0][r], *s1 = &sm.sum[sl][1][0][r];
+                const float l0 = s0[0] + s0[kMaxRows] + s0[2 * kMaxRows] + s0[3 * kMaxRows], ref0 = -sm.nref[sl][0][r];
+                const float l1 = s1[0] + s1[kMaxRows] + s1[2 * kMaxRows] + s1[3 * kMaxRows], ref1 = -sm.nref[sl][1][r];
+                // (a sum of 0 has no reference)
+                const float ref = l0 == 0.f ? ref1 : l1 == 0.f ? ref0 : fmaxf(ref0, ref1);
+                f0 = l0 == 0.f ? 0.f : ex2_approx(ref0 - ref);
+                f1 = l1 == 0.f ? 0.f : ex2_approx(ref1 - ref);
+                const float l = __fadd_rn(__fmul_rn(l0, f0), __fmul_rn(l1, f1));  // (the same whichever set began)
+                const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+                // (what is 0 stays it under a NaN sum: an O that nobody wrote is not read)
+                if (f0 != 0.f) f0 *= inv;
+                if (f1 != 0.f) f1 *= inv;
                 if (w == 0) {
-                    const float z = l > 0.f ? logf(l) - sm.nref[sl][r] * 0.69314718f : (l == 0.f ? neg_inf() : l);  // (a NaN sum stays one)
+                    const float z = l > 0.f ? ref * 0.69314718f + logf(l) : (l == 0.f ? neg_inf() : l);  // (a NaN sum stays one)
                     if (!whole) p.part_lse[at] = z;
                     else p.lse[((size_t)rec.vidx * p.Hq + (size_t)rec.g * p.G + gi) * (p.k + 1) + j] = z;
                 }
             }
+            // (an item of one tile has one O: the set that met no tile has sums of 0)
+            const bool any0 = __any_sync(0xffffffffu, f0 != 0.f), any1 = __any_sync(0xffffffffu, f1 != 0.f);
 #pragma unroll 1
             for (int r0 = 0; r0 < min(32, p.M - h); r0 += 8) {
-                float o[8];
-                tmem_ld8(tm + ((uint32_t)w << 21) + kTmemO + sl * 64 + h + r0, o);
+                float o[8], o1[8];
+                const uint32_t from = tm + ((uint32_t)w << 21) + kTmemO + h + r0;
+                tmem_ld8(from, o);
+                tmem_ld8(from + 64, o1);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float y = o[e] * __shfl_sync(0xffffffffu, f, r0 + e);
+                    const float a0 = __shfl_sync(0xffffffffu, f0, r0 + e), a1 = __shfl_sync(0xffffffffu, f1, r0 + e);
                     const int row = __shfl_sync(0xffffffffu, at, r0 + e);
+                    const float y = __fadd_rn(any0 ? __fmul_rn(o[e], a0) : 0.f, any1 ? __fmul_rn(o1[e], a1) : 0.f);
                     if (row >= 0 && d < D) {
                         const size_t to = (size_t)row * D + d;
                         if (whole) p.out[to] = (uint16_t)pack_bf16x2(y, 0.f);
@@ -787,7 +804,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attn_kv4_kernel(const __grid_con
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.k_full[i], 4);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4 * kGroups);
+            mbar_init(&sm.p_full[i], 2 * kGroups);
             mbar_init(&sm.v_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.o_full[i], 1);
