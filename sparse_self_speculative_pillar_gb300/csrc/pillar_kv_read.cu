@@ -4,7 +4,7 @@
 // rounding (none under the power-of-two scales that the append writes, short of
 // the ends of bf16's range).
 //
-// One thread has eight values (16 bytes of output).  What bounds it: memory,
+// One thread has sixteen values (32 bytes of output).  What bounds it: memory,
 // mostly the rows written (2 bytes a value, after 0.56 or 1 read).
 #include "pillar_kv4.cuh"
 #include "pillar_kv4.h"
@@ -14,8 +14,7 @@ namespace pillar {
 
 namespace {
 
-constexpr int kThreadsR = 256;
-constexpr int kMaxCtaRowsR = 16;
+constexpr int kResident = 5, kUnroll = 2;  // CTAs of an SM, pieces of a thread in flight
 
 __device__ __forceinline__ float2 f32_of(uint32_t h) {
     float2 v;
@@ -25,64 +24,82 @@ __device__ __forceinline__ float2 f32_of(uint32_t h) {
     return v;
 }
 
-template <int D, int kBits>
-__global__ void __launch_bounds__(kThreadsR) kv_read_kernel(const KvReadArgs a, int rows) {
-    __shared__ long long s_place[kMapRows];
-    const int t0 = blockIdx.x * rows;
-    if (threadIdx.x < 32) {
-        const RowMap m{a.out_off, a.first, a.table, a.flags, a.n, a.B, a.max_blocks, a.num_blocks, a.max_len, false};
-        find_rows(m, t0, rows, s_place);
-    }
-    __syncthreads();
-    constexpr int PR = D / 8;
-    const int half = a.Hkv * PR;
-    for (Walk w(kThreadsR, 2 * half); w.token < rows; w.next()) {
-        const long long place = s_place[w.token];
-        if (place < 0) continue;
-        const bool value = w.piece >= half;
-        const int p = value ? w.piece - half : w.piece, h = p / PR, c = p - h * PR;
-        const size_t unit = (size_t)(place / PILLAR_KV_BLOCK) * a.Hkv + h, row = unit * PILLAR_KV_BLOCK + place % PILLAR_KV_BLOCK;
-        uint32_t o[4];
-        if (kBits == 4) {
-            const uint32_t codes = __ldg(reinterpret_cast<const uint32_t *>((value ? a.v : a.k) + row * (D / 2) + c * 4));
-            const uint32_t byte = __ldg(static_cast<const uint8_t *>(value ? a.v_scale : a.k_scale) + row * (D / kGroup4) + (c >> 1));
-            const uint32_t s = scale_pair(byte, 0);
-            uint32_t x[4];
-            f16_of_e2m1(codes, x);
+template <int D, int kBits, bool kWide>
+__global__ void __launch_bounds__(kRowThreads, kResident) kv_read_kernel(const KvReadArgs a, int rows) {
+    constexpr int PR = D / 16;  // pieces of a row
+    const bool value = threadIdx.x >= kRowWorkers / 2;
+    uint16_t *const out = value ? a.v_out : a.k_out;
+    const long long stride = value ? a.v_stride : a.k_stride;
+    const uint8_t *const from = value ? a.v : a.k;
+    const void *const scales = value ? a.v_scale : a.k_scale;
+    const RowMap m{a.out_off, a.first, a.table, a.flags, a.n, a.B, a.Hkv, a.max_blocks, a.num_blocks, a.max_len, false};
+    for_rows(m, rows, [&](long long t0, const int *place) {
+        Walk w(threadIdx.x % (kRowWorkers / 2), kRowWorkers / 2, a.Hkv * PR);
+        while (w.token < rows) {
+            uint4 codes[kUnroll];
+            uint32_t scale[kUnroll];
+            uint16_t *dst[kUnroll];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = f32_of(mul_f16x2(x[i], s));
-                o[i] = pack_bf16x2(v.x, v.y);
+            for (int i = 0; i < kUnroll; ++i, w.next()) {
+                dst[i] = nullptr;
+                const int at = w.token < rows ? place[w.token] : -1;
+                if (at < 0) continue;
+                const int h = w.piece / PR, c = w.piece % PR;
+                const size_t row = (size_t)(unsigned)(at + h * PILLAR_KV_BLOCK);
+                dst[i] = out + (t0 + w.token) * stride + w.piece * 16;
+                if (kBits == 4) {
+                    const uint2 y = __ldg(reinterpret_cast<const uint2 *>(from + row * (D / 2)) + c);
+                    codes[i].x = y.x, codes[i].y = y.y;
+                    scale[i] = __ldg(static_cast<const uint8_t *>(scales) + row * PR + c);
+                } else {
+                    codes[i] = __ldg(reinterpret_cast<const uint4 *>(from + row * D) + c);
+                    scale[i] = __ldg(static_cast<const uint32_t *>(scales) + row / PILLAR_KV_BLOCK);
+                }
             }
-        } else {
-            const uint2 codes = __ldg(reinterpret_cast<const uint2 *>((value ? a.v : a.k) + row * D + c * 8));
-            const float s = __ldg(static_cast<const float *>(value ? a.v_scale : a.k_scale) + unit);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t two = (i < 2 ? codes.x : codes.y) >> (16 * (i & 1));
-                uint32_t x;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)two));
-                const float2 v = f32_of(x);
-                o[i] = pack_bf16x2(v.x * s, v.y * s);
+            for (int i = 0; i < kUnroll; ++i) {
+                if (!dst[i]) continue;
+                uint32_t o[8];
+                if (kBits == 4) {
+                    const uint32_t s = scale[i] * 0x00800080u;  // (a scale byte in bits 7 to 14 is its f16 value)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t x[4];
+                        f16_of_e2m1(q ? codes[i].y : codes[i].x, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v = f32_of(mul_f16x2(x[e], s));
+                            o[4 * q + e] = pack_bf16x2(v.x, v.y);
+                        }
+                    }
+                } else {
+                    const float s = __uint_as_float(scale[i]);
+                    const uint32_t wd[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t x;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)(wd[e >> 1] >> (16 * (e & 1)))));
+                        const float2 v = f32_of(x);
+                        o[e] = pack_bf16x2(v.x * s, v.y * s);
+                    }
+                }
+                store32<kWide>(dst[i], o);
             }
         }
-        uint16_t *dst = (value ? a.v_out : a.k_out) + (long long)(t0 + w.token) * (value ? a.v_stride : a.k_stride) + (long long)p * 8;
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    });
 }
 
 }  // namespace
 
 cudaError_t launch_kv_read(const KvReadArgs &a, int nsm, cudaStream_t st) {
-    const int rows = a.n <= 16 * nsm ? 1 : kMaxCtaRowsR;
-    const unsigned grid = (unsigned)((a.n + (long long)rows - 1) / rows);
-    if (a.bits == 4) {
-        if (a.D == 128) kv_read_kernel<128, 4><<<grid, kThreadsR, 0, st>>>(a, rows);
-        else kv_read_kernel<64, 4><<<grid, kThreadsR, 0, st>>>(a, rows);
-    } else {
-        if (a.D == 128) kv_read_kernel<128, 8><<<grid, kThreadsR, 0, st>>>(a, rows);
-        else kv_read_kernel<64, 8><<<grid, kThreadsR, 0, st>>>(a, rows);
-    }
+    const int rows = rows_of_turn(a.n, nsm);
+    const unsigned grid = row_ctas(a.n, rows, kResident, nsm);
+    const bool wide = rows_wide(a.k_out, a.v_out, a.k_stride, a.v_stride);
+    const auto f = a.bits == 4 ? (a.D == 128 ? (wide ? kv_read_kernel<128, 4, true> : kv_read_kernel<128, 4, false>)
+                                             : (wide ? kv_read_kernel<64, 4, true> : kv_read_kernel<64, 4, false>))
+                               : (a.D == 128 ? (wide ? kv_read_kernel<128, 8, true> : kv_read_kernel<128, 8, false>)
+                                             : (wide ? kv_read_kernel<64, 8, true> : kv_read_kernel<64, 8, false>));
+    f<<<grid, kRowThreads, 0, st>>>(a, rows);
     return cudaGetLastError();
 }
 

@@ -15,17 +15,18 @@ struct RowMap {
     const int *base;   // [B]: lengths that include the rows (ends), or positions of the first rows
     const int *table;  // [B, max_blocks]
     int *flags;        // device error word, or null
-    int n, B, max_blocks, num_blocks, max_len;
+    int n, B, Hkv, max_blocks, num_blocks, max_len;
     bool ends;
 };
 
 constexpr int kMapRows = 32;  // rows that one call maps, at most
 
-// The places of rows [t0, t0 + rows) as block * 16 + row of the block, or -1, by one warp.  The request of row t0 is found
-// 32 offsets at a time (two dependent rounds for a thousand requests), the others' by the offsets that follow it.
-__device__ __forceinline__ void find_rows(const RowMap &m, int t0, int rows, long long *place) {
+// The places of rows [t0, t0 + rows), for KV head 0, as rows of the pools (block * Hkv * 16 + row of the block; head h lies 16 h
+// further on), or -1, by one warp.  The request of row t0 is found 32 offsets at a time (two dependent rounds for a thousand
+// requests), the others' by the offsets that follow it.
+__device__ __forceinline__ void find_rows(const RowMap &m, long long t0, int rows, int *place) {
     const int lane = threadIdx.x & 31;
-    const long long t = (long long)t0 + lane;
+    const long long t = t0 + lane;
     const int all = min(m.n, __ldg(m.off + m.B));
     int lo = 0;
     for (int n = m.B; n > 1;) {  // the last offset at or below t0 is one of n from lo on
@@ -43,7 +44,7 @@ __device__ __forceinline__ void find_rows(const RowMap &m, int t0, int rows, lon
         if (lane == i) b = lo + at;
     }
     if (lane >= rows) return;
-    long long at = -1;
+    int at = -1;
     if (t < all) {
         for (b = min(b, m.B - 1); b + 1 < m.B && __ldg(m.off + b + 1) <= t;) ++b;
         const int first = __ldg(m.off + b), end = __ldg(m.off + b + 1), base = __ldg(m.base + b);
@@ -56,20 +57,20 @@ __device__ __forceinline__ void find_rows(const RowMap &m, int t0, int rows, lon
         } else {
             const int block = __ldg(m.table + (size_t)b * m.max_blocks + pos / PILLAR_KV_BLOCK);
             if (block < 0 || block >= m.num_blocks) bad = PILLAR_FLAG_SLOT;
-            else at = (long long)block * PILLAR_KV_BLOCK + pos % PILLAR_KV_BLOCK;
+            else at = block * m.Hkv * PILLAR_KV_BLOCK + (int)(pos % PILLAR_KV_BLOCK);
         }
         if (bad && m.flags) atomicOr(m.flags, bad);
     }
     place[lane] = at;
 }
 
-// A packed batch is worked on in pieces of 16 bytes of bf16 (eight values): piece j of a token, K's first, then V's.  A
-// CTA's threads walk over the pieces of its tokens; the pair (token, piece) moves on without a division.
+// A packed batch is worked on in pieces of sixteen values (32 bytes of bf16), K's by the first half of a CTA's workers, V's by
+// the second.  The pair (token, piece of the token) of a thread moves on by that many threads without a division.
 struct Walk {
     int token, piece, dt, dp, pieces;
-    __device__ __forceinline__ Walk(int threads, int pieces_) : pieces(pieces_) {
-        token = threadIdx.x / pieces;
-        piece = threadIdx.x - token * pieces;
+    __device__ __forceinline__ Walk(int thread, int threads, int pieces_) : pieces(pieces_) {
+        token = thread / pieces;
+        piece = thread - token * pieces;
         dt = threads / pieces;
         dp = threads - dt * pieces;
     }
@@ -79,5 +80,61 @@ struct Walk {
         if (piece >= pieces) piece -= pieces, ++token;
     }
 };
+
+// 32 bytes; kWide: at a multiple of 32.
+struct Half16 {
+    uint32_t w[8];
+};
+template <bool kWide>
+__device__ __forceinline__ Half16 load32(const uint16_t *src) {
+    Half16 x;
+    if (kWide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
+                     : "l"(src));
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+        x = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    }
+    return x;
+}
+template <bool kWide>
+__device__ __forceinline__ void store32(uint16_t *dst, const uint32_t (&w)[8]) {
+    if (kWide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+// Rows of both tensors at multiples of 32 bytes.
+inline bool rows_wide(const void *k, const void *v, long long k_stride, long long v_stride) {
+    return ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0 && ((k_stride | v_stride) & 15) == 0;
+}
+
+// CTAs of eight warps that work and one that finds the rows of the next `rows` tokens meanwhile (a chain of four or five
+// dependent loads), each going through the batch by the number of CTAs.
+constexpr int kRowWorkers = 256, kRowThreads = kRowWorkers + 32;
+template <typename Work>
+__device__ __forceinline__ void for_rows(const RowMap &m, int rows, Work work) {
+    __shared__ int s_place[2][kMapRows];
+    const int groups = (int)(((long long)m.n + rows - 1) / rows);
+    int buf = 0;
+    for (int i = blockIdx.x; i < groups; i += gridDim.x, buf ^= 1) {
+        const long long t0 = (long long)i * rows;
+        if (threadIdx.x >= kRowWorkers) find_rows(m, t0, rows, s_place[buf]);
+        __syncthreads();  // (and the rows before last have been worked on)
+        if (threadIdx.x < kRowWorkers) work(t0, s_place[buf]);
+    }
+}
+// rows of a CTA's turn, and CTAs: one row while that gives every SM at most sixteen CTAs (a decode step: all in flight), else
+// sixteen, and no more CTAs than are resident.
+inline int rows_of_turn(int n, int nsm) { return n <= 16 * nsm ? 1 : 16; }
+inline unsigned row_ctas(int n, int rows, int resident, int nsm) {
+    const long long groups = ((long long)n + rows - 1) / rows, most = rows == 1 ? groups : (long long)resident * nsm;
+    return (unsigned)(groups < most ? groups : most);
+}
 
 }  // namespace pillar
