@@ -128,8 +128,15 @@ __device__ __forceinline__ bool elect_one4() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
     return one != 0;
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+template <int kOff>
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {  // to dst + kOff
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1], 16;" ::"r"(dst), "l"(src), "n"(kOff) : "memory");
+}
+template <int kOff>
+__device__ __forceinline__ int lds_int(uint32_t at) {
+    int v;
+    asm volatile("ld.shared.s32 %0, [%1+%2];" : "=r"(v) : "r"(at), "n"(kOff) : "memory");
+    return v;
 }
 template <int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
@@ -246,8 +253,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "n"(kOff));
     return v;
 }
-__device__ __forceinline__ void sts128(uint32_t at, int off, const uint32_t (&v)[4]) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + off), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+template <int kOff>
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.u32 [%0+%5], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "n"(kOff) : "memory");
 }
 
 // Warp w of the four that turn K (or V) into operands: keys 32 w .. 32 w + 31 of every tile, from the copies on.  (Code is kept
@@ -296,12 +304,15 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, i
             more = tiles > 0;
         }
         if (more) {
-            const int *rows = sm.row[slot] + at * kTile + 32 * w;
-#pragma unroll
-            for (int i = 0; i < RC; ++i)  // (the codes of a key that is not there: any, its scales are 0)
-                copy16(to_codes + st * (kTile * S::kRow) + i * (32 / RC) * S::kRow,
-                       codes + (size_t)(uint32_t)max(rows[r0 + i * (32 / RC)], 0) * S::kRow);
-            const int row = rows[lane];
+            const uint32_t rows = smem_u32(sm.row[slot] + at * kTile + 32 * w), mine = rows + r0 * 4, dst = to_codes + st * (kTile * S::kRow);
+            constexpr int RP = 32 / RC;  // (the codes of a key that is not there: any, its scales are 0)
+            copy16<0>(dst, codes + (size_t)(uint32_t)max(lds_int<0>(mine), 0) * S::kRow);
+            copy16<RP * S::kRow>(dst, codes + (size_t)(uint32_t)max(lds_int<4 * RP>(mine), 0) * S::kRow);
+            if (RC == 4) {
+                copy16<2 * RP * S::kRow>(dst, codes + (size_t)(uint32_t)max(lds_int<8 * RP>(mine), 0) * S::kRow);
+                copy16<3 * RP * S::kRow>(dst, codes + (size_t)(uint32_t)max(lds_int<12 * RP>(mine), 0) * S::kRow);
+            }
+            const int row = lds_int<0>(rows + lane * 4);
             copy_small<S::kScales>(to_scales + st * (kTile * S::kScales), scales + (size_t)(uint32_t)max(row, 0) * S::kScales,
                                    row >= 0 ? S::kScales : 0);
             ++issued;
@@ -316,6 +327,7 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, i
         // the operand's buffer is free: the scores (the outputs) of the tile before last are done
         if (!wait4(kValue ? &sm.pv_done[buf] : &sm.s_full[buf], (x >> 1 & 1) ^ 1, sm)) break;
         tc_fence_after();
+        const uint32_t into = out + buf * (kTile * D * 2), columns = tm + ((uint32_t)w << 21) + kTmemK + buf * 64;
 #pragma unroll
         for (int i = 0; i < RC; ++i) {
             const uint32_t word[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
@@ -329,10 +341,13 @@ __device__ void convert4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, i
             }
             if (kValue) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sts128((out + buf * (kTile * D * 2)) ^ (((i & 1) * 4 + e) << 4), (i >> 1) * (kTile * 128), h[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t to = into ^ (((i & 1) * 4 + e) << 4);
+                    if (i < 2) sts128<0>(to, h[e]);
+                    else sts128<kTile * 128>(to, h[e]);
+                }
             } else {
-                tmem_st16(tm + ((uint32_t)w << 21) + kTmemK + buf * 64 + i * 16, &h[0][0]);
+                tmem_st16(columns + i * 16, &h[0][0]);
             }
         }
         if (kValue) {
