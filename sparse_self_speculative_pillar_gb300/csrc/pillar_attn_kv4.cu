@@ -17,6 +17,8 @@
 //     O^T [D x rows]   += V^T P^T    V and P from shared memory
 // so that a key's row is made into an operand once, whatever the number of
 // query rows.
+// A row is (head, query token), the tokens of a head together: the rows' logits
+// lie one after another.
 //   * The resolver warp takes items from the planner's queue and turns their
 //     keys into rows of the pools, 512 at a time.
 //   * Four warps each for K and V copy the rows of the tiles ahead (16 bytes a
@@ -68,10 +70,9 @@ struct Smem4 {
     alignas(16) int row[kChunks][kChunkKeys];   // rows of the pools ((block * Hkv + g) * 16 + position % 16), or -1
     int chunk_tiles[kChunks];                   // 0: no more
     ItemRec item[kItems];
-    // per query row: logit = sum * fac, in base-2 units sum * fac2; last position seen; its logits, or null
+    // per query row: logit = sum * fac, in base-2 units sum * fac2; last position seen
     alignas(16) float fac[kItems][kMaxRows], fac2[kItems][kMaxRows];
     int lim[kItems][kMaxRows];
-    alignas(16) float *lb[kItems][kMaxRows];
     // per item (in turn), set and row: kLift - reference maximum (base 2); sums of weights, by the keys' warp of a tile
     alignas(16) float nref[2][2][kMaxRows], sum[2][2][4][kMaxRows];
     float top[kGroups][4][32];                  // a group's largest scores, per warp
@@ -475,7 +476,7 @@ __device__ __forceinline__ float warp_max(float x) {  // (a NaN is passed over)
     return y;
 }
 
-// (Without a clobber of memory: the loads of the next row's place need not wait for it.)
+// (Without a clobber of memory: other loads need not wait for it.)
 __device__ __forceinline__ void store_global(float *dst, float v) { asm volatile("st.global.f32 [%0], %1;" ::"l"(dst), "f"(v)); }
 __device__ __forceinline__ void load8(const float *src, float *v) {
     const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
@@ -533,8 +534,10 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp,
         }
         Key4 kk;
         kk.pos = rec.begin + key;
+        const long long row_logits = rec.L;
+        float *logits = p.logits + (rec.logit_off + ((long long)rec.g * rows + 8 * half) * row_logits + kk.pos);  // of row 8 half
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t, ++x, kk.pos += kTile) {
+        for (int t = 0; t < tiles; ++t, ++x, kk.pos += kTile, logits += kTile) {
             if (t % kChunkTiles == 0) dead |= !wait4(&sm.rows_full[slot], phase, sm);
             kk.there = sm.row[slot][t % kChunkTiles * kTile + key] >= 0;
             if (t % kChunkTiles == kChunkTiles - 1 || t == tiles - 1) {
@@ -624,10 +627,11 @@ __device__ void softmax4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int grp,
                     make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
                 if (dump) {
                     const int r0 = 8 * half + 16 * ch;
+                    float *to = logits + 16 * ch * row_logits;
                     load8(sm.fac[is] + r0, f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (r0 + e < rows) store_global(sm.lb[is][r0 + e] + kk.pos, s[e] * f[e]);
+                    for (int e = 0; e < 8; ++e, to += row_logits)
+                        if (r0 + e < rows) store_global(to, s[e] * f[e]);
                 }
             }
             tmem_wait_st();
@@ -676,7 +680,7 @@ __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, int lane) {
 #pragma unroll 1
         for (int r0 = 0; r0 < (p.M + 7) / 8 * 8; r0 += 4) {
             // (lane l looks after row r0 + l % 4)
-            const int my = r0 + (lane & 3), j = my / p.G, gi = my - j * p.G;
+            const int my = r0 + (lane & 3), gi = my / (p.k + 1), j = my - gi * (p.k + 1);
             const int at = my < p.M ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : -1;
             uint32_t x[4][W], mine = 0;
 #pragma unroll
@@ -717,8 +721,6 @@ __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, int lane) {
                 sm.fac[is][my] = fac;
                 sm.fac2[is][my] = fmaxf(fac * kLog2e, __int_as_float(1));
                 sm.lim[is][my] = my < p.M ? rec.L - (p.k + 1) + j : 0x7fffffff;
-                if (my < p.M && p.logits)
-                    sm.lb[is][my] = p.logits + (rec.logit_off + ((long long)(rec.g * p.G + gi) * (p.k + 1) + j) * rec.L);
             }
         }
         fence_proxy_async_smem();
@@ -745,11 +747,11 @@ __device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, 
 #pragma unroll 1
         for (int h = 0; h < p.M; h += 32) {
             // row h + lane: where it goes (-1: there is none), and what the sets' O are multiplied by
-            const int r = h + lane, j = r / p.G, gi = r - j * p.G;
+            const int r = h + lane, gi = r / (p.k + 1), j = r - gi * (p.k + 1);
             int at = -1;
             float f0 = 0.f, f1 = 0.f;
             if (r < p.M) {
-                at = whole ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : rec.rec + r;
+                at = whole ? (rec.q_off + j) * p.Hq + rec.g * p.G + gi : rec.rec + j * p.G + gi;
                 const float *s0 = &sm.sum[sl][0][0][r], *s1 = &sm.sum[sl][1][0][r];
                 const float l0 = s0[0] + s0[kMaxRows] + s0[2 * kMaxRows] + s0[3 * kMaxRows], ref0 = -sm.nref[sl][0][r];
                 const float l1 = s1[0] + s1[kMaxRows] + s1[2 * kMaxRows] + s1[3 * kMaxRows], ref1 = -sm.nref[sl][1][r];
@@ -765,7 +767,7 @@ __device__ void epilogue4(const Kv4Params &p, Smem4<D> &sm, uint32_t tm, int w, 
                 if (w == 0) {
                     const float z = l > 0.f ? ref * 0.69314718f + logf(l) : (l == 0.f ? neg_inf() : l);  // (a NaN sum stays one)
                     if (!whole) p.part_lse[at] = z;
-                    else p.lse[((size_t)rec.vidx * p.Hq + (size_t)rec.g * p.G + gi) * (p.k + 1) + j] = z;
+                    else p.lse[(size_t)rec.vidx * p.Hq * (p.k + 1) + (size_t)rec.g * p.M + r] = z;
                 }
             }
             // (an item of one tile has one O: the set that met no tile has sums of 0)
