@@ -437,3 +437,73 @@ def test_more_items_than_ctas(Hq, k):
     d = c.device()
     c.call(d)
     c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,k,B,lo,hi,shape", [
+    (32, 8, 128, 8, 150, 9, 128, {}),                   # a tile an item, many items a CTA
+    (24, 8, 64, 6, 170, 7, 300, {}),                    # one to three tiles
+    (20, 4, 64, 4, 40, 5, 900, dict(verify_chunk=64)),  # pieces of half a tile
+    (8, 2, 128, 2, 60, 3, 400, dict(verify_chunk=64, draft_chunk=64)),  # 12 rows, and lists
+    (6, 1, 64, 2, 9, 1, 700, {}),                       # 18 rows: a group of eight with two in it
+])
+def test_short_items_in_numbers(Hq, Hkv, D, k, B, lo, hi, shape):
+    c = Case(90, Hq, Hkv, D, k, *mixed(90, B, lo, hi, k), **shape)
+    d = c.device()
+    c.call(d)
+    c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_from_a_plan_without_a_dump_and_captured(D):
+    c = Case(91, 32, 4, D, 4, [300, 77, 20, 1100], [1, 0, 1, 1], verify_chunk=256)
+    d, e, f = c.device(), c.device(dump=False), c.device()
+    c.call(d)
+    c.check(d)
+    c.call(e)
+    assert torch.equal(d["out"], e["out"]) and torch.equal(d["lse"], e["lse"])
+    P.pillar_attn_plan(c.shape, f["mode"], f["len"], f["cnt"], f["ws"])
+    run = lambda: P.pillar_attn_run_kv4(c.shape, f["q"], f["k4"], f["v4"], f["ks"], f["vs"], f["table"], f["idx"], f["out"],  # noqa: E731
+                                        f["logits"], f["lse"], f["ws"])
+    run()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(2):
+        for name in ("out", "logits", "lse"):
+            assert torch.equal(d[name], f[name]), name
+            f[name].fill_(0x7fc0 if name == "out" else SENTINEL)
+        g.replay()
+    assert P.pillar_get_error(f["ws"]) == 0
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_anywhere_in_the_pipeline():
+    """Bounds from one microsecond to more than the call takes, in items of more than sixteen rows: every CTA ends, the call says so
+    and a whole one that follows at once on the stream, on a workspace of its own, is right; so is the next on the same workspace."""
+    g = np.random.default_rng(92)
+    big = dict(seed=92, Hq=32, Hkv=8, D=128, k=6, lens=g.integers(600, 1500, 24), modes=(np.arange(24) % 4 != 1).astype(int))
+    short, full = Case(**big, wait_timeout_us=1), Case(**big)
+    small = Case(93, 32, 8, 128, 4, [300, 90, 400], [1, 0, 1])
+    want, d, after = small.device(), full.device(), small.device()
+    small.call(want)
+    small.check(want)
+    seen = 0
+    for bound in (1, 2, 3, 4, 6, 9, 13, 20, 30, 50, 5000):
+        short.shape.wait_timeout_us = bound
+        short.call(d)
+        small.call(after)
+        flags = P.pillar_get_error(d["ws"])
+        assert flags & ~P.FLAG_TIMEOUT == 0 and P.pillar_get_error(after["ws"]) == 0, bound
+        seen |= flags if bound == 1 else 0
+        for name in ("out", "logits", "lse"):
+            assert torch.equal(after[name], want[name]), (bound, name)
+            after[name].fill_(0x7fc0 if name == "out" else SENTINEL)
+    assert seen == P.FLAG_TIMEOUT, "no wait ran out"
+    d["out"].fill_(0x7fc0)
+    d["logits"].fill_(SENTINEL)
+    d["lse"].fill_(SENTINEL)
+    full.call(d)
+    full.check(d)
