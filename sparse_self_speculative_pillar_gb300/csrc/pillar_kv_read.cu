@@ -4,8 +4,10 @@
 // rounding (none under the power-of-two scales that the append writes, short of
 // the ends of bf16's range).
 //
-// One thread has sixteen values (32 bytes of output).  What bounds it: memory,
-// mostly the rows written (2 bytes a value, after 0.56 or 1 read).
+// One thread has sixteen values (32 bytes of output), two at a time.  What bounds it: memory, mostly the rows written (2 bytes a
+// value, after 0.56 or 1 read).  1.3 GB of 4-bit codes and rows take 207 us and 1.5 GB of 8-bit ones 240: 6.2 and 6.3 TB/s, 0.92
+// and 0.93 of a plain copy's rate (16-byte accesses: 235 and 291).  (Three CTAs of four pieces a thread: 205 and 239 us; six of two,
+// with 32 registers: 246 and 278.)
 #include "pillar_kv4.cuh"
 #include "pillar_kv4.h"
 #include "pillar_rows.cuh"
@@ -25,7 +27,7 @@ __device__ __forceinline__ float2 f32_of(uint32_t h) {
 }
 
 template <int D, int kBits, bool kWide>
-__global__ void __launch_bounds__(kRowThreads, kResident) kv_read_kernel(const KvReadArgs a, int rows) {
+__global__ void __launch_bounds__(kRowThreads, kResident) kv_read_kernel(KvReadArgs a, int most) {
     constexpr int PR = D / 16;  // pieces of a row
     const bool value = threadIdx.x >= kRowWorkers / 2;
     uint16_t *const out = value ? a.v_out : a.k_out;
@@ -33,7 +35,7 @@ __global__ void __launch_bounds__(kRowThreads, kResident) kv_read_kernel(const K
     const uint8_t *const from = value ? a.v : a.k;
     const void *const scales = value ? a.v_scale : a.k_scale;
     const RowMap m{a.out_off, a.first, a.table, a.flags, a.n, a.B, a.Hkv, a.max_blocks, a.num_blocks, a.max_len, false};
-    for_rows(m, rows, [&](long long t0, const int *place) {
+    for_rows(m, most, [&](long long t0, int rows, const int *place) {
         Walk w(threadIdx.x % (kRowWorkers / 2), kRowWorkers / 2, a.Hkv * PR);
         while (w.token < rows) {
             uint4 codes[kUnroll];
@@ -99,8 +101,7 @@ cudaError_t launch_kv_read(const KvReadArgs &a, int nsm, cudaStream_t st) {
                                              : (wide ? kv_read_kernel<64, 4, true> : kv_read_kernel<64, 4, false>))
                                : (a.D == 128 ? (wide ? kv_read_kernel<128, 8, true> : kv_read_kernel<128, 8, false>)
                                              : (wide ? kv_read_kernel<64, 8, true> : kv_read_kernel<64, 8, false>));
-    f<<<grid, kRowThreads, 0, st>>>(a, rows);
-    return cudaGetLastError();
+    return launch_rows(f, a, rows, grid, st);
 }
 
 }  // namespace pillar
