@@ -22,8 +22,9 @@ namespace pillar {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kCtas = 4;   // CTAs of an SM
-constexpr int kSlots = 3;  // 16-key pieces of a warp: one being read, two on their way
+template <int NT>
+constexpr int kCtas = NT == 1 ? 4 : 3;  // CTAs of an SM (of two row tiles: a fourth takes the registers that hold O)
+constexpr int kSlots = 3;  // 16-key pieces of a warp: one being read, two on their way (four and five of one row tile: no case faster)
 constexpr int kPieces = kMaxChunk / 16 / kWarps;  // of a warp in an item, at most
 static_assert(kPieces <= 32, "a lane keeps what it knows of a piece");
 
@@ -44,7 +45,12 @@ template <int D, int NT>
 struct Smem4 {
     static constexpr int kRows = 8 * NT;
     Piece4<D> piece[kWarps][kSlots];
-    float o[kWarps][8][D + 4], m[kWarps][8], l[kWarps][8];  // the warps' parts of a row tile
+    // the warps' parts of a row tile; of items of one, O takes the place of its warp's pieces
+    float own_o[NT == 1 ? 1 : kWarps][8][NT == 1 ? 4 : D + 4], m[kWarps][8], l[kWarps][8];
+    __device__ __forceinline__ float *o(int w, int row) {
+        return NT == 1 ? reinterpret_cast<float *>(piece[w]) + row * (D + 4) : own_o[NT == 1 ? 0 : w][row];
+    }
+    static_assert(8 * (D + 4) * sizeof(float) <= kSlots * sizeof(Piece4<D>), "O in the place of the pieces");
     uint2 q[NT][NT == 1 ? 1 : D / 16][32];                  // two row tiles: query operands by row tile, step, lane
     alignas(8) float fac[kRows], fac2[kRows];               // per row: logit = sum * fac, fac2 in base 2
     int lim[kRows];                                         // last position seen
@@ -313,7 +319,7 @@ __device__ __forceinline__ void keys16(const Smem4<D, NT> &sm, uint32_t pc, cons
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __grid_constant__ FewParams fp) {
+__global__ void __launch_bounds__(kThreads, kCtas<NT>) attn_kv4_few_kernel(const __grid_constant__ FewParams fp) {
     using Pc = Piece4<D>;
     extern __shared__ __align__(128) char smem[];
     Smem4<D, NT> &sm = *reinterpret_cast<Smem4<D, NT> *>(smem);
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
             if (t == 1 && more) begin_item(sm.w[turn ^ 1]);  // (what it looked up has come meanwhile)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float *dst = &sm.o[warp][2 * c + e][g * (D / 8)];
+                float *dst = sm.o(warp, 2 * c + e) + g * (D / 8);
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 2)
                     *reinterpret_cast<float4 *>(dst + 2 * i) =
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
 #pragma unroll 4
                 for (int s = 0; s < kWarps; ++s) {
                     const float ls = sm.l[s][lr], f = ls == 0.f ? 0.f : ex2_approx(sm.m[s][lr] - mx);
-                    const float4 o = *reinterpret_cast<const float4 *>(&sm.o[s][lr][d]);
+                    const float4 o = *reinterpret_cast<const float4 *>(sm.o(s, lr) + d);
                     l += f * ls;
                     v.x += f * o.x, v.y += f * o.y, v.z += f * o.z, v.w += f * o.w;
                 }
@@ -603,7 +609,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
             }
         }
         if (more) {
-            if (NT == 1) begin_item(sm.w[turn ^ 1]);
+            if (NT == 1) {
+                __syncthreads();  // (O has been read; `more` is every thread's)
+                begin_item(sm.w[turn ^ 1]);
+            }
             if (stages) queries(sm.w[turn ^ 1]);
         }
         __syncthreads();  // (the next item's queries and rows are there)
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_kv4_few_kernel(const __g
 template <int D, int NT>
 cudaError_t launch_t(const FewParams &p, int nsm, cudaStream_t st) {
     constexpr int kSmem = (int)sizeof(Smem4<D, NT>);
-    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
+    static_assert(kCtas<NT> * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
     static unsigned long long configured[kMaxDevices] = {};
     int dev = 0;
     unsigned long long ctx = 0;
@@ -635,7 +644,7 @@ cudaError_t launch_t(const FewParams &p, int nsm, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCtas * nsm);
+    cfg.gridDim = dim3(kCtas<NT> * nsm);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
