@@ -10,8 +10,8 @@
 // magnitude brought to [2^14, 2^15)), but for elements 2^-28 below that.  So
 // both products take f16 operands and the scores are sums of exact products.
 //
-// Here are the verify items of more than sixteen rows; pillar_attn_kv4_few.cu has
-// the others.  One persistent CTA an SM, 128 keys a tile, the keys on the M of
+// Here are the verify items of more than sixteen rows (24 without a dump of logits);
+// pillar_attn_kv4_few.cu has the others.  One persistent CTA an SM, 128 keys a tile, the keys on the M of
 // tcgen05:
 //     S^T [keys x rows] = K Q^T      K from tensor memory, Q from shared memory
 //     O^T [D x rows]   += V^T P^T    V and P from shared memory
@@ -928,7 +928,7 @@ cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaS
     if (p.M <= 8 || a.schedule == PILLAR_SCHEDULE_DRAFT_ONLY) {
         e = launch_attn_kv4_few(p, a.D, 8, 0, false, nsm, st);
     } else {
-        e = p.M <= kFewRows ? launch_attn_kv4_few(p, a.D, p.M, 1, false, nsm, st)
+        e = p.M <= (p.logits ? kFewRowsDumped : kFewRows) ? launch_attn_kv4_few(p, a.D, p.M, 1, false, nsm, st)
                             : a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
         if (e == cudaSuccess && a.schedule != PILLAR_SCHEDULE_VERIFY_ONLY) e = launch_attn_kv4_few(p, a.D, 8, 2, true, nsm, st);
     }

@@ -1,4 +1,4 @@
-// pillar_attn_kv4.cuh -- what the two kernels of the 4-bit attention share: items of at most sixteen query rows
+// pillar_attn_kv4.cuh -- what the two kernels of the 4-bit attention share: items of few query rows
 // (pillar_attn_kv4_few.cu) and the others (pillar_attn_kv4.cu).
 #pragma once
 
@@ -6,7 +6,11 @@
 
 namespace pillar {
 
-constexpr int kFewRows = 16;
+// Verify items of at most so many rows, without a dump of logits and with one, go to warps of mma.sync; the others to tcgen05,
+// whose work for a key is the same whatever the rows.  (128 requests of 8192 tokens, 32 heads on 8, verify steps of 4, 5 and 6
+// tokens, that is 16, 20 and 24 rows: 134 us against 179 without a dump for 16 rows, 140 against 152 for 24; with one 157 against 185
+// for 16, but 187 against 179 for 20 and 171 against 165 for 24.)
+constexpr int kFewRows = 24, kFewRowsDumped = 16;
 
 struct Kv4Params {
     const uint16_t *q;

@@ -1,10 +1,10 @@
-// pillar_attn_kv4_few.cu -- the 4-bit attention's items of at most sixteen query rows: drafts, plain decoding, short
-// verify steps.
+// pillar_attn_kv4_few.cu -- the 4-bit attention's items of at most 24 query rows: drafts, plain decoding, short verify
+// steps.
 //
 // Every warp works alone on 16 keys at a time: S^T = K Q^T and O^T = V^T P^T
-// with m16n8k16, the keys (the dimensions) on m and one or two tiles of eight
+// with m16n8k16, the keys (the dimensions) on m and one to three tiles of eight
 // rows on n, both operands f16 (every cache value is one).  Nothing waits for
-// another warp before an item's end, where the eight warps of the CTA, which share
+// another warp before an item's end, where the four warps of the CTA, which share
 // its keys, join through shared memory.
 //   * The codes come by 16-byte asynchronous copies into three slots of the warp's
 //     own.  K: lane c of four has dimensions [32c, 32c + 32) of its key, 16 bytes
@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 template <int NT>
-constexpr int kCtas = NT == 1 ? 4 : 3;  // CTAs of an SM (of two row tiles: a fourth takes the registers that hold O)
+constexpr int kCtas = 5 - NT;  // CTAs of an SM (more would take the registers that hold O)
 constexpr int kSlots = 3;  // 16-key pieces of a warp: one being read, two on their way (four and five of one row tile: no case faster)
 constexpr int kPieces = kMaxChunk / 16 / kWarps;  // of a warp in an item, at most
 static_assert(kPieces <= 32, "a lane keeps what it knows of a piece");
@@ -51,11 +51,11 @@ struct Smem4 {
         return NT == 1 ? reinterpret_cast<float *>(piece[w]) + row * (D + 4) : own_o[NT == 1 ? 0 : w][row];
     }
     static_assert(8 * (D + 4) * sizeof(float) <= kSlots * sizeof(Piece4<D>), "O in the place of the pieces");
-    uint2 q[NT][NT == 1 ? 1 : D / 16][32];                  // two row tiles: query operands by row tile, step, lane
+    uint2 q[NT][NT == 1 ? 1 : D / 16][32];                  // more than one row tile: query operands by row tile, step, lane
     alignas(8) float fac[kRows], fac2[kRows];               // per row: logit = sum * fac, fac2 in base 2
     int lim[kRows];                                         // last position seen
     float *lb[kRows];                                       // where its logits at position 0 go, or null
-    int row[kWarps][NT == 1 ? kPieces * 16 : 1];            // lists (of one row tile): rows of the pools, or -1
+    int row[kWarps][NT == 1 ? kPieces * 16 : 1];            // lists (one row tile): rows of the pools, or -1
     struct alignas(16) {
         Item item;
         ReqInfo req;
@@ -189,7 +189,7 @@ __device__ __forceinline__ void keys16(const Smem4<D, NT> &sm, uint32_t pc, cons
             sc[0][1] = lds8<1>(ks) * kBoth;
             sc[1][1] = lds8<Pc::kScales + 1>(ks) * kBoth;
         }
-        const uint2 *q = &sm.q[0][0][lane];  // (two row tiles)
+        const uint2 *q = &sm.q[0][0][lane];  // (more than one row tile)
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             uint32_t h0[4], h1[4];
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<NT>) attn_kv4_few_kernel(const
     };
     if (tid == 0) open(sm.w[0]);
     __syncthreads();
-    // Of its pieces of the item (warp, warp + 8, ..) a lane keeps the first row of piece `lane` (contexts) and which of its keys
+    // Of its pieces of the item (warp, warp + 4, ..) a lane keeps the first row of piece `lane` (contexts) and which of its keys
     // there are; lists have their rows in shared memory.
     unsigned base = 0, vis = 0;
     State4<D, NT> a;
@@ -662,7 +662,8 @@ cudaError_t launch_attn_kv4_few(const Kv4Params &p, int D, int rows, int part, b
     f.counter = part == 2 ? &p.hdr->draft_counter : &p.hdr->item_counter;
     f.after = after;
     if (rows <= 8) return D == 128 ? launch_t<128, 1>(f, nsm, st) : launch_t<64, 1>(f, nsm, st);
-    return D == 128 ? launch_t<128, 2>(f, nsm, st) : launch_t<64, 2>(f, nsm, st);
+    if (rows <= 16) return D == 128 ? launch_t<128, 2>(f, nsm, st) : launch_t<64, 2>(f, nsm, st);
+    return D == 128 ? launch_t<128, 3>(f, nsm, st) : launch_t<64, 3>(f, nsm, st);
 }
 
 }  // namespace pillar

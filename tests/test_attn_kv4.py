@@ -507,3 +507,16 @@ def test_waits_that_run_out_anywhere_in_the_pipeline():
     d["lse"].fill_(SENTINEL)
     full.call(d)
     full.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,k,shape", [
+    (8, 2, 128, 4, {}), (6, 1, 64, 2, dict(verify_chunk=64)), (8, 2, 64, 5, dict(verify_chunk=256)), (8, 1, 128, 2, {}), (10, 2, 128, 2, {}),
+    (16, 2, 128, 2, dict(verify_chunk=2048)), (7, 1, 64, 3, {}),
+])
+def test_up_to_32_rows_without_a_dump(Hq, Hkv, D, k, shape):
+    """15 to 28 rows a verify item; a first item of fewer keys than warps have, one of many pieces."""
+    c = Case(94, Hq, Hkv, D, k, [k + 1, 40, 700, 2100, 129], [1, 0, 1, 1, 1], **shape)
+    d = c.device(dump=False)
+    c.call(d)
+    c.check(d)
