@@ -783,8 +783,27 @@ PILLAR_API int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_po
 /*
  * pillar_attn_kv4 -- the unified draft/verify step over the 4-bit cache:
  * pillar_attn_kv8 with k4_pool, v4_pool and the scale bytes in the place of the
- * 8-bit pools and scales (scales 8-byte aligned); every other argument, and
- * what the call writes, flags and refuses, is as there.
+ * 8-bit pools and scales.  With k = 0 and every request in verify mode it is
+ * plain decoding.  Alignment: q, out and the pools 16 bytes, verify_logits and
+ * the scales 8, the other arrays 4.  Schedules, workspace, skipped blocks and
+ * positions and their flags are as there.
+ *
+ * The products are exact (cache values and scaled queries are f16 values; an
+ * element of a query row is off by up to 2^-39 of the row's largest), their
+ * sums fp32.  A probability is rounded to f16: one below 2^-20 of the largest
+ * among the keys that it is summed with keeps fewer than eleven bits and is off
+ * by up to 2^-31 of that.
+ *
+ * Verify items of many rows go through a pipeline whose waits are bounded by
+ * the shape's wait_timeout_us (0: one second); past it PILLAR_FLAG_TIMEOUT is
+ * recorded, the outputs are incomplete and the next call on the workspace is
+ * whole.
+ *
+ * A NaN or infinity in q makes its row NaN.  The append writes scale bytes of 1
+ * to 226; under others (0 is a scale of 0) a value may be infinite or NaN.  That
+ * of a K row makes the rows of its request and KV head that see the key NaN
+ * (verify_lse as well), that of a V row the sixteen dimensions of the rows that
+ * do not see it, too.  All that holds however the context is split.
  *
  * pillar_attn_run_kv4 -- the same on the plan that pillar_attn_plan left in the
  * workspace (as pillar_attn_run): one plan for the layers of a model step.
