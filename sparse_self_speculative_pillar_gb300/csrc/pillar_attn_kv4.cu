@@ -31,13 +31,13 @@
 //     more than 2^8, which a vote of the group finds out.
 //   * Four warps write finished items, one stages queries.
 //
-// What bounds it: issue slots.  On 128 requests of 8192 tokens, 15 of them verifying 36 rows a KV head, logits dumped (its share of
-// the call's 146 us is 111 alone on the device, 141 MB read and 142 written), an SM's schedulers issue 0.63 of their cycles: a
-// tile takes some 4200 instructions and 520 more for eight rows (conversions and operand stores, softmax, the dump's stores).
-// The tensor cores are at 0.11, DRAM at 0.27.  Keys rather than rows on the M: a tile's products then cost what its rows do, and
-// K goes from a thread's registers to tensor memory without a transpose.  With mma.sync at 36 rows (five row tiles a warp) the
-// call takes 216 us, with blocks of codes copied by TMA into the same roles 160; items
-// of 1024 keys took 164 where those of 2048 took 158.
+// What bounds it: issue slots.  On 128 requests of 6144 to 10240 tokens, 15 of them verifying 36 rows a KV head, logits dumped (146 us
+// a call, 2.3 TB/s; the bf16 step 170, the 8-bit one 200), an SM's schedulers issue 0.63 of their cycles: a tile takes some 4200
+// instructions and 520 more for eight rows (conversions and operand stores, softmax, the dump's stores).  The tensor cores are
+// at 0.11, DRAM at 0.27.  Keys rather than rows on the M: a tile's products then cost what its rows do, and K goes from a
+// thread's registers to tensor memory without a transpose.  With mma.sync at 36 rows (five row tiles a warp) the call took 216 us
+// where this took 158; with blocks of codes copied by TMA into the same roles 160 where this takes 146; items of 1024 keys took 164
+// where those of 2048 took 158.
 #include "pillar_attn_kv4.cuh"
 
 namespace pillar {

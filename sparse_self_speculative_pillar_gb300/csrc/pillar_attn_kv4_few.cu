@@ -16,10 +16,10 @@
 //   * Each warp has reference maxima of its own; one moves when a score passes it
 //     by more than 2^8, which a vote of the warp finds out.
 //
-// What bounds it.  64 contexts of 1000 to 30000 keys, four rows (32 heads on 8, D = 128): 125 us of the call's 138, 549 MB, 4.4 TB/s;
-// some 370 instructions for 16 keys, issued in 0.65 of the schedulers' cycles by sixteen warps an SM (per issue 1.3 of 3.8 warps
-// wait for fixed latencies, 0.16 for memory).  Lists (128 requests, 307 to 512 keys each): 38 us of 52 for 63 MB, the chain of
-// queue, list, table and rows at an item's start and accesses of 64 bytes; issue 0.37.  One row tile on tcgen05 with the roles of
+// What bounds it.  64 contexts of 1000 to 30000 keys, four rows (32 heads on 8, D = 128): 138 us a call, 549 MB, 4.0 TB/s; some
+// 370 instructions for 16 keys, issued in 0.65 of the schedulers' cycles by sixteen warps an SM (per issue 1.3 warps wait for
+// fixed latencies, 0.16 for memory).  Lists (128 requests, 300 to 520 keys each): 52 us a call for 63 MB, the chain of queue, list,
+// table and rows at an item's start and accesses of 64 bytes; issue 0.37.  One row tile on tcgen05 with the roles of
 // pillar_attn_kv4.cu: 215 us where this took 184.  Two CTAs of eight warps instead of four of four: 157 where this took 143.
 #include "pillar_attn_kv4.cuh"
 

@@ -7,9 +7,8 @@
 // the values are.
 //
 // One thread has the sixteen values of a scale, two at a time.  What bounds it: memory, 2 bytes read and 0.56 written per
-// value.  26 K rows of K and V (8 heads, D = 128; 108 MB read, 30 written) take 28 us, 4.9 TB/s, with the launch and the first
-// rows' chain of loads in it; of 14 warps per issue 5.6 wait for loads and 2.4 at a turn's end, the ALU is at 0.49.  Stored and
-// read back they take 53.5 us; with turns dealt out one by one instead of a range to a CTA, and launches that wait for the
+// value.  Of 14 warps per issue 5.7 wait for loads and 2.8 at a turn's end, the ALU is at 0.49.  26 K rows of K and V (8 heads,
+// D = 128) stored and read back take 53.5 us, 4.6 TB/s; with turns dealt out one by one instead of a range to a CTA, and launches that wait for the
 // kernel before, 59.5; with 8-byte pieces of four values a thread 80.  (Three CTAs of four pieces a thread: 52 to 54 us; two of
 // eight: 63; five of two, with 40 registers: 59.)
 #include "pillar_kv4.cuh"
