@@ -213,6 +213,7 @@ int pillar_attn_run(const pillar_shape_t *shape, const uint16_t *q, const uint16
     aa.ws = static_cast<char *>(workspace);
     aa.lay = attn_layout(s);
     aa.num_slots = s.num_slots;
+    aa.B = s.B;
     aa.Hq = s.Hq;
     aa.Hkv = s.Hkv;
     aa.D = s.D;
@@ -547,6 +548,7 @@ static int run_kv8(const pillar_shape_t &s, const uint16_t *q, Kv8Cache c, const
     aa.ws = static_cast<char *>(workspace);
     aa.lay = attn_layout(s);
     aa.num_slots = s.num_slots;
+    aa.B = s.B;
     aa.Hq = s.Hq;
     aa.Hkv = s.Hkv;
     aa.D = s.D;
@@ -709,6 +711,7 @@ static int run_kv4(const pillar_shape_t &s, const uint16_t *q, Kv4Cache c, const
     aa.ws = static_cast<char *>(workspace);
     aa.lay = attn_layout(s);
     aa.num_slots = s.num_slots;
+    aa.B = s.B;
     aa.Hq = s.Hq;
     aa.Hkv = s.Hkv;
     aa.D = s.D;

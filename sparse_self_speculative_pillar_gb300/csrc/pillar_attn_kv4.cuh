@@ -24,7 +24,7 @@ struct Kv4Params {
     const UnitInfo *unit;
     const Item *items;
     float *part_o, *part_lse;
-    int Hq, Hkv, G, k, M, max_sparse;
+    int B, Hq, Hkv, G, k, M, max_sparse;
     float scale;
     unsigned long long wait_ns;
 };

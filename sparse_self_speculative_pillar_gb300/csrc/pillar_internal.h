@@ -162,7 +162,7 @@ struct AttnArgs {
     char *ws;
     AttnLayout lay;
     long long num_slots;
-    int Hq, Hkv, D, k, max_sparse;
+    int B, Hq, Hkv, D, k, max_sparse;
     int schedule;  // PILLAR_SCHEDULE_*
     float scale;
     unsigned long long wait_ns;  // bound of every pipeline wait
