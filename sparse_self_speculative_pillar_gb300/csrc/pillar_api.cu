@@ -720,7 +720,9 @@ static int run_kv4(const pillar_shape_t &s, const uint16_t *q, Kv4Cache c, const
     aa.schedule = s.schedule;
     aa.scale = s.sm_scale > 0.f ? s.sm_scale : 1.0f / std::sqrt((float)s.D);
     aa.wait_ns = s.wait_timeout_us > 0 ? (unsigned long long)s.wait_timeout_us * 1000ull : kWaitTimeoutNs;
-    return launch_attn_kv4(aa, c, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
+    const int most = s.verify_chunk > 0 ? s.verify_chunk : kDefaultVerifyChunk;  // keys of a context that is not split
+    const bool whole = s.max_sparse <= draft_chunk_of(s) && (s.max_len <= most || s.schedule == PILLAR_SCHEDULE_DRAFT_ONLY);
+    return launch_attn_kv4(aa, c, whole, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
 }
 
 // Item size of long contexts, 0 for the planner's own: where pieces of that size would leave CTAs of the kernel for at most

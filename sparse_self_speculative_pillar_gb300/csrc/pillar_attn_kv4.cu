@@ -31,12 +31,12 @@
 //     more than 2^8, which a vote of the group finds out.
 //   * Four warps write finished items, one stages queries.
 //
-// What bounds it: issue slots.  On 128 requests of 6144 to 10240 tokens, 15 of them verifying 36 rows a KV head, logits dumped (146 us
+// What bounds it: issue slots.  On 128 requests of 6144 to 10240 tokens, 15 of them verifying 36 rows a KV head, logits dumped (144 us
 // a call, 2.3 TB/s; the bf16 step 170, the 8-bit one 200), an SM's schedulers issue 0.63 of their cycles: a tile takes some 4200
 // instructions and 520 more for eight rows (conversions and operand stores, softmax, the dump's stores).  The tensor cores are
 // at 0.11, DRAM at 0.27.  Keys rather than rows on the M: a tile's products then cost what its rows do, and K goes from a
 // thread's registers to tensor memory without a transpose.  With mma.sync at 36 rows (five row tiles a warp) the call took 216 us
-// where this took 158; with blocks of codes copied by TMA into the same roles 160 where this takes 146; items of 1024 keys took 164
+// where this took 158; with blocks of codes copied by TMA into the same roles 160 where this took 146; items of 1024 keys took 164
 // where those of 2048 took 158.
 #include "pillar_attn_kv4.cuh"
 
@@ -921,7 +921,7 @@ cudaError_t launch_t(const Kv4Params &p, int nsm, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaStream_t st) {
+cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, bool whole, int nsm, cudaStream_t st) {
     Kv4Params p;
     p.q = a.q;
     p.c = c;
@@ -952,10 +952,14 @@ cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaS
         e = launch_attn_kv4_few(p, a.D, 8, 0, false, nsm, st);
     } else {
         e = p.M <= (p.logits ? kFewRowsDumped : kFewRows) ? launch_attn_kv4_few(p, a.D, p.M, 1, false, nsm, st)
-                            : a.D == 128 ? launch_t<128>(p, nsm, st) : launch_t<64>(p, nsm, st);
+            : a.D == 128                                  ? launch_t<128>(p, nsm, st)
+                                                          : launch_t<64>(p, nsm, st);
         if (e == cudaSuccess && a.schedule != PILLAR_SCHEDULE_VERIFY_ONLY) e = launch_attn_kv4_few(p, a.D, 8, 2, true, nsm, st);
     }
-    return e == cudaSuccess ? launch_merge(a, nsm, st) : e;
+    // Nothing to merge where no item is split (two draft and two verify requests, as a graph: 22.6 us -> 20.7); the kernels of few rows have set the queues
+    // up for the next run, which those of the many verify rows alone leave to the merge.
+    const bool queues = p.M <= kFewRowsDumped || a.schedule != PILLAR_SCHEDULE_VERIFY_ONLY;
+    return e == cudaSuccess && !(whole && queues) ? launch_merge(a, nsm, st) : e;
 }
 
 }  // namespace pillar

@@ -624,9 +624,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<NT>) attn_kv4_few_kernel(const
         __syncthreads();  // (the next item's queries and rows are there)
     }
     copies_wait<0>();
+    // (each CTA has drawn one number past the items: who has the last of these sets the queue up for the next run on the plan)
+    if (tid == 0 && sm.item == num_items + (int)gridDim.x - 1) *fp.counter = 0;
     if (bad) atomicOr(&p.hdr->err, bad);
     // (what follows on the stream waits for this kernel: let that mean the verify items' kernel, too)
-    if (fp.after) pdl_wait_prerequisites();
+    if (fp.after) {
+        pdl_wait_prerequisites();
+        if (blockIdx.x == 0 && tid == 0) p.hdr->item_counter = 0;
+    }
 }
 
 template <int D, int NT>

@@ -185,7 +185,8 @@ struct Kv4Cache {
     const int *table;
     int max_blocks, num_blocks;
 };
-cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, int nsm, cudaStream_t st);
+// whole: the plan splits no unit.
+cudaError_t launch_attn_kv4(const AttnArgs &a, const Kv4Cache &c, bool whole, int nsm, cudaStream_t st);
 
 struct TopkArgs {
     const float *logits, *lse;

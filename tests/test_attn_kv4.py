@@ -520,3 +520,32 @@ def test_up_to_32_rows_without_a_dump(Hq, Hkv, D, k, shape):
     d = c.device(dump=False)
     c.call(d)
     c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("schedule", [P.SCHEDULE_UNIFIED, P.SCHEDULE_DRAFT_ONLY, P.SCHEDULE_VERIFY_ONLY])
+@pytest.mark.parametrize("Hq,Hkv,k", [(8, 2, 0), (8, 2, 2), (32, 4, 4)])
+def test_runs_on_one_plan_that_splits_nothing(Hq, Hkv, k, schedule):
+    """Contexts of one item each, more items than CTAs: a run on the plan of an earlier one finds the whole queue again."""
+    g = np.random.default_rng(95)
+    B = 400
+    c = Case(95, Hq, Hkv, 64, k, g.integers(k + 1, 100, B), g.integers(0, 2, B), schedule=schedule)
+    full = Case(95, Hq, Hkv, 64, k, c.lens, c.modes)
+    d, f = full.device(), c.device()
+    full.call(d)
+    assert P.pillar_get_error(d["ws"]) == 0
+    off = np.concatenate([[0], np.cumsum(np.where(c.modes == 1, k + 1, 1))])
+    rows = torch.zeros(c.T, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        rows[off[b]:off[b + 1]] = bool(schedule == P.SCHEDULE_UNIFIED or (c.modes[b] == 1) == (schedule == P.SCHEDULE_VERIFY_ONLY))
+    P.pillar_attn_plan(c.shape, f["mode"], f["len"], f["cnt"], f["ws"])
+    for _ in range(3):
+        f["out"].fill_(0x7fc0)
+        f["logits"].fill_(SENTINEL)
+        f["lse"].fill_(SENTINEL)
+        P.pillar_attn_run_kv4(c.shape, f["q"], f["k4"], f["v4"], f["ks"], f["vs"], f["table"], f["idx"], f["out"], f["logits"],
+                              f["lse"], f["ws"])
+        assert torch.equal(f["out"][rows], d["out"][rows]) and torch.all(f["out"][~rows] == 0x7fc0)
+        for name in ("logits", "lse"):
+            assert torch.all(f[name] == SENTINEL) if schedule == P.SCHEDULE_DRAFT_ONLY else torch.equal(f[name], d[name]), name
+    assert P.pillar_get_error(f["ws"]) == 0
