@@ -725,18 +725,6 @@ static int run_kv4(const pillar_shape_t &s, const uint16_t *q, Kv4Cache c, const
     return launch_attn_kv4(aa, c, whole, nsm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PILLAR_OK : PILLAR_ERR_CUDA;
 }
 
-// Item size of long contexts, 0 for the planner's own: where pieces of that size would leave CTAs of the kernel for at most
-// sixteen rows without an item, the pieces that give each one, down to the planner's smaller size, which the workspace is made
-// for (one context of 100001 tokens, 32 heads on 8: 58 us -> 52).
-static int kv4_chunk(const pillar_shape_t &s) {
-    const int nsm = sm_count();
-    if ((s.k + 1) * (s.Hq / s.Hkv) > 16 || s.max_len < kLongContext || nsm <= 0) return 0;
-    const long long pieces = 4ll * nsm / ((long long)s.B * s.Hkv);  // of a context
-    if (pieces < 1) return 0;
-    const long long c = ((s.max_len + pieces - 1) / pieces + kTileKeys - 1) / kTileKeys * kTileKeys;
-    return c >= kLongVerifyChunk ? 0 : (int)std::max<long long>(c, kDefaultVerifyChunk);
-}
-
 int pillar_attn_run_kv4(const pillar_shape_t *shape, const uint16_t *q, const uint8_t *k4_pool, const uint8_t *v4_pool,
                         const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table, int32_t max_blocks,
                         const int32_t *sparse_idx, uint16_t *out, float *verify_logits, float *verify_lse,
@@ -757,7 +745,7 @@ int pillar_attn_kv4(const pillar_shape_t *shape, const uint16_t *q, const uint8_
     const int st = attn_kv4_checks(shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, ws_bytes);
     if (st != PILLAR_OK) return st;
     pillar_shape_t cut = *shape;
-    if (cut.verify_chunk == 0) cut.verify_chunk = kv4_chunk(cut);
+    if (cut.verify_chunk == 0) cut.verify_chunk = kv4_chunk(cut, sm_count());
     const int sp = pillar_attn_plan(&cut, req_mode, req_len, sparse_cnt, workspace, ws_bytes, stream);
     if (sp != PILLAR_OK || shape->B == 0) return sp;
     return run_kv4(*shape, q, c, sparse_idx, out, verify_logits, verify_lse, workspace, stream);

@@ -2,6 +2,7 @@
 // planner, the unified attention kernel, the Top-K kernels and the host API.
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -96,6 +97,17 @@ void *driver_entry(const char *name, int version);
 // 0: the default, chosen per request by its context length (see kLongContext)
 inline int verify_chunk_of(const pillar_shape_t &s) { return s.verify_chunk > 0 ? s.verify_chunk : 0; }
 inline int draft_chunk_of(const pillar_shape_t &s) { return s.draft_chunk > 0 ? s.draft_chunk : kDefaultDraftChunk; }
+
+// pillar_attn_kv4's item size for long contexts on a GPU of nsm SMs, 0 for the planner's own: where pieces of that size would leave
+// CTAs of the kernel for at most sixteen rows without an item, the pieces that give each one, down to the planner's smaller size,
+// which the workspace is made for (one context of 100001 tokens, 32 heads on 8: 58 us -> 52).
+inline int kv4_chunk(const pillar_shape_t &s, int nsm) {
+    if (s.B <= 0 || (s.k + 1) * (s.Hq / s.Hkv) > 16 || s.max_len < kLongContext || nsm <= 0) return 0;
+    const long long pieces = 4ll * nsm / ((long long)s.B * s.Hkv);  // of a context
+    if (pieces < 1) return 0;
+    const long long c = ((s.max_len + pieces - 1) / pieces + kTileKeys - 1) / kTileKeys * kTileKeys;
+    return c >= kLongVerifyChunk ? 0 : (int)std::max<long long>(c, kDefaultVerifyChunk);
+}
 
 // Partials: an item of a (request, KV head) split over several items writes
 // its rows (M = (k+1)*G for verify, G for draft); each partial row is D fp32
