@@ -799,7 +799,8 @@ PILLAR_API int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_po
  * recorded, the outputs are incomplete and the next call on the workspace is
  * whole.
  *
- * A NaN or infinity in q makes its row NaN.  The append writes scale bytes of 1
+ * A NaN or infinity in q makes its row of out and verify_lse NaN, unless the row
+ * sees no position at all.  The append writes scale bytes of 1
  * to 226; under others (0 is a scale of 0) a value may be infinite or NaN.  That
  * of a K row makes the rows of its request and KV head that see the key NaN
  * (verify_lse as well), that of a V row the sixteen dimensions of the rows that

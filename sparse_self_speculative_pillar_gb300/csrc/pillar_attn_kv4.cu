@@ -741,8 +741,9 @@ __device__ void queries4(const Kv4Params &p, Smem4<D> &sm, int lane) {
                 query_scale(mine, &up, &down);
                 const float fac = fmaxf(down * p.scale, __int_as_float(1));  // (above 0: a masked score stays -inf)
                 sm.fac[is][my] = fac;
-                sm.fac2[is][my] = fmaxf(fac * kLog2e, __int_as_float(1));
-                sm.lim[is][my] = my < p.M ? rec.L - (p.k + 1) + j : 0x7fffffff;
+                const int lim = my < p.M ? rec.L - (p.k + 1) + j : 0x7fffffff;
+                sm.fac2[is][my] = softmax_factor(fac, mine, lim);
+                sm.lim[is][my] = lim;
             }
         }
         fence_proxy_async_smem();

@@ -46,6 +46,13 @@ __device__ __forceinline__ void query_scale(uint32_t mx, float *up, float *down)
     *down = __uint_as_float((e - 14u) << 23);
 }
 
+// A row's factor in base 2 (scores = sum * factor), above 0 so that a masked score stays -inf.  mx as above, lim the last position
+// that the row sees.  NaN for a row with a NaN or an infinity that sees any: its scores are infinite or NaN, and where all of them
+// are -inf their weights alone would not tell them from masked ones.
+__device__ __forceinline__ float softmax_factor(float fac, uint32_t mx, int lim) {
+    return mx >= 0x7f80u && lim >= 0 ? __int_as_float(0x7fffffff) : fmaxf(fac * kLog2e, __int_as_float(1));
+}
+
 // The items of part 0 (all), 1 (of verify requests) or 2 (the others), of `rows` <= kFewRows rows at most.  after: another
 // kernel on this stream has the verify items, and is the one waited for at the end.
 cudaError_t launch_attn_kv4_few(const Kv4Params &p, int D, int rows, int part, bool after, int nsm, cudaStream_t st);

@@ -515,8 +515,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<NT>) attn_kv4_few_kernel(const
             const int rows = w.verify ? p.M : p.G, r = qtile * 8 + g, j = w.verify ? r / p.G : 0, gi = r - j * p.G;
             const float fac = fmaxf(down * p.scale, __int_as_float(1));  // (above 0: a masked score stays -inf)
             sm.fac[r] = fac;
-            sm.fac2[r] = fmaxf(fac * kLog2e, __int_as_float(1));
-            sm.lim[r] = w.verify && r < rows ? w.L - (p.k + 1) + j : 0x7fffffff;
+            const int lim = w.verify && r < rows ? w.L - (p.k + 1) + j : 0x7fffffff;
+            sm.fac2[r] = softmax_factor(fac, mx, lim);
+            sm.lim[r] = lim;
             sm.lb[r] = w.verify && p.logits && r < rows
                            ? p.logits + w.logit_off + ((long long)(w.g * p.G + gi) * (p.k + 1) + j) * w.L : nullptr;
         }
