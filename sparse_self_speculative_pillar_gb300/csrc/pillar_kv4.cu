@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads, kResident) kv4_append_kernel(Kv4A
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, int nsm, cudaStream_t st) {
-    const int rows = rows_of_turn(a.n, nsm);
+    const int rows = rows_of_turn(a.n, kResident, nsm);
     const unsigned grid = row_ctas(a.n, rows, kResident, nsm);
     const bool wide = rows_wide(a.k_new, a.v_new, a.k_stride, a.v_stride);
     const auto f = a.D == 128 ? (wide ? kv4_append_kernel<128, true> : kv4_append_kernel<128, false>)

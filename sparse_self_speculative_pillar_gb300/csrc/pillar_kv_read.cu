@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kRowThreads, kResident) kv_read_kernel(KvReadA
 }  // namespace
 
 cudaError_t launch_kv_read(const KvReadArgs &a, int nsm, cudaStream_t st) {
-    const int rows = rows_of_turn(a.n, nsm);
+    const int rows = rows_of_turn(a.n, kResident, nsm);
     const unsigned grid = row_ctas(a.n, rows, kResident, nsm);
     const bool wide = rows_wide(a.k_out, a.v_out, a.k_stride, a.v_stride);
     const auto f = a.bits == 4 ? (a.D == 128 ? (wide ? kv_read_kernel<128, 4, true> : kv_read_kernel<128, 4, false>)

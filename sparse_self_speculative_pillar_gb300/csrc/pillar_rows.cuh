@@ -132,11 +132,13 @@ __device__ __forceinline__ void for_rows(const RowMap &m, int most, Work work) {
         t0 += rows;
     }
 }
-// Most rows of a CTA's turn, and CTAs: one row while that gives every SM at most sixteen CTAs (a decode step: all in flight), else
-// sixteen (26 K rows stored and read back: 53.5 us; eight 54.6, thirty-two 53.8), and no more CTAs than are resident.
-inline int rows_of_turn(int n, int nsm) { return n <= 16 * nsm ? 1 : 16; }
+// Most rows of a CTA's turn, and CTAs: one row while that many CTAs are resident at once (a decode step), else sixteen (26 K rows
+// stored and read back: 53.5 us; eight 54.6, thirty-two 53.8), and no more CTAs than are resident.  (Ten in a graph, 8 heads of
+// D = 128.  Appends of 608 rows, one to a CTA: 39 us; of 760 60 in turns of sixteen rows, 63 one by one; of 2432 62 and 122.  Reads of
+// 760 rows, one to a CTA: 41, in turns of sixteen 55; of 912 56 and 60; of 2432 60 and 109.)
+inline int rows_of_turn(int n, int resident, int nsm) { return n <= resident * nsm ? 1 : 16; }
 inline unsigned row_ctas(int n, int rows, int resident, int nsm) {
-    const long long groups = ((long long)n + rows - 1) / rows, most = rows == 1 ? groups : (long long)resident * nsm;
+    const long long groups = ((long long)n + rows - 1) / rows, most = (long long)resident * nsm;
     return (unsigned)(groups < most ? groups : most);
 }
 // (Launched while the kernel before on the stream still runs: its launch is over when that kernel is.)
