@@ -771,8 +771,9 @@ PILLAR_API int pillar_kv4_append(const pillar_shape_t *shape, const uint16_t *k_
                                  int32_t *device_flags, void *stream);
 
 /*
- * pillar_kv4_read -- positions of the 4-bit cache as bf16 rows (exact); the
- * arguments are pillar_kv8_read's, the scales 8-byte aligned.
+ * pillar_kv4_read -- positions of the 4-bit cache as bf16 rows: exact under the
+ * scales that pillar_kv4_append writes; under larger ones a value past f16's range
+ * is infinite.  The arguments are pillar_kv8_read's, the scales 8-byte aligned.
  */
 PILLAR_API int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_pool, const uint8_t *v4_pool,
                                const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table,
@@ -800,11 +801,13 @@ PILLAR_API int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_po
  * whole.
  *
  * A NaN or infinity in q makes its row of out and verify_lse NaN, unless the row
- * sees no position at all.  The append writes scale bytes of 1
- * to 226; under others (0 is a scale of 0) a value may be infinite or NaN.  That
- * of a K row makes the rows of its request and KV head that see the key NaN
- * (verify_lse as well), that of a V row the sixteen dimensions of the rows that
- * do not see it, too.  All that holds however the context is split.
+ * sees no position at all.  The append writes scale bytes of 1 to 226; under
+ * others (0 is a scale of 0) a value past f16's range is infinite, and one may be
+ * NaN.  A score that such a K row makes NaN or +inf makes the row of out and
+ * verify_lse NaN; a key whose score is -inf counts as one that is not there.  A
+ * value of a V row that is NaN or infinite makes its dimension so in the rows that
+ * see the key (an infinity may make it NaN), and may make it NaN in other rows of
+ * the request and KV head.  All that holds however the context is split.
  *
  * pillar_attn_run_kv4 -- the same on the plan that pillar_attn_plan left in the
  * workspace (as pillar_attn_run): one plan for the layers of a model step.

@@ -72,3 +72,53 @@ def test_a_row_that_sees_no_position_is_zero_whatever_its_query(Hq, k, bits):
     assert torch.all(out[:k - 1] == 0) and torch.all(torch.isneginf(z[0, :, :k - 1]))
     assert torch.all(torch.isnan(out[k - 1:k + 1])) and torch.all(torch.isnan(z[0, :, k - 1:]))
     assert torch.all(torch.isfinite(out[k + 1:])) and torch.all(torch.isfinite(z[1]))
+
+
+def with_a_bad_key(Hq, Hkv, D, k, chunk, what):
+    """Position 40 of the second request and of the lists' has an infinite scale in its second group of the last KV head."""
+    c = batch(Hq, Hkv, D, k, chunk, seed=102)
+    c.idx[2, Hkv - 1, 0] = 40
+    for b in (1, 2):
+        at = (int(c.table[b, 2]), Hkv - 1, 8)
+        codes, scales = (c.k4, c.ks) if what == "k" else (c.v4, c.vs)
+        codes[at][16:32] = c.g.integers(1, 8, 16)
+        scales[at][1] = 0xf8
+    return c
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunk", [64, 2048])
+@pytest.mark.parametrize("Hq,Hkv,D,k,dump", KINDS)
+def test_a_key_whose_score_is_minus_infinity_counts_as_one_that_is_not_there(Hq, Hkv, D, k, dump, chunk):
+    """(The definition's weight of 0, within its usual tolerances.)"""
+    c = with_a_bad_key(Hq, Hkv, D, k, chunk, "k")
+    c.q[..., 16:32] |= 0x8000
+    d = c.device(dump)
+    c.call(d)
+    c.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunk", [64, 2048])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("Hq,Hkv,D,k,dump", KINDS)
+def test_an_infinite_value_reaches_the_rows_that_see_it(Hq, Hkv, D, k, dump, what, chunk):
+    """A score of +inf: NaN.  An infinite value of V: its dimensions are not finite; they may be NaN in rows that do not see it, but
+    all of these see it.  Everything else is bit for bit what it is with a scale of 1 there."""
+    c = with_a_bad_key(Hq, Hkv, D, k, chunk, what)
+    c.q[..., 16:32] &= 0x7fff
+    e = c.device(dump)
+    (c.ks if what == "k" else c.vs)[(c.ks if what == "k" else c.vs) == 0xf8] = 0x78
+    d = c.device(dump)
+    for x in (d, e):
+        c.call(x)
+        assert P.pillar_get_error(x["ws"]) == 0
+    heads = slice(Hq - Hq // Hkv, Hq)
+    rows, lse = np.zeros((c.T, Hq, D), bool), np.zeros((2, Hq, k + 1), bool)
+    rows[k + 1:, heads, slice(None) if what == "k" else slice(16, 32)] = True
+    lse[1, heads] = what == "k"
+    at, z = torch.from_numpy(rows), torch.from_numpy(lse)
+    got, want = values(e), values(d)
+    assert torch.all(torch.isnan(got[at]) if what == "k" else ~torch.isfinite(got[at])) and torch.equal(got[~at], want[~at])
+    got, want = e["lse"].cpu(), d["lse"].cpu()
+    assert torch.all(torch.isnan(got[z])) and torch.equal(got[~z], want[~z])
