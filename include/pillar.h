@@ -84,7 +84,8 @@ typedef struct pillar_shape {
     int32_t row_hi;        /*   the k draft rows are [1, k+1) */
     int32_t max_topk;      /* row stride of next_idx (>= 1) */
     int32_t verify_chunk;  /* keys per verify work item (multiple of 64, <= 2048); 0: 1024 for
-                              contexts under 8192 positions, 2048 from 8192 on */
+                              contexts under 8192 positions, 2048 from 8192 on
+                              (pillar_attn_kv4 may choose another: see there) */
     int32_t draft_chunk;   /* listed keys per draft work item (multiple of 64, <= 2048; 0 = 2048) */
     int64_t num_slots;     /* rows of k_pool / v_pool */
     float sm_scale;        /* logit scale; 0 means 1/sqrt(D) */
@@ -798,16 +799,25 @@ PILLAR_API int pillar_kv4_read(const pillar_shape_t *shape, const uint8_t *k4_po
  * Verify items of many rows go through a pipeline whose waits are bounded by
  * the shape's wait_timeout_us (0: one second); past it PILLAR_FLAG_TIMEOUT is
  * recorded, the outputs are incomplete and the next call on the workspace is
- * whole.
+ * whole.  (A wait is also given up after four million polls, were the bound longer
+ * than these; an item takes microseconds.)
+ *
+ * Where verify_chunk is 0, max_len at least 8192 and (k+1)*G at most 16, the call
+ * plans with a verify_chunk of its own: the share of max_len that gives each of
+ * 4 CTAs an SM a piece, rounded up to 64 and at least 1024, if that is less than
+ * 2048.  pillar_attn_plan does not: what pillar_attn_run_kv4 computes on its plan
+ * may differ in the last bits, and a shape with that verify_chunk gives both the
+ * same items.
  *
  * A NaN or infinity in q makes its row of out and verify_lse NaN, unless the row
- * sees no position at all.  The append writes scale bytes of 1 to 226; under
- * others (0 is a scale of 0) a value past f16's range is infinite, and one may be
- * NaN.  A score that such a K row makes NaN or +inf makes the row of out and
- * verify_lse NaN; a key whose score is -inf counts as one that is not there.  A
- * value of a V row that is NaN or infinite makes its dimension so in the rows that
- * see the key (an infinity may make it NaN), and may make it NaN in other rows of
- * the request and KV head.  All that holds however the context is split.
+ * has no position to see (one that is skipped counts).  The append writes scale
+ * bytes of 1 to 226; under others (0 is a scale of 0) a value past f16's range is
+ * infinite, and one may be NaN.  A score that such a K row makes NaN or +inf makes
+ * the row of out and verify_lse NaN; a key whose score is -inf counts as one that
+ * is not there.  A value of a V row that is NaN or infinite makes its dimension so
+ * in the rows that see the key (an infinity may make it NaN), and may make it NaN
+ * in other rows of the request and KV head.  All that holds however the context is
+ * split.
  *
  * pillar_attn_run_kv4 -- the same on the plan that pillar_attn_plan left in the
  * workspace (as pillar_attn_run): one plan for the layers of a model step.

@@ -31,7 +31,7 @@
 //     more than 2^8, which a vote of the group finds out.
 //   * Four warps write finished items, one stages queries.
 //
-// What bounds it: issue slots.  On 128 requests of 6144 to 10240 tokens, 15 of them verifying 36 rows a KV head, logits dumped (144 us
+// What bounds it: issue slots.  On 128 requests of 6144 to 10240 tokens, 15 of them verifying 36 rows a KV head, logits dumped (145 us
 // a call, 2.3 TB/s; the bf16 step 170, the 8-bit one 200), an SM's schedulers issue 0.63 of their cycles: a tile takes some 4200
 // instructions and 520 more for eight rows (conversions and operand stores, softmax, the dump's stores).  The tensor cores are
 // at 0.11, DRAM at 0.27.  Keys rather than rows on the M: a tile's products then cost what its rows do, and K goes from a
@@ -97,7 +97,7 @@ static_assert(sizeof(Smem4<64>) > 114 * 1024, "never two CTAs on an SM: each tak
 // A wait by a whole warp, a few instructions long (every wait that is inlined costs the roles' shared instruction cache; with
 // the clock in each, plain decoding took 227 us here, and 215 without).  The products' warps watch the clock for all: nothing
 // moves in a CTA for long without them, and one that has had nothing to do for the bound raises the abort flag.  A count of polls
-// bounds the waits that outlive it.
+// bounds the waits that outlive it, whatever the caller's bound is (an item takes microseconds).
 constexpr int kMostPolls = 1 << 22;
 template <int D>
 __device__ __forceinline__ bool wait4(uint64_t *bar, uint32_t parity, Smem4<D> &sm) {
@@ -184,8 +184,9 @@ static_assert(kMaxRows == 64 && kGroups == 4, "four chunks of eight rows a group
 // ------------------------------------------------------------------ resolver warp
 
 // A CTA's share of the drafts' lists and of the block tables into L2, as it runs out of verify items: the drafts' kernel begins with
-// chains of loads from them (128 requests, 15 verify: 145.7 us -> 144.7).  Arrays so large that a call may well read only
-// a fraction of them are left out.
+// chains of loads from them (128 requests, 15 verify: 147.5 us -> 146.4; five query heads a KV head, contexts of 4096 to 24576: 190.9 ->
+// 190.2; medians of five runs of either, which lie within 0.2).  Arrays so large that a call may well read only a fraction of them are
+// left out.
 constexpr long long kPrefetchBytes = 8 << 20;
 __device__ __forceinline__ void prefetch_lists(const Kv4Params &p, int lane) {
     const long long list = (long long)p.B * p.Hkv * p.max_sparse * 4, table = (long long)p.B * p.c.max_blocks * 4;

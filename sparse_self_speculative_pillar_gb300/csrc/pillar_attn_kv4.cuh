@@ -7,9 +7,10 @@
 namespace pillar {
 
 // Verify items of at most so many rows, without a dump of logits and with one, go to warps of mma.sync; the others to tcgen05,
-// whose work for a key is the same whatever the rows.  (128 requests of 8192 tokens, 32 heads on 8, verify steps of 4, 5 and 6
-// tokens, that is 16, 20 and 24 rows: 134 us against 179 without a dump for 16 rows, 140 against 152 for 24; with one 157 against 185
-// for 16, but 187 against 179 for 20 and 171 against 165 for 24.)
+// whose work for a key is the same whatever the rows.  (128 requests of 8192 tokens, 32 heads on 8, one in k + 1 of them
+// verifying, the others on lists of 410; mma.sync first, repeats within 1 us, floors of 52, 44 and 39 us, with a dump 72, 64 and 59.
+// 16 rows: 122 us and 155, with a dump 143 and 166; 20: 137 and 148, with one 171 and 159; 24: 125 and 138, with one 150 and 149.  32
+// requests that all verify: 113 and 129, with one 137 both; 143 and 144, with one 191 and 156; 145 both, with one 192 and 158.)
 constexpr int kFewRows = 24, kFewRowsDumped = 16;
 
 struct Kv4Params {

@@ -122,3 +122,20 @@ def test_an_infinite_value_reaches_the_rows_that_see_it(Hq, Hkv, D, k, dump, wha
     assert torch.all(torch.isnan(got[at]) if what == "k" else ~torch.isfinite(got[at])) and torch.equal(got[~at], want[~at])
     got, want = e["lse"].cpu(), d["lse"].cpu()
     assert torch.all(torch.isnan(got[z])) and torch.equal(got[~z], want[~z])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [0x7f80, 0x7fc0])
+@pytest.mark.parametrize("Hq,k", [(2, 3), (4, 3), (8, 6)])
+def test_a_position_that_is_skipped_is_one_to_see(Hq, k, bits):
+    c = Case(103, Hq, 1, 64, k, [20, 30, 30, 40], [1, 0, 0, 0])
+    c.table[0] = c.blocks
+    c.cnt[:, 0] = [0, 2, 0, 3]
+    c.idx[1, 0, :2] = [-1, 30]
+    d = c.device()
+    d["q"][:k + 3] = bits
+    c.call(d)
+    assert P.pillar_get_error(d["ws"]) == P.FLAG_SLOT | P.FLAG_INDEX
+    out = values(d)
+    assert torch.all(torch.isnan(out[:k + 2])) and torch.all(torch.isnan(d["lse"]))
+    assert torch.all(out[k + 2] == 0) and torch.all(torch.isfinite(out[k + 3]))  # an empty list; a sound one
